@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_PKG_DIR, "libaqlm_mi355x.so")
 AQLM_OK = 0
 STATUS_NAMES = {0: "AQLM_OK", 1: "AQLM_ERR_NULL", 2: "AQLM_ERR_SHAPE", 3: "AQLM_ERR_SCHEME",
                 4: "AQLM_ERR_ALIGN", 5: "AQLM_ERR_BATCH", 6: "AQLM_ERR_HIP",
-                7: "AQLM_ERR_WORKSPACE", 8: "AQLM_ERR_SCRATCH"}
+                7: "AQLM_ERR_WORKSPACE", 8: "AQLM_ERR_SCRATCH", 9: "AQLM_ERR_TYPE"}
 EXPORTED_SYMBOLS = ("aqlm_dequant", "aqlm_gemv", "aqlm_gemv_batched", "aqlm_gemv_workspace_size",
                     "aqlm_gemv_ws", "aqlm_gemm", "aqlm_gemm_workspace_size", "aqlm_gemm_ws",
                     "aqlm_gemm_noalloc", "aqlm_status_string", "aqlm_abi_version")

@@ -123,10 +123,12 @@ const char *aqlm_status_string(int status) {
     case AQLM_ERR_ALIGN: return "a pointer is not 16-byte aligned";
     case AQLM_ERR_BATCH: return "batch outside the entry point's range";
     case AQLM_ERR_HIP: return "the HIP runtime reported an error";
-    case AQLM_ERR_WORKSPACE: return "the workspace is smaller than aqlm_gemm_workspace_size";
+    case AQLM_ERR_WORKSPACE: return "the workspace is smaller than the entry point's "
+                                    "*_workspace_size";
     case AQLM_ERR_SCRATCH: return "the call needs more scratch memory than the library's static "
                                   "scratch array holds (AQLM_STATIC_SCRATCH_BYTES = 64 MiB); "
                                   "use aqlm_gemm_ws with a workspace or aqlm_gemm";
+    case AQLM_ERR_TYPE: return "unknown element type or scale rule";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,216 @@
+// Microscaled quantisation and expansion.
+//
+// Both move whole matrices once and compute next to nothing, so HBM bounds
+// them. A thread owns eight consecutive columns (an octet: one 16-byte access
+// of a half matrix, one word of codes), so four neighbouring lanes share a
+// block of 32 and every access of a wavefront is contiguous.
+#include <algorithm>
+
+#include "mx_device.hpp"
+
+namespace aqlm {
+namespace {
+
+constexpr int kCThreads = 256;
+constexpr int kCUnroll = 4;  // octets per thread, a block's threads apart
+
+// Eight consecutive elements, as loaded.
+template <MxType T> struct Octet {
+  uint32_t w[T == MxType::kF32 ? 8 : 4];
+};
+
+template <MxType T> __device__ __forceinline__ Octet<T> load_octet(const void *x, int64_t i) {
+  Octet<T> o;
+  const u32x4_t *p = static_cast<const u32x4_t *>(x) + i * (T == MxType::kF32 ? 2 : 1);
+#pragma unroll
+  for (int k = 0; k < (T == MxType::kF32 ? 2 : 1); ++k) {
+    const u32x4_t v = p[k];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o.w[4 * k + e] = v[e];
+  }
+  return o;
+}
+
+// Largest magnitude of a block as float32 bits, from the octets of its four
+// lanes. Magnitudes order like their bits read as integers, with NaN above
+// infinity above the numbers, so the maximum is taken on integers.
+template <MxType T> __device__ __forceinline__ uint32_t block_max(const Octet<T> &o) {
+  uint32_t m = 0;
+  if constexpr (T == MxType::kF32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, o.w[e] & 0x7FFFFFFFu);
+  } else {
+    u16x2_t p = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      p = __builtin_elementwise_max(p, __builtin_bit_cast(u16x2_t, o.w[e] & 0x7FFF7FFFu));
+    m = max((uint32_t)p.x, (uint32_t)p.y);
+  }
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadXor1, 0xF, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadXor2, 0xF, 0xF, false));
+  if constexpr (T == MxType::kF16) return __builtin_bit_cast(uint32_t, h2f(m));  // exact
+  if constexpr (T == MxType::kBF16) return m << 16;
+  return m;
+}
+
+// E8M0 byte of a block from its largest magnitude m * 2^e (float32 bits). With
+// 1 <= m < 2, m * 2^e / 2^(e-2) = 4 m: at most 6 up to m = 1.5 (mantissa bits
+// 0x400000), which is where the ceil rule takes the next power. Exponent
+// fields below 3 (subnormals among them) give scales under 2^-127, held as
+// 2^-127.
+template <bool CEIL> __device__ __forceinline__ uint32_t scale_byte(uint32_t bits) {
+  if (bits >= 0x7F800000u) return 255u;
+  if (bits == 0u) return 127u;
+  int b = (int)(bits >> 23) - 2;
+  if (CEIL) b += (bits & 0x7FFFFFu) > 0x400000u;
+  return (uint32_t)max(b, 0);
+}
+
+// Eight codes of an octet: v_cvt_scalef32_pk_fp4 divides by the scale, rounds
+// to nearest even and saturates at 6.
+template <MxType T> __device__ __forceinline__ uint32_t encode8(const Octet<T> &o, float s) {
+  uint32_t r = 0;
+  if constexpr (T == MxType::kF16) {
+#define AQLM_ENC(i) \
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(half2_t, o.w[i]), s, i);
+    AQLM_ENC(0) AQLM_ENC(1) AQLM_ENC(2) AQLM_ENC(3)
+#undef AQLM_ENC
+  } else if constexpr (T == MxType::kBF16) {
+#define AQLM_ENC(i) \
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bhalf2_t, o.w[i]), s, i);
+    AQLM_ENC(0) AQLM_ENC(1) AQLM_ENC(2) AQLM_ENC(3)
+#undef AQLM_ENC
+  } else {
+#define AQLM_ENC(i)                                                                              \
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __builtin_bit_cast(float, o.w[2 * i]),         \
+                                               __builtin_bit_cast(float, o.w[2 * i + 1]), s, i);
+    AQLM_ENC(0) AQLM_ENC(1) AQLM_ENC(2) AQLM_ENC(3)
+#undef AQLM_ENC
+  }
+  return r;
+}
+
+template <MxType T, bool CEIL>
+__global__ __launch_bounds__(kCThreads) void mx_quantize_kernel(const void *__restrict__ x,
+                                                                uint32_t *__restrict__ codes,
+                                                                uint8_t *__restrict__ scales,
+                                                                int64_t octets) {
+  // octets is a multiple of 4 and so is every thread group's start: the four
+  // lanes of a block are all inside or all outside
+  const int64_t step = (int64_t)gridDim.x * (kCThreads * kCUnroll);
+  for (int64_t base = (int64_t)blockIdx.x * (kCThreads * kCUnroll) + threadIdx.x; base < octets;
+       base += step) {
+    Octet<T> o[kCUnroll];
+#pragma unroll
+    for (int u = 0; u < kCUnroll; ++u) {
+      const int64_t i = base + u * kCThreads;
+      if (i < octets) o[u] = load_octet<T>(x, i);
+      else o[u] = {};
+    }
+#pragma unroll
+    for (int u = 0; u < kCUnroll; ++u) {
+      const int64_t i = base + u * kCThreads;
+      const uint32_t b = scale_byte<CEIL>(block_max<T>(o[u]));
+      const uint32_t c = b == 255u ? 0u : encode8<T>(o[u], mx_scale(b));
+      if (i < octets) {
+        codes[i] = c;
+        if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)b;
+      }
+    }
+  }
+}
+
+template <MxType T>
+__global__ __launch_bounds__(kCThreads) void mx_dequant_kernel(const uint32_t *__restrict__ codes,
+                                                               const uint8_t *__restrict__ scales,
+                                                               u32x4_t *__restrict__ W,
+                                                               int64_t octets) {
+  const int64_t step = (int64_t)gridDim.x * (kCThreads * kCUnroll);
+  for (int64_t base = (int64_t)blockIdx.x * (kCThreads * kCUnroll) + threadIdx.x; base < octets;
+       base += step) {
+    uint32_t c[kCUnroll], b[kCUnroll];
+#pragma unroll
+    for (int u = 0; u < kCUnroll; ++u) {
+      const int64_t i = base + u * kCThreads;
+      const bool in = i < octets;
+      c[u] = in ? codes[i] : 0u;
+      b[u] = in ? scales[i >> 2] : 127u;
+    }
+#pragma unroll
+    for (int u = 0; u < kCUnroll; ++u) {
+      const int64_t i = base + u * kCThreads;
+      if (i >= octets) break;
+      const float s = mx_scale(b[u]);
+      if constexpr (T == MxType::kF32) {
+        typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+        const u32x2_t v[4] = {
+            __builtin_bit_cast(u32x2_t, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], s, 0)),
+            __builtin_bit_cast(u32x2_t, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], s, 1)),
+            __builtin_bit_cast(u32x2_t, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], s, 2)),
+            __builtin_bit_cast(u32x2_t, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u], s, 3))};
+        W[2 * i] = u32x4_t{v[0].x, v[0].y, v[1].x, v[1].y};
+        W[2 * i + 1] = u32x4_t{v[2].x, v[2].y, v[3].x, v[3].y};
+      } else {
+        const uint4 r = mx_decode8<T>(c[u], s);
+        W[i] = u32x4_t{r.x, r.y, r.z, r.w};
+      }
+    }
+  }
+}
+
+// Workgroups of a pass over `octets`: one per kCUnroll * kCThreads octets, up to
+// 2^30 threads (each then takes several turns).
+unsigned convert_grid(int64_t octets) {
+  const int64_t per = kCThreads * kCUnroll;
+  return (unsigned)std::min<int64_t>((octets + per - 1) / per, int64_t(1) << 22);
+}
+
+template <MxType T>
+void quantize_as(const void *x, int64_t octets, bool ceil_rule, uint8_t *codes, uint8_t *scales,
+                 hipStream_t stream) {
+  uint32_t *cw = reinterpret_cast<uint32_t *>(codes);
+  if (ceil_rule)
+    hipLaunchKernelGGL((mx_quantize_kernel<T, true>), dim3(convert_grid(octets)), dim3(kCThreads), 0,
+                       stream, x, cw, scales, octets);
+  else
+    hipLaunchKernelGGL((mx_quantize_kernel<T, false>), dim3(convert_grid(octets)), dim3(kCThreads),
+                       0, stream, x, cw, scales, octets);
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const void *x, MxType type, int64_t rows, int64_t cols,
+                              bool ceil_rule, uint8_t *codes, uint8_t *scales,
+                              hipStream_t stream) {
+  const int64_t octets = rows * cols / 8;
+  switch (type) {
+    case MxType::kF16: quantize_as<MxType::kF16>(x, octets, ceil_rule, codes, scales, stream); break;
+    case MxType::kBF16: quantize_as<MxType::kBF16>(x, octets, ceil_rule, codes, scales, stream); break;
+    case MxType::kF32: quantize_as<MxType::kF32>(x, octets, ceil_rule, codes, scales, stream); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequant(const MxDesc &m, MxType type, void *W, hipStream_t stream) {
+  const int64_t octets = m.rows * m.cols / 8;
+  const dim3 grid(convert_grid(octets)), block(kCThreads);
+  const uint32_t *codes = reinterpret_cast<const uint32_t *>(m.codes);
+  u32x4_t *out = static_cast<u32x4_t *>(W);
+  switch (type) {
+    case MxType::kF16:
+      hipLaunchKernelGGL(mx_dequant_kernel<MxType::kF16>, grid, block, 0, stream, codes, m.scales,
+                         out, octets);
+      break;
+    case MxType::kBF16:
+      hipLaunchKernelGGL(mx_dequant_kernel<MxType::kBF16>, grid, block, 0, stream, codes, m.scales,
+                         out, octets);
+      break;
+    case MxType::kF32:
+      hipLaunchKernelGGL(mx_dequant_kernel<MxType::kF32>, grid, block, 0, stream, codes, m.scales,
+                         out, octets);
+      break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace aqlm

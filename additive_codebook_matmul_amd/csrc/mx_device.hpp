@@ -1,0 +1,120 @@
+// Device helpers of the microscaled (MXFP4) kernels for gfx950.
+#pragma once
+
+#include <type_traits>
+
+#include "aqlm_device.hpp"
+#include "mx_internal.hpp"
+
+namespace aqlm {
+
+typedef __bf16 bhalf2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bhalf8_t __attribute__((ext_vector_type(8)));
+typedef float float2_t __attribute__((ext_vector_type(2)));
+typedef int int8_vt __attribute__((ext_vector_type(8)));
+
+// Offset past every buffer resource made here: the load returns zero.
+constexpr uint32_t kMxOOB = 0x80000000u;
+
+// The E8M0 byte s as a float32 operand of the conversion instructions, which
+// read its exponent field alone: s = 0 (bits of 0.0f) is taken as 2^-127, s =
+// 255 (bits of infinity) as NaN.
+__device__ __forceinline__ float mx_scale(uint32_t s) {
+  return __builtin_bit_cast(float, s << 23);
+}
+
+__device__ __forceinline__ uint32_t buf_load_u8(Rsrc r, uint32_t off) {
+  return (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0);
+}
+
+// Eight E2M1 codes (one word, lowest nibble first) times a scale, as eight
+// halves; one rounding where the type needs one.
+template <MxType T> __device__ __forceinline__ uint4 mx_decode8(uint32_t w, float s) {
+  uint4 r;
+  if constexpr (T == MxType::kF16) {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3));
+  } else {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+  }
+  return r;
+}
+
+// Whether float16 holds every weight of a block with scale byte s exactly:
+// 0.5 * 2^(s-127) >= 2^-24 and 6 * 2^(s-127) <= 65504 (NaN needs no care).
+__device__ __forceinline__ bool mx_fits_f16(uint32_t s) { return s - 104u <= 36u || s == 255u; }
+
+// Eight float16 activations as the exact sum hi + lo of two bfloat16 vectors
+// (11 significant bits: hi takes the nearest 8, what is left has 3 or fewer
+// and a magnitude bfloat16 holds). Infinities and NaN stay in hi alone.
+__device__ __forceinline__ void split_f16(const uint4 &x, uint4 &hi, uint4 &lo) {
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t hw[2], lw[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float v = h2f(e ? in[i] >> 16 : in[i] & 0xFFFFu);
+      const __bf16 a = static_cast<__bf16>(v);
+      const float rest = v - static_cast<float>(a);
+      const bool finite = __builtin_fabsf(v) < __builtin_inff();
+      const __bf16 b = static_cast<__bf16>(finite ? rest : 0.0f);
+      hw[e] = __builtin_bit_cast(uint16_t, a);
+      lw[e] = __builtin_bit_cast(uint16_t, b);
+    }
+    h[i] = hw[0] | (hw[1] << 16);
+    l[i] = lw[0] | (lw[1] << 16);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// v_mfma_f32_16x16x32 / 32x32x16 on halves of type T.
+template <MxType T>
+__device__ __forceinline__ float4_t mx_mfma16(const uint4 &a, const uint4 &b, float4_t c) {
+  if constexpr (T == MxType::kF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a),
+                                                  __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bhalf8_t, a),
+                                                   __builtin_bit_cast(bhalf8_t, b), c, 0, 0, 0);
+}
+template <MxType T>
+__device__ __forceinline__ float16_t mx_mfma32(const uint4 &a, const uint4 &b, float16_t c) {
+  if constexpr (T == MxType::kF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a),
+                                                  __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bhalf8_t, a),
+                                                   __builtin_bit_cast(bhalf8_t, b), c, 0, 0, 0);
+}
+
+// float32 -> 16 bits of T, round to nearest even.
+template <MxType T> __device__ __forceinline__ uint32_t f2t(float f) {
+  if constexpr (T == MxType::kF16) return f2h(f);
+  else return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+}
+
+// Four consecutive results of one output row: one 8-byte store where `packed`
+// (n a multiple of 4, so that all four are inside or none is).
+template <MxType T>
+__device__ __forceinline__ void store4(uint16_t *row, int64_t c, int64_t n, const float4_t &v,
+                                       bool packed) {
+  if (packed) {
+    if (c < n)
+      *reinterpret_cast<uint2 *>(row + c) = make_uint2(f2t<T>(v[0]) | (f2t<T>(v[1]) << 16),
+                                                       f2t<T>(v[2]) | (f2t<T>(v[3]) << 16));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < n) row[c + e] = (uint16_t)f2t<T>(v[e]);
+  }
+}
+
+}  // namespace aqlm

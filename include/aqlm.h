@@ -89,9 +89,11 @@ typedef enum aqlm_status {
   AQLM_ERR_ALIGN = 4,  /* a pointer is not 16-byte aligned */
   AQLM_ERR_BATCH = 5,  /* batch outside the entry point's range */
   AQLM_ERR_HIP = 6,    /* the HIP runtime reported an error at launch */
-  AQLM_ERR_WORKSPACE = 7, /* the workspace is smaller than aqlm_gemm_workspace_size */
-  AQLM_ERR_SCRATCH = 8    /* aqlm_gemm_noalloc: the call needs more than
+  AQLM_ERR_WORKSPACE = 7, /* the workspace is smaller than the entry point's
+                             *_workspace_size */
+  AQLM_ERR_SCRATCH = 8,   /* aqlm_gemm_noalloc: the call needs more than
                              AQLM_STATIC_SCRATCH_BYTES of scratch memory */
+  AQLM_ERR_TYPE = 9       /* aqlm_mx.h: unknown element type or scale rule */
 } aqlm_status;
 
 /* Size of the static device scratch array behind aqlm_gemm_noalloc (64 MiB;

@@ -7,3 +7,4 @@ from .aqlm_oracle import (  # noqa: F401
     packed_bits_per_weight, product, unpack_codes, within_tolerance,
 )
 from . import encoder_oracle  # noqa: F401
+from . import mx_oracle  # noqa: F401
