@@ -154,9 +154,7 @@ hipError_t gemm_as(const MxDesc &W, const void *x, int64_t batch, void *y, hipSt
   Group g;
   g.n = 1;
   g.item[0] = item_of(W, x, y);
-  if (batch <= 16) return launch_skinny<T, 1, 1, 8>(g, batch, stream);
-  if (batch <= 32) return launch_skinny<T, 1, 2, 8>(g, batch, stream);
-  return launch_skinny<T, 2, 4, 4>(g, batch, stream);
+  return launch_skinny<T, 1, 1, 8>(g, batch, stream);
 }
 
 }  // namespace
@@ -170,10 +168,13 @@ hipError_t launch_mx_gemv_batched(const MxDesc *W, const void *const *x, void *c
                               : launch_skinny<MxType::kBF16, 1, 1, 8>(g, batch, stream);
 }
 
-int64_t mx_gemm_ws_bytes(const MxDesc &, int64_t) { return 0; }
+int64_t mx_gemm_ws_bytes(const MxDesc &W, int64_t batch) {
+  return batch < kMxTileBatch ? 0 : mx_gemm_tile_ws_bytes(W, batch);
+}
 
 hipError_t launch_mx_gemm(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
-                          void *, hipStream_t stream) {
+                          void *ws, hipStream_t stream) {
+  if (batch >= kMxTileBatch) return launch_mx_gemm_tile(W, x, batch, y, type, ws, stream);
   return type == MxType::kF16 ? gemm_as<MxType::kF16>(W, x, batch, y, stream)
                               : gemm_as<MxType::kBF16>(W, x, batch, y, stream);
 }

@@ -1,0 +1,330 @@
+// Product of half activations with microscaled weights for many rows of
+// activations: y = x . W^T with one workgroup per [rows of W] x [tokens] tile.
+//
+// Expanding E2M1 costs one conversion for two weights, little enough that each
+// wavefront expands its own rows straight from the codes in registers: the
+// weights never pass through LDS, where only the activations lie, shared by
+// the workgroup's wavefronts.
+//   * Wavefront w owns rows 32 RT w .. + 32 RT - 1 of the tile and all of its
+//     32 NT tokens: RT x NT tiles of v_mfma_f32_32x32x16.
+//   * A K step is 64 inputs, two blocks: lane (r, h) = (lane % 32, lane / 32)
+//     loads the 16 bytes that hold block h of row r and feeds codes 8 s ..
+//     8 s + 7 of it to the step's instruction s, whose activation operand is
+//     then the 16 bytes of inputs 32 h + 8 s of its token.
+//   * Activations are loaded one K step ahead into registers and stored to
+//     one of two LDS buffers; rows there are 128 bytes and 16-byte chunk j of
+//     row t lies at chunk j ^ ((t >> 1) & 7), so that the 16 lanes of an LDS
+//     pass touch 16 distinct groups of banks.
+//   * Where there are few tiles the K steps are split over workgroups whose
+//     float32 sums go to the workspace, as the accumulator registers lie, and
+//     a second kernel adds them in a fixed order.
+#include <algorithm>
+
+#include "mx_device.hpp"
+
+namespace aqlm {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+
+// Byte offset of 16-byte chunk j of activation row t in an LDS buffer.
+__device__ __forceinline__ uint32_t x_off(int t, int j) {
+  return (uint32_t)t * 128u + (uint32_t)((j ^ ((t >> 1) & 7)) << 4);
+}
+
+struct TileArgs {
+  const uint8_t *codes;
+  const uint8_t *scales;
+  const uint16_t *x;
+  uint16_t *y;
+  float4_t *part;  // [splits][tiles][RT * NT * 4][threads], or null
+  int rows, cols, batch;
+  int row_tiles, tok_tiles, splits, steps_per_split;
+};
+
+// Workgroup -> tile. Workgroups go round the 8 XCDs in turn, each with an L2
+// of its own: give every XCD one run of consecutive tiles, tokens fastest, so
+// that the workgroups at work on an XCD share rows of W and steps of x.
+__device__ __forceinline__ int xcd_tile(int b, int n) {
+  const int per = n >> 3, rest = n & 7, xcd = b & 7, i = b >> 3;
+  return xcd * per + min(xcd, rest) + i;
+}
+
+template <MxType T, int RT, int NT>
+__global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) {
+  __shared__ __attribute__((aligned(16))) uint8_t xt[2][NT * 32 * 128];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+  const int tiles = A.row_tiles * A.tok_tiles;
+  const int job = xcd_tile((int)blockIdx.x, tiles * A.splits);
+  const int split = job / tiles, tile = job - split * tiles;
+  const int row_tile = tile / A.tok_tiles;
+  const int tok0 = (tile - row_tile * A.tok_tiles) * (32 * NT);
+  const int row0 = (row_tile * kWaves + wave) * (32 * RT);
+  const int nb = A.cols >> 5;
+  const int steps = (nb + 1) >> 1;
+  const int k0 = split * A.steps_per_split, k1 = min(steps, k0 + A.steps_per_split);
+
+  // resources that end with the tile's last row: rows past it read zero
+  const uint32_t half = (uint32_t)A.cols >> 1;
+  const int wave_rows = max(0, min(32 * RT, A.rows - row0));
+  const int tile_toks = min(32 * NT, A.batch - tok0);
+  const Rsrc crs = make_rsrc(A.codes + (int64_t)row0 * half, (uint32_t)wave_rows * half);
+  const Rsrc srs = make_rsrc(A.scales + (int64_t)row0 * nb, (uint32_t)wave_rows * nb);
+  const Rsrc xrs = make_rsrc(A.x + (int64_t)tok0 * A.cols, (uint32_t)tile_toks * A.cols * 2u);
+
+  float16_t acc[RT][NT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  // one K step's loads: activation chunks c = tid + 256 i (token c / 8, chunk
+  // c % 8), the wavefront's own codes and scale bytes
+  uint4 xr[NT];
+  auto load_x = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int c = tid + i * kThreads, t = c >> 3, j = c & 7;
+      const bool in = k < k1 && 2 * k + (j >> 2) < nb;
+      xr[i] = buf_load16(xrs, in ? (uint32_t)t * (uint32_t)A.cols * 2u + (uint32_t)k * 128u + 16u * j
+                                 : kMxOOB);
+    }
+  };
+  auto store_x = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int c = tid + i * kThreads;
+      *reinterpret_cast<uint4 *>(xt[buf] + x_off(c >> 3, c & 7)) = xr[i];
+    }
+  };
+  auto load_w = [&](int k, uint4 (&wv)[RT], uint32_t (&sv)[RT]) __attribute__((always_inline)) {
+    const int blk = 2 * k + h;
+    const bool in = k < k1 && blk < nb;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const uint32_t r = 32u * i + l32;
+      wv[i] = buf_load16(crs, in ? r * half + (uint32_t)blk * 16u : kMxOOB);
+      const uint32_t s = buf_load_u8(srs, in ? r * nb + (uint32_t)blk : kMxOOB);
+      sv[i] = in && (int)r < wave_rows ? s : 127u;
+    }
+  };
+  auto step = [&](int k, int buf, const uint4 (&wv)[RT], const uint32_t (&sv)[RT], uint4 (&wn)[RT],
+                  uint32_t (&sn)[RT]) __attribute__((always_inline)) {
+    load_x(k + 1);
+    load_w(k + 2, wn, sn);
+    const uint8_t *X = xt[buf];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      uint4 b[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        b[j] = *reinterpret_cast<const uint4 *>(X + x_off(32 * j + l32, 4 * h + s));
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+        const uint4 a = mx_decode8<T>(ww[s], mx_scale(sv[i]));
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma32<T>(a, b[j], acc[i][j]);
+      }
+    }
+    store_x(buf ^ 1);
+    __syncthreads();
+  };
+
+  // Steps go in pairs, the second of which may lie past the end: its codes
+  // and activations are zeros, its scales 1.
+  uint4 w[2][RT], wn[2][RT];
+  uint32_t sb[2][RT], sn[2][RT];
+  load_x(k0);
+  load_w(k0, w[0], sb[0]);
+  load_w(k0 + 1, w[1], sb[1]);
+  store_x(0);
+  __syncthreads();
+  auto next = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        w[u][i] = wn[u][i];
+        sb[u][i] = sn[u][i];
+      }
+  };
+  int k = k0;
+  for (; k < k1; k += 2) {
+    if constexpr (T == MxType::kF16) {
+      bool fits = true;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) fits = fits && mx_fits_f16(sb[0][i]) && mx_fits_f16(sb[1][i]);
+      if (!__all(fits)) break;
+    }
+    step(k, 0, w[0], sb[0], wn[0], sn[0]);
+    step(k + 1, 1, w[1], sb[1], wn[1], sn[1]);
+    next();
+  }
+  // From the wavefront's first scale that float16 weights cannot take: the
+  // same product in bfloat16, which holds every weight, with x split exactly
+  // in two. The barriers are those of the other loop, one a step, so
+  // wavefronts in either meet.
+  if constexpr (T == MxType::kF16) {
+    for (; k < k1; k += 2) {
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {
+        load_x(k + u + 1);
+        if (u == 0) load_w(k + 2, wn[0], sn[0]);
+        else load_w(k + 3, wn[1], sn[1]);
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            uint4 hi, lo;
+            split_f16(*reinterpret_cast<const uint4 *>(xt[u] + x_off(32 * j + l32, 4 * h + s)), hi,
+                      lo);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              const uint4 c = u == 0 ? w[0][i] : w[1][i];
+              const uint32_t word = s == 0 ? c.x : s == 1 ? c.y : s == 2 ? c.z : c.w;
+              const uint4 a =
+                  mx_decode8<MxType::kBF16>(word, mx_scale(u == 0 ? sb[0][i] : sb[1][i]));
+              acc[i][j] = mx_mfma32<MxType::kBF16>(a, hi, acc[i][j]);
+              acc[i][j] = mx_mfma32<MxType::kBF16>(a, lo, acc[i][j]);
+            }
+          }
+        store_x(u ^ 1);
+        __syncthreads();
+      }
+      next();
+    }
+  }
+
+  // register 4 g + e of a 32 x 32 tile: row 8 g + 4 h + e, token l32
+  if (A.splits > 1) {
+    float4_t *p = A.part + (int64_t)job * (RT * NT * 4 * kThreads) + tid;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          p[((i * NT + j) * 4 + g) * kThreads] = float4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1],
+                                                          acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+    return;
+  }
+  const bool packed = (A.rows & 3) == 0;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int tok = tok0 + 32 * j + l32;
+    if (tok >= A.batch) continue;
+    uint16_t *row = A.y + (int64_t)tok * A.rows;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        store4<T>(row, row0 + 32 * i + 8 * g + 4 * h, A.rows,
+                  float4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                           acc[i][j][4 * g + 3]},
+                  packed);
+  }
+}
+
+// Sums of the split parts, in order of the split, rounded and stored.
+template <MxType T, int RT, int NT>
+__global__ __launch_bounds__(kThreads) void mx_tile_sum_kernel(const TileArgs A) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tiles = A.row_tiles * A.tok_tiles;
+  const int slot = (int)blockIdx.x % (RT * NT * 4), tile = (int)blockIdx.x / (RT * NT * 4);
+  const float4_t *p = A.part + ((int64_t)tile * (RT * NT * 4) + slot) * kThreads + tid;
+  const int64_t stride = (int64_t)tiles * (RT * NT * 4) * kThreads;
+  float4_t v = p[0];
+  for (int s = 1; s < A.splits; ++s) v += p[s * stride];
+  const int g = slot & 3, j = (slot >> 2) % NT, i = (slot >> 2) / NT;
+  const int row_tile = tile / A.tok_tiles;
+  const int tok = (tile - row_tile * A.tok_tiles) * (32 * NT) + 32 * j + (lane & 31);
+  const int row = (row_tile * kWaves + wave) * (32 * RT) + 32 * i + 8 * g + 4 * (lane >> 5);
+  if (tok < A.batch) store4<T>(A.y + (int64_t)tok * A.rows, row, A.rows, v, (A.rows & 3) == 0);
+}
+
+// Tile of a product: rows of W per wavefront in units of 32, tokens in units
+// of 32, workgroups K is split over.
+struct Plan {
+  int rt, nt, splits, steps_per_split;
+  int64_t row_tiles, tok_tiles;
+};
+
+Plan plan_of(int64_t rows, int64_t cols, int64_t batch) {
+  Plan p;
+  p.nt = batch <= 32 ? 1 : batch <= 64 ? 2 : batch <= 96 ? 3 : 4;
+  p.rt = 2;
+  p.tok_tiles = (batch + 32 * p.nt - 1) / (32 * p.nt);
+  p.row_tiles = (rows + 32 * kWaves * p.rt - 1) / (32 * kWaves * p.rt);
+  if (p.row_tiles * p.tok_tiles < 256) {
+    p.rt = 1;
+    p.row_tiles = (rows + 32 * kWaves - 1) / (32 * kWaves);
+  }
+  const int64_t steps = (cols / 32 + 1) / 2, tiles = p.row_tiles * p.tok_tiles;
+  // about two workgroups per CU, at least eight K steps each
+  int64_t s = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, steps / 8));
+  if (tiles >= 192) s = 1;
+  p.steps_per_split = (int)((steps + s - 1) / s);
+  p.splits = (int)((steps + p.steps_per_split - 1) / p.steps_per_split);
+  return p;
+}
+
+template <MxType T, int RT, int NT>
+hipError_t launch_tile(const TileArgs &A, hipStream_t stream) {
+  const unsigned tiles = (unsigned)(A.row_tiles * A.tok_tiles);
+  hipLaunchKernelGGL((mx_tile_kernel<T, RT, NT>), dim3(tiles * A.splits), dim3(kThreads), 0, stream,
+                     A);
+  if (A.splits > 1)
+    hipLaunchKernelGGL((mx_tile_sum_kernel<T, RT, NT>), dim3(tiles * RT * NT * 4), dim3(kThreads), 0,
+                       stream, A);
+  return hipGetLastError();
+}
+
+template <MxType T> hipError_t tile_as(const Plan &p, const TileArgs &A, hipStream_t stream) {
+  switch (p.rt * 8 + p.nt) {
+    case 9: return launch_tile<T, 1, 1>(A, stream);
+    case 10: return launch_tile<T, 1, 2>(A, stream);
+    case 11: return launch_tile<T, 1, 3>(A, stream);
+    case 12: return launch_tile<T, 1, 4>(A, stream);
+    case 17: return launch_tile<T, 2, 1>(A, stream);
+    case 18: return launch_tile<T, 2, 2>(A, stream);
+    case 19: return launch_tile<T, 2, 3>(A, stream);
+    default: return launch_tile<T, 2, 4>(A, stream);
+  }
+}
+
+}  // namespace
+
+int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch) {
+  const Plan p = plan_of(W.rows, W.cols, batch);
+  if (p.splits == 1) return 0;
+  return p.row_tiles * p.tok_tiles * p.splits * (int64_t)(p.rt * p.nt * 4 * kThreads) *
+         (int64_t)sizeof(float4_t);
+}
+
+hipError_t launch_mx_gemm_tile(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
+                               void *ws, hipStream_t stream) {
+  const Plan p = plan_of(W.rows, W.cols, batch);
+  TileArgs A;
+  A.codes = W.codes;
+  A.scales = W.scales;
+  A.x = static_cast<const uint16_t *>(x);
+  A.y = static_cast<uint16_t *>(y);
+  A.part = static_cast<float4_t *>(ws);
+  A.rows = (int)W.rows;
+  A.cols = (int)W.cols;
+  A.batch = (int)batch;
+  A.row_tiles = (int)p.row_tiles;
+  A.tok_tiles = (int)p.tok_tiles;
+  A.splits = p.splits;
+  A.steps_per_split = p.steps_per_split;
+  return type == MxType::kF16 ? tile_as<MxType::kF16>(p, A, stream)
+                              : tile_as<MxType::kBF16>(p, A, stream);
+}
+
+}  // namespace aqlm
