@@ -59,8 +59,9 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
   const int l32 = lane & 31, h = lane >> 5;
   const int tiles = A.row_tiles * A.tok_tiles;
   const int job = xcd_tile((int)blockIdx.x, tiles * A.splits);
-  const int split = job / tiles, tile = job - split * tiles;
-  const int row_tile = tile / A.tok_tiles;
+  // (uniform, but divisions run on the vector unit: back to scalar registers)
+  const int split = __builtin_amdgcn_readfirstlane(job / tiles), tile = job - split * tiles;
+  const int row_tile = __builtin_amdgcn_readfirstlane(tile / A.tok_tiles);
   const int tok0 = (tile - row_tile * A.tok_tiles) * (32 * NT);
   const int row0 = (row_tile * kWaves + wave) * (32 * RT);
   const int nb = A.cols >> 5;
@@ -69,8 +70,8 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
 
   // resources that end with the tile's last row: rows past it read zero
   const uint32_t half = (uint32_t)A.cols >> 1;
-  const int wave_rows = max(0, min(32 * RT, A.rows - row0));
-  const int tile_toks = min(32 * NT, A.batch - tok0);
+  const int wave_rows = __builtin_amdgcn_readfirstlane(max(0, min(32 * RT, A.rows - row0)));
+  const int tile_toks = __builtin_amdgcn_readfirstlane(min(32 * NT, A.batch - tok0));
   const Rsrc crs = make_rsrc(A.codes + (int64_t)row0 * half, (uint32_t)wave_rows * half);
   const Rsrc srs = make_rsrc(A.scales + (int64_t)row0 * nb, (uint32_t)wave_rows * nb);
   const Rsrc xrs = make_rsrc(A.x + (int64_t)tok0 * A.cols, (uint32_t)tile_toks * A.cols * 2u);
@@ -109,35 +110,53 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
     for (int i = 0; i < RT; ++i) {
       const uint32_t r = 32u * i + l32;
       wv[i] = buf_load16(crs, in ? r * half + (uint32_t)blk * 16u : kMxOOB);
-      const uint32_t s = buf_load_u8(srs, in ? r * nb + (uint32_t)blk : kMxOOB);
-      sv[i] = in && (int)r < wave_rows ? s : 127u;
+      sv[i] = buf_load_u8(srs, in ? r * nb + (uint32_t)blk : kMxOOB);
     }
+  };
+  // whether a step's scales suit float16 weights (those that exist)
+  auto fits = [&](int k, const uint32_t (&sv)[RT]) __attribute__((always_inline)) {
+    bool f = true;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      f = f && (mx_fits_f16(sv[i]) || 2 * k + h >= nb || 32 * i + l32 >= wave_rows);
+    return f;
   };
   auto step = [&](int k, int buf, const uint4 (&wv)[RT], const uint32_t (&sv)[RT], uint4 (&wn)[RT],
                   uint32_t (&sn)[RT]) __attribute__((always_inline)) {
+    // the loads go out before anything else of the step
     load_x(k + 1);
     load_w(k + 2, wn, sn);
+    __builtin_amdgcn_sched_barrier(0);
     const uint8_t *X = xt[buf];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      uint4 b[NT];
+    uint4 b[2][NT];
+    auto reads = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        b[j] = *reinterpret_cast<const uint4 *>(X + x_off(32 * j + l32, 4 * h + s));
+        b[s & 1][j] = *reinterpret_cast<const uint4 *>(X + x_off(32 * j + l32, 4 * h + s));
+    };
+    reads(0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s < 3) reads(s + 1);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
         const uint4 a = mx_decode8<T>(ww[s], mx_scale(sv[i]));
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma32<T>(a, b[j], acc[i][j]);
+        for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma32<T>(a, b[s & 1][j], acc[i][j]);
+      }
+      if (s < 3) {  // the next instruction's operands are read before this one's products
+        __builtin_amdgcn_sched_group_barrier(0x100, NT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, RT * NT, 0);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
     store_x(buf ^ 1);
     __syncthreads();
   };
 
   // Steps go in pairs, the second of which may lie past the end: its codes
-  // and activations are zeros, its scales 1.
+  // and activations are zeros.
   uint4 w[2][RT], wn[2][RT];
   uint32_t sb[2][RT], sn[2][RT];
   load_x(k0);
@@ -157,10 +176,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
   int k = k0;
   for (; k < k1; k += 2) {
     if constexpr (T == MxType::kF16) {
-      bool fits = true;
-#pragma unroll
-      for (int i = 0; i < RT; ++i) fits = fits && mx_fits_f16(sb[0][i]) && mx_fits_f16(sb[1][i]);
-      if (!__all(fits)) break;
+      if (!__all(fits(k, sb[0]) && (k + 1 >= k1 || fits(k + 1, sb[1])))) break;
     }
     step(k, 0, w[0], sb[0], wn[0], sn[0]);
     step(k + 1, 1, w[1], sb[1], wn[1], sn[1]);
