@@ -47,7 +47,7 @@ template <MxType T> __device__ __forceinline__ uint4 mx_decode8(uint32_t w, floa
 
 // Whether float16 holds every weight of a block with scale byte s exactly:
 // 0.5 * 2^(s-127) >= 2^-24 and 6 * 2^(s-127) <= 65504 (NaN needs no care).
-__device__ __forceinline__ bool mx_fits_f16(uint32_t s) { return s - 104u <= 36u || s == 255u; }
+__device__ __forceinline__ bool mx_fits_f16(uint32_t s) { return (s - 104u <= 36u) | (s == 255u); }
 
 // Eight float16 activations as the exact sum hi + lo of two bfloat16 vectors
 // (11 significant bits: hi takes the nearest 8, what is left has 3 or fewer

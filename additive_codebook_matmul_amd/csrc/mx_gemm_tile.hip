@@ -103,23 +103,21 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
       *reinterpret_cast<uint4 *>(xt[buf] + x_off(c >> 3, c & 7)) = xr[i];
     }
   };
+  // Past the last row or block the codes are zeros; the scale byte is that of
+  // the last one there is, so that it is one of this row (or of a row that is
+  // not stored) and no care is needed where it is used: only a NaN would show,
+  // in a row that is NaN already.
+  uint32_t srow[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) srow[i] = (uint32_t)max(0, min(32 * i + l32, wave_rows - 1)) * nb;
   auto load_w = [&](int k, uint4 (&wv)[RT], uint32_t (&sv)[RT]) __attribute__((always_inline)) {
     const int blk = 2 * k + h;
     const bool in = k < k1 && blk < nb;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const uint32_t r = 32u * i + l32;
-      wv[i] = buf_load16(crs, in ? r * half + (uint32_t)blk * 16u : kMxOOB);
-      sv[i] = buf_load_u8(srs, in ? r * nb + (uint32_t)blk : kMxOOB);
+      wv[i] = buf_load16(crs, in ? (32u * i + l32) * half + (uint32_t)blk * 16u : kMxOOB);
+      sv[i] = buf_load_u8(srs, srow[i] + (uint32_t)min(blk, nb - 1));
     }
-  };
-  // whether a step's scales suit float16 weights (those that exist)
-  auto fits = [&](int k, const uint32_t (&sv)[RT]) __attribute__((always_inline)) {
-    bool f = true;
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-      f = f && (mx_fits_f16(sv[i]) || 2 * k + h >= nb || 32 * i + l32 >= wave_rows);
-    return f;
   };
   auto step = [&](int k, int buf, const uint4 (&wv)[RT], const uint32_t (&sv)[RT], uint4 (&wn)[RT],
                   uint32_t (&sn)[RT]) __attribute__((always_inline)) {
@@ -176,7 +174,10 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
   int k = k0;
   for (; k < k1; k += 2) {
     if constexpr (T == MxType::kF16) {
-      if (!__all(fits(k, sb[0]) && (k + 1 >= k1 || fits(k + 1, sb[1])))) break;
+      bool f = true;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) f = f & mx_fits_f16(sb[0][i]) & mx_fits_f16(sb[1][i]);
+      if (!__all(f) & (wave_rows > 0)) break;
     }
     step(k, 0, w[0], sb[0], wn[0], sn[0]);
     step(k + 1, 1, w[1], sb[1], wn[1], sn[1]);
@@ -188,11 +189,10 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
   // wavefronts in either meet.
   if constexpr (T == MxType::kF16) {
     for (; k < k1; k += 2) {
-#pragma unroll 1
+#pragma unroll
       for (int u = 0; u < 2; ++u) {
         load_x(k + u + 1);
-        if (u == 0) load_w(k + 2, wn[0], sn[0]);
-        else load_w(k + 3, wn[1], sn[1]);
+        load_w(k + u + 2, wn[u], sn[u]);
 #pragma unroll 1
         for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -202,10 +202,9 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
                       lo);
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
-              const uint4 c = u == 0 ? w[0][i] : w[1][i];
+              const uint4 c = w[u][i];
               const uint32_t word = s == 0 ? c.x : s == 1 ? c.y : s == 2 ? c.z : c.w;
-              const uint4 a =
-                  mx_decode8<MxType::kBF16>(word, mx_scale(u == 0 ? sb[0][i] : sb[1][i]));
+              const uint4 a = mx_decode8<MxType::kBF16>(word, mx_scale(sb[u][i]));
               acc[i][j] = mx_mfma32<MxType::kBF16>(a, hi, acc[i][j]);
               acc[i][j] = mx_mfma32<MxType::kBF16>(a, lo, acc[i][j]);
             }
