@@ -7,14 +7,18 @@
 // the workgroup's wavefronts.
 //   * Wavefront w owns rows 32 RT w .. + 32 RT - 1 of the tile and all of its
 //     32 NT tokens: RT x NT tiles of v_mfma_f32_32x32x16.
-//   * A K step is 64 inputs, two blocks: lane (r, h) = (lane % 32, lane / 32)
-//     loads the 16 bytes that hold block h of row r and feeds codes 8 s ..
-//     8 s + 7 of it to the step's instruction s, whose activation operand is
-//     then the 16 bytes of inputs 32 h + 8 s of its token.
-//   * Activations are loaded one K step ahead into registers and stored to
-//     one of two LDS buffers; rows there are 128 bytes and 16-byte chunk j of
-//     row t lies at chunk j ^ ((t >> 1) & 7), so that the 16 lanes of an LDS
-//     pass touch 16 distinct groups of banks.
+//   * K goes in groups of four steps, eight blocks of 32 inputs: lane (r, h) =
+//     (lane % 32, lane / 32) takes blocks 4 h .. 4 h + 3 of the group, whose
+//     scales are one word, and step u multiplies block 4 h + u: its 16 bytes of
+//     codes give the operands of four instructions, s taking codes 8 s .. 8 s +
+//     7, so that the activation operand is the 16 bytes of inputs 8 s of the
+//     same block of the lane's token. (The sum over K does not care which
+//     inputs meet in an instruction, so no code ever changes lanes.)
+//   * Activations go from memory straight to LDS three steps ahead, into one
+//     of four stages, codes to registers two steps ahead. LDS rows are 128
+//     bytes (blocks u and 4 + u) and 16-byte chunk j of row t lies at chunk
+//     j ^ ((t >> 1) & 7), so that the 16 lanes of an LDS pass touch 16
+//     distinct groups of banks.
 //   * Where there are few tiles the K steps are split over workgroups whose
 //     float32 sums go to the workspace, as the accumulator registers lie, and
 //     a second kernel adds them in a fixed order.
@@ -40,7 +44,7 @@ struct TileArgs {
   uint16_t *y;
   float4_t *part;  // [splits][tiles][RT * NT * 4][threads], or null
   int rows, cols, batch;
-  int row_tiles, tok_tiles, splits, steps_per_split;
+  int row_tiles, tok_tiles, splits, groups_per_split;
 };
 
 // Workgroup -> tile. Workgroups go round the 8 XCDs in turn, each with an L2
@@ -53,7 +57,10 @@ __device__ __forceinline__ int xcd_tile(int b, int n) {
 
 template <MxType T, int RT, int NT>
 __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) {
-  __shared__ __attribute__((aligned(16))) uint8_t xt[2][NT * 32 * 128];
+  // one array per stage: the compiler then knows which loads into LDS a read
+  // of LDS can depend on
+  __shared__ __attribute__((aligned(16))) uint8_t xt0[NT * 32 * 128], xt1[NT * 32 * 128],
+      xt2[NT * 32 * 128], xt3[NT * 32 * 128];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, h = lane >> 5;
@@ -65,8 +72,8 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
   const int tok0 = (tile - row_tile * A.tok_tiles) * (32 * NT);
   const int row0 = (row_tile * kWaves + wave) * (32 * RT);
   const int nb = A.cols >> 5;
-  const int steps = (nb + 1) >> 1;
-  const int k0 = split * A.steps_per_split, k1 = min(steps, k0 + A.steps_per_split);
+  const int g0 = split * A.groups_per_split;
+  const int g1 = min((nb + 7) >> 3, g0 + A.groups_per_split);
 
   // resources that end with the tile's last row: rows past it read zero
   const uint32_t half = (uint32_t)A.cols >> 1;
@@ -84,137 +91,163 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  // one K step's loads: activation chunks c = tid + 256 i (token c / 8, chunk
-  // c % 8), the wavefront's own codes and scale bytes
-  uint4 xr[NT];
-  auto load_x = [&](int k) __attribute__((always_inline)) {
+  // A step's activations, straight into LDS: each load of a wavefront fills 1
+  // KiB (eight rows) in lane order, so a chunk's place in its row is chosen by
+  // where the lane reads from. Chunks past the last block are zeros.
+  const int xrow = tid >> 3, xj = (tid & 7) ^ ((tid >> 4) & 7);
+  auto load_x = [&](int g, int u, uint8_t *dst) __attribute__((always_inline)) {
+    const int blk = 8 * g + u + (xj & 4);
+    const bool in = (g < g1) & (blk < nb);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int c = tid + i * kThreads, t = c >> 3, j = c & 7;
-      const bool in = k < k1 && 2 * k + (j >> 2) < nb;
-      xr[i] = buf_load16(xrs, in ? (uint32_t)t * (uint32_t)A.cols * 2u + (uint32_t)k * 128u + 16u * j
-                                 : kMxOOB);
+      const uint32_t off = (uint32_t)(xrow + 32 * i) * (uint32_t)A.cols * 2u + (uint32_t)blk * 64u +
+                           16u * (xj & 3);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          xrs, (__attribute__((address_space(3))) void *)(dst + i * 4096 + wave * 1024), 16,
+          in ? off : kMxOOB, 0, 0, 0);
     }
   };
-  auto store_x = [&](int buf) __attribute__((always_inline)) {
+  auto load_w = [&](int g, int u, uint4 (&wv)[RT]) __attribute__((always_inline)) {
+    const int blk = 8 * g + 4 * h + u;
+    const bool in = (g < g1) & (blk < nb);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int c = tid + i * kThreads;
-      *reinterpret_cast<uint4 *>(xt[buf] + x_off(c >> 3, c & 7)) = xr[i];
-    }
+    for (int i = 0; i < RT; ++i)
+      wv[i] = buf_load16(crs, in ? (32u * i + l32) * half + (uint32_t)blk * 16u : kMxOOB);
   };
-  // Past the last row or block the codes are zeros; the scale byte is that of
-  // the last one there is, so that it is one of this row (or of a row that is
-  // not stored) and no care is needed where it is used: only a NaN would show,
-  // in a row that is NaN already.
+  // The four scale bytes of a group. Past the last row or block the codes are
+  // zeros and the byte is that of the last one there is, so that it is one of
+  // this row (or of a row that is not stored) and needs no care: only a NaN
+  // would show, in a row that is NaN already.
   uint32_t srow[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) srow[i] = (uint32_t)max(0, min(32 * i + l32, wave_rows - 1)) * nb;
-  auto load_w = [&](int k, uint4 (&wv)[RT], uint32_t (&sv)[RT]) __attribute__((always_inline)) {
-    const int blk = 2 * k + h;
-    const bool in = k < k1 && blk < nb;
+  const bool whole = (nb & 7) == 0;  // whole groups: every word aligned and inside its row
+  auto load_s = [&](int g, uint32_t (&sv)[RT]) __attribute__((always_inline)) {
+    const int blk = 8 * min(g, g1 - 1) + 4 * h;
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      wv[i] = buf_load16(crs, in ? (32u * i + l32) * half + (uint32_t)blk * 16u : kMxOOB);
-      sv[i] = buf_load_u8(srs, srow[i] + (uint32_t)min(blk, nb - 1));
-    }
-  };
-  auto step = [&](int k, int buf, const uint4 (&wv)[RT], const uint32_t (&sv)[RT], uint4 (&wn)[RT],
-                  uint32_t (&sn)[RT]) __attribute__((always_inline)) {
-    // the loads go out before anything else of the step
-    load_x(k + 1);
-    load_w(k + 2, wn, sn);
-    __builtin_amdgcn_sched_barrier(0);
-    const uint8_t *X = xt[buf];
-    uint4 b[2][NT];
-    auto reads = [&](int s) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        b[s & 1][j] = *reinterpret_cast<const uint4 *>(X + x_off(32 * j + l32, 4 * h + s));
-    };
-    reads(0);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (s < 3) reads(s + 1);
+      for (int i = 0; i < RT; ++i) sv[i] = buf_load4(srs, srow[i] + (uint32_t)blk);
+    } else {
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
-        const uint4 a = mx_decode8<T>(ww[s], mx_scale(sv[i]));
+        uint32_t v[4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma32<T>(a, b[s & 1][j], acc[i][j]);
-      }
-      if (s < 3) {  // the next instruction's operands are read before this one's products
-        __builtin_amdgcn_sched_group_barrier(0x100, NT, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, RT * NT, 0);
+        for (int u = 0; u < 4; ++u) v[u] = buf_load_u8(srs, srow[i] + (uint32_t)min(blk + u, nb - 1));
+        sv[i] = v[0] | (v[1] << 8) | (v[2] << 16) | (v[3] << 24);
       }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    store_x(buf ^ 1);
-    __syncthreads();
   };
 
-  // Steps go in pairs, the second of which may lie past the end: its codes
-  // and activations are zeros.
-  uint4 w[2][RT], wn[2][RT];
-  uint32_t sb[2][RT], sn[2][RT];
-  load_x(k0);
-  load_w(k0, w[0], sb[0]);
-  load_w(k0 + 1, w[1], sb[1]);
-  store_x(0);
-  __syncthreads();
-  auto next = [&]() __attribute__((always_inline)) {
+  // One step. `X` holds its activations; `far` is the stage that the step
+  // before read and the third one from here reads. Before the barrier the
+  // wavefront waits for the next step's codes `w1` (the empty asm uses them):
+  // loads return in order, and those were asked for a step after the next
+  // step's activations, so these lie in LDS. The operand reads of this step
+  // have long returned, since products used them.
+  auto step = [&](auto wide_c, int g, auto u_c, const uint8_t *X, uint8_t *far,
+                  const uint4 (&wv)[RT], const uint32_t (&sv)[RT], uint4 (&w1)[RT], uint4 (&w2)[RT])
+                  __attribute__((always_inline)) {
+    constexpr bool WIDE = decltype(wide_c)::value;
+    constexpr int U = decltype(u_c)::value;
+    load_w(U < 2 ? g : g + 1, (U + 2) & 3, w2);
+    load_x(U < 1 ? g : g + 1, (U + 3) & 3, far);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (!WIDE) {
+      uint4 b[2][NT];
+      auto reads = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+        for (int j = 0; j < NT; ++j)
+          b[s & 1][j] = *reinterpret_cast<const uint4 *>(X + x_off(32 * j + l32, 4 * h + s));
+      };
+      reads(0);
+      __builtin_amdgcn_sched_group_barrier(0x100, NT, 0);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        w[u][i] = wn[u][i];
-        sb[u][i] = sn[u][i];
+      for (int s = 0; s < 4; ++s) {
+        if (s < 3) reads(s + 1);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+          const uint4 a = mx_decode8<T>(ww[s], mx_scale((sv[i] >> (8 * U)) & 0xFFu));
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma32<T>(a, b[s & 1][j], acc[i][j]);
+        }
+        if (s < 3) {  // the next instruction's operands are read before this one's products
+          __builtin_amdgcn_sched_group_barrier(0x100, NT, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, RT * NT, 0);
+        }
       }
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint4 hi, lo;
+          split_f16(*reinterpret_cast<const uint4 *>(X + x_off(32 * j + l32, 4 * h + s)), hi, lo);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const uint32_t word = s == 0 ? wv[i].x : s == 1 ? wv[i].y : s == 2 ? wv[i].z : wv[i].w;
+            const uint4 a =
+                mx_decode8<MxType::kBF16>(word, mx_scale((sv[i] >> (8 * U)) & 0xFFu));
+            acc[i][j] = mx_mfma32<MxType::kBF16>(a, hi, acc[i][j]);
+            acc[i][j] = mx_mfma32<MxType::kBF16>(a, lo, acc[i][j]);
+          }
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) asm volatile("" : "+v"(w1[i].x) : : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_sched_barrier(0);
   };
-  int k = k0;
-  for (; k < k1; k += 2) {
+
+  uint4 w[4][RT];
+  uint32_t sc[RT], sn[RT];
+  load_s(g0, sc);
+  load_x(g0, 0, xt0);
+  __builtin_amdgcn_sched_barrier(0);
+  load_w(g0, 0, w[0]);
+  load_x(g0, 1, xt1);
+  __builtin_amdgcn_sched_barrier(0);
+  load_w(g0, 1, w[1]);
+  load_x(g0, 2, xt2);
+#pragma unroll
+  for (int i = 0; i < RT; ++i) asm volatile("" : "+v"(w[0][i].x) : : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" : : : "memory");
+  typedef std::integral_constant<int, 0> U0;
+  typedef std::integral_constant<int, 1> U1;
+  typedef std::integral_constant<int, 2> U2;
+  typedef std::integral_constant<int, 3> U3;
+  auto group = [&](auto wide_c, int g) __attribute__((always_inline)) {
+    load_s(g + 1, sn);
+    step(wide_c, g, U0{}, xt0, xt3, w[0], sc, w[1], w[2]);
+    step(wide_c, g, U1{}, xt1, xt0, w[1], sc, w[2], w[3]);
+    step(wide_c, g, U2{}, xt2, xt1, w[2], sc, w[3], w[0]);
+    step(wide_c, g, U3{}, xt3, xt2, w[3], sc, w[0], w[1]);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) sc[i] = sn[i];
+  };
+  int g = g0;
+  for (; g < g1; ++g) {
     if constexpr (T == MxType::kF16) {
       bool f = true;
 #pragma unroll
-      for (int i = 0; i < RT; ++i) f = f & mx_fits_f16(sb[0][i]) & mx_fits_f16(sb[1][i]);
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) f = f & mx_fits_f16((sc[i] >> (8 * u)) & 0xFFu);
       if (!__all(f) & (wave_rows > 0)) break;
     }
-    step(k, 0, w[0], sb[0], wn[0], sn[0]);
-    step(k + 1, 1, w[1], sb[1], wn[1], sn[1]);
-    next();
+    group(std::false_type{}, g);
   }
-  // From the wavefront's first scale that float16 weights cannot take: the
-  // same product in bfloat16, which holds every weight, with x split exactly
-  // in two. The barriers are those of the other loop, one a step, so
+  // From the wavefront's first group with a scale that float16 weights cannot
+  // take: the same product in bfloat16, which holds every weight, with x split
+  // exactly in two. The barriers are those of the other loop, one a step, so
   // wavefronts in either meet.
-  if constexpr (T == MxType::kF16) {
-    for (; k < k1; k += 2) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        load_x(k + u + 1);
-        load_w(k + u + 2, wn[u], sn[u]);
-#pragma unroll 1
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            uint4 hi, lo;
-            split_f16(*reinterpret_cast<const uint4 *>(xt[u] + x_off(32 * j + l32, 4 * h + s)), hi,
-                      lo);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-              const uint4 c = w[u][i];
-              const uint32_t word = s == 0 ? c.x : s == 1 ? c.y : s == 2 ? c.z : c.w;
-              const uint4 a = mx_decode8<MxType::kBF16>(word, mx_scale(sb[u][i]));
-              acc[i][j] = mx_mfma32<MxType::kBF16>(a, hi, acc[i][j]);
-              acc[i][j] = mx_mfma32<MxType::kBF16>(a, lo, acc[i][j]);
-            }
-          }
-        store_x(u ^ 1);
-        __syncthreads();
-      }
-      next();
-    }
-  }
+  if constexpr (T == MxType::kF16)
+    for (; g < g1; ++g) group(std::true_type{}, g);
+  // the zeros past the last group are in LDS before the wavefront can end
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 
   // register 4 g + e of a 32 x 32 tile: row 8 g + 4 h + e, token l32
   if (A.splits > 1) {
@@ -266,7 +299,7 @@ __global__ __launch_bounds__(kThreads) void mx_tile_sum_kernel(const TileArgs A)
 // Tile of a product: rows of W per wavefront in units of 32, tokens in units
 // of 32, workgroups K is split over.
 struct Plan {
-  int rt, nt, splits, steps_per_split;
+  int rt, nt, splits, groups_per_split;
   int64_t row_tiles, tok_tiles;
 };
 
@@ -280,12 +313,12 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t batch) {
     p.rt = 1;
     p.row_tiles = (rows + 32 * kWaves - 1) / (32 * kWaves);
   }
-  const int64_t steps = (cols / 32 + 1) / 2, tiles = p.row_tiles * p.tok_tiles;
-  // about two workgroups per CU, at least eight K steps each
-  int64_t s = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, steps / 8));
+  const int64_t groups = (cols / 32 + 7) / 8, tiles = p.row_tiles * p.tok_tiles;
+  // about two workgroups per CU, at least two groups of K steps each
+  int64_t s = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, groups / 2));
   if (tiles >= 192) s = 1;
-  p.steps_per_split = (int)((steps + s - 1) / s);
-  p.splits = (int)((steps + p.steps_per_split - 1) / p.steps_per_split);
+  p.groups_per_split = (int)((groups + s - 1) / s);
+  p.splits = (int)((groups + p.groups_per_split - 1) / p.groups_per_split);
   return p;
 }
 
@@ -337,7 +370,7 @@ hipError_t launch_mx_gemm_tile(const MxDesc &W, const void *x, int64_t batch, vo
   A.row_tiles = (int)p.row_tiles;
   A.tok_tiles = (int)p.tok_tiles;
   A.splits = p.splits;
-  A.steps_per_split = p.steps_per_split;
+  A.groups_per_split = p.groups_per_split;
   return type == MxType::kF16 ? tile_as<MxType::kF16>(p, A, stream)
                               : tile_as<MxType::kBF16>(p, A, stream);
 }
