@@ -2,26 +2,29 @@
 // activations: y = x . W^T with one workgroup per [rows of W] x [tokens] tile.
 //
 // Expanding E2M1 costs one conversion for two weights, little enough that each
-// wavefront expands its own rows straight from the codes in registers: the
-// weights never pass through LDS, where only the activations lie, shared by
-// the workgroup's wavefronts.
-//   * Wavefront w owns rows 32 RT w .. + 32 RT - 1 of the tile and all of its
-//     32 NT tokens: RT x NT tiles of v_mfma_f32_32x32x16.
-//   * K goes in groups of four steps, eight blocks of 32 inputs: lane (r, h) =
-//     (lane % 32, lane / 32) takes blocks 4 h .. 4 h + 3 of the group, whose
-//     scales are one word, and step u multiplies block 4 h + u: its 16 bytes of
-//     codes give the operands of four instructions, s taking codes 8 s .. 8 s +
-//     7, so that the activation operand is the 16 bytes of inputs 8 s of the
-//     same block of the lane's token. (The sum over K does not care which
-//     inputs meet in an instruction, so no code ever changes lanes.)
-//   * Activations go from memory straight to LDS three steps ahead, into one
-//     of four stages, codes to registers two steps ahead. LDS rows are 128
-//     bytes (blocks u and 4 + u) and 16-byte chunk j of row t lies at chunk
-//     j ^ ((t >> 1) & 7), so that the 16 lanes of an LDS pass touch 16
-//     distinct groups of banks.
-//   * Where there are few tiles the K steps are split over workgroups whose
-//     float32 sums go to the workspace, as the accumulator registers lie, and
-//     a second kernel adds them in a fixed order.
+// wavefront expands its operands in registers, from codes that lie in LDS.
+//   * A workgroup has four wavefronts along the rows (32 RT each) times TW
+//     along the tokens (32 NT each) times KW that share out K, and multiplies
+//     with v_mfma_f32_32x32x16.
+//   * A K step is 64 inputs, two blocks: lane (r, h) = (lane % 32, lane / 32)
+//     takes block h of row r, 16 bytes of codes, which give the operands of
+//     four instructions: instruction s multiplies codes 8 s .. 8 s + 7, so its
+//     activation operand is the 16 bytes of inputs 8 s of the same block of
+//     the lane's token. (The sum over K does not care which inputs meet in an
+//     instruction, so no code changes lanes after its load.)
+//   * Codes and activations go from memory straight to LDS, three steps ahead,
+//     into one of four stages. The loads read whole stretches of rows (32
+//     bytes of codes, 128 of activations, by neighbouring lanes): a lane that
+//     loads its own row's 16 bytes straight to registers costs the address
+//     unit a cache line a lane, which bounded an earlier form of this kernel
+//     (190 us; 178 with the activations alone through LDS three steps ahead; 174 now,
+//     for 2048 x 11008 x 4096).
+//   * Chunks of 16 bytes are permuted within a row on their way (x_off,
+//     w_off), so that the 16 lanes of an LDS pass touch 16 distinct groups of
+//     banks.
+//   * Where there are few tiles K is split over workgroups too, whose float32
+//     sums go to the workspace, as the accumulator registers lie, and a second
+//     kernel adds them in a fixed order.
 #include <algorithm>
 
 #include "mx_device.hpp"
@@ -29,12 +32,15 @@
 namespace aqlm {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
+constexpr int kRowWaves = 4;
 
-// Byte offset of 16-byte chunk j of activation row t in an LDS buffer.
+// Byte offset of 16-byte chunk j (of 8) of activation row t in a stage.
 __device__ __forceinline__ uint32_t x_off(int t, int j) {
   return (uint32_t)t * 128u + (uint32_t)((j ^ ((t >> 1) & 7)) << 4);
+}
+// Byte offset of block h (of 2) of weight row r in a stage.
+__device__ __forceinline__ uint32_t w_off(int r, int h) {
+  return (uint32_t)r * 32u + (uint32_t)((h ^ ((r >> 3) & 1)) << 4);
 }
 
 struct TileArgs {
@@ -55,32 +61,42 @@ __device__ __forceinline__ int xcd_tile(int b, int n) {
   return xcd * per + min(xcd, rest) + i;
 }
 
-template <MxType T, int RT, int NT>
-__global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) {
+template <MxType T, int RT, int NT, int TW, int KW>
+__global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const TileArgs A) {
+  constexpr int kWaves = kRowWaves * TW;             // of one share of K
+  constexpr int kXBytes = TW * NT * 32 * 128, kWBytes = kRowWaves * RT * 32 * 32;
+  constexpr int kStage = kXBytes + kWBytes;
+  constexpr int kSums = RT * NT * kWaves * 1024;     // a quarter of a share's sums
+  constexpr int kArray = KW == 1 || KW * kStage > kSums ? KW * kStage : kSums;
   // one array per stage: the compiler then knows which loads into LDS a read
   // of LDS can depend on
-  __shared__ __attribute__((aligned(16))) uint8_t xt0[NT * 32 * 128], xt1[NT * 32 * 128],
-      xt2[NT * 32 * 128], xt3[NT * 32 * 128];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  __shared__ __attribute__((aligned(16))) uint8_t xa0[kArray], xa1[kArray], xa2[kArray], xa3[kArray];
+  const int lane = threadIdx.x & 63;
+  const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = KW == 1 ? 0 : wave_all / kWaves, wave = KW == 1 ? wave_all : wave_all % kWaves;
+  const int rw = wave / TW, tw = wave % TW;
   const int l32 = lane & 31, h = lane >> 5;
   const int tiles = A.row_tiles * A.tok_tiles;
   const int job = xcd_tile((int)blockIdx.x, tiles * A.splits);
   // (uniform, but divisions run on the vector unit: back to scalar registers)
   const int split = __builtin_amdgcn_readfirstlane(job / tiles), tile = job - split * tiles;
   const int row_tile = __builtin_amdgcn_readfirstlane(tile / A.tok_tiles);
-  const int tok0 = (tile - row_tile * A.tok_tiles) * (32 * NT);
-  const int row0 = (row_tile * kWaves + wave) * (32 * RT);
+  const int tok0 = (tile - row_tile * A.tok_tiles) * (32 * NT * TW);
+  const int row0 = row_tile * (kRowWaves * 32 * RT);
   const int nb = A.cols >> 5;
-  const int g0 = split * A.groups_per_split;
-  const int g1 = min((nb + 7) >> 3, g0 + A.groups_per_split);
+
+  // K goes in groups of eight steps, 16 blocks. The groups of this split, and
+  // of those the wavefront's: each of the KW shares takes as many turns as the
+  // largest (past its end with zeros), so that all meet at every barrier.
+  const int s0 = split * A.groups_per_split, s1 = min((nb + 15) >> 4, s0 + A.groups_per_split);
+  const int share = (s1 - s0 + KW - 1) / KW;
+  const int g0 = s0 + kw * share, g1 = min(s1, g0 + share), gend = g0 + share;
 
   // resources that end with the tile's last row: rows past it read zero
   const uint32_t half = (uint32_t)A.cols >> 1;
-  const int wave_rows = __builtin_amdgcn_readfirstlane(max(0, min(32 * RT, A.rows - row0)));
-  const int tile_toks = __builtin_amdgcn_readfirstlane(min(32 * NT, A.batch - tok0));
-  const Rsrc crs = make_rsrc(A.codes + (int64_t)row0 * half, (uint32_t)wave_rows * half);
-  const Rsrc srs = make_rsrc(A.scales + (int64_t)row0 * nb, (uint32_t)wave_rows * nb);
+  const int tile_rows = __builtin_amdgcn_readfirstlane(min(kRowWaves * 32 * RT, A.rows - row0));
+  const int tile_toks = __builtin_amdgcn_readfirstlane(min(32 * NT * TW, A.batch - tok0));
+  const Rsrc crs = make_rsrc(A.codes + (int64_t)row0 * half, (uint32_t)tile_rows * half);
   const Rsrc xrs = make_rsrc(A.x + (int64_t)tok0 * A.cols, (uint32_t)tile_toks * A.cols * 2u);
 
   float16_t acc[RT][NT];
@@ -91,152 +107,223 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  // A step's activations, straight into LDS: each load of a wavefront fills 1
-  // KiB (eight rows) in lane order, so a chunk's place in its row is chosen by
-  // where the lane reads from. Chunks past the last block are zeros.
-  const int xrow = tid >> 3, xj = (tid & 7) ^ ((tid >> 4) & 7);
-  auto load_x = [&](int g, int u, uint8_t *dst) __attribute__((always_inline)) {
-    const int blk = 8 * g + u + (xj & 4);
-    const bool in = (g < g1) & (blk < nb);
+  // Step t (of group t / 8) into a stage. One load of a wavefront fills 1 KiB
+  // in lane order, eight rows of activations or 32 rows of codes, so a chunk's
+  // place in its row is chosen by where the lane reads from. Blocks past the
+  // last one are zeros. Wavefront w of the share makes loads w, w + kWaves, ..
+  constexpr int kXLoads = NT, kWLoads = (kRowWaves * RT + kWaves - 1) / kWaves;
+  constexpr bool kAllW = (kRowWaves * RT) % kWaves == 0;  // every wavefront loads codes
+  const int xrow = lane >> 3, wrow = lane >> 1;
+  auto fill = [&](int t, uint8_t *a) __attribute__((always_inline)) {
+    const bool run = t < 8 * g1;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const uint32_t off = (uint32_t)(xrow + 32 * i) * (uint32_t)A.cols * 2u + (uint32_t)blk * 64u +
-                           16u * (xj & 3);
+    for (int i = 0; i < kXLoads; ++i) {
+      const int c = wave + i * kWaves, r = 8 * c + xrow;
+      const int j = (lane & 7) ^ ((r >> 1) & 7);
+      const bool in = run & (2 * t + (j >> 2) < nb);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          xrs, (__attribute__((address_space(3))) void *)(dst + i * 4096 + wave * 1024), 16,
-          in ? off : kMxOOB, 0, 0, 0);
+          xrs, (__attribute__((address_space(3))) void *)(a + (kw * kStage + c * 1024)), 16,
+          in ? (uint32_t)r * (uint32_t)A.cols * 2u + (uint32_t)t * 128u + 16u * j : kMxOOB, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kWLoads; ++i) {
+      const int c = wave + i * kWaves, r = 32 * c + wrow;
+      const int j = (lane & 1) ^ ((r >> 3) & 1);
+      const bool in = run & (2 * t + j < nb);
+      if (kAllW || c < kRowWaves * RT)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            crs, (__attribute__((address_space(3))) void *)(a + (kw * kStage + kXBytes + c * 1024)), 16,
+            in ? (uint32_t)r * half + (uint32_t)t * 32u + 16u * j : kMxOOB, 0, 0, 0);
     }
   };
-  auto load_w = [&](int g, int u, uint4 (&wv)[RT]) __attribute__((always_inline)) {
-    const int blk = 8 * g + 4 * h + u;
-    const bool in = (g < g1) & (blk < nb);
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-      wv[i] = buf_load16(crs, in ? (32u * i + l32) * half + (uint32_t)blk * 16u : kMxOOB);
-  };
-  // The four scale bytes of a group. Past the last row or block the codes are
-  // zeros and the byte is that of the last one there is, so that it is one of
-  // this row (or of a row that is not stored) and needs no care: only a NaN
-  // would show, in a row that is NaN already.
+  // The 16 scale bytes of a group for the lane's rows. Past the last row they
+  // are those of the last one; past the last block they are those of the last
+  // block or 127. (The codes there are zeros; a NaN of another row would
+  // still show.)
+  const int my_rows = tile_rows - rw * 32 * RT;  // of this wavefront, where there are any
   uint32_t srow[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) srow[i] = (uint32_t)max(0, min(32 * i + l32, wave_rows - 1)) * nb;
-  const bool whole = (nb & 7) == 0;  // whole groups: every word aligned and inside its row
-  auto load_s = [&](int g, uint32_t (&sv)[RT]) __attribute__((always_inline)) {
-    const int blk = 8 * min(g, g1 - 1) + 4 * h;
-    if (whole) {
+  for (int i = 0; i < RT; ++i)
+    srow[i] = (uint32_t)max(0, min(rw * 32 * RT + 32 * i + l32, tile_rows - 1)) * nb;
+  const int base = (int)(((int64_t)row0 * nb) & 3);  // of the tile's scales within a word
+  const Rsrc srw = make_rsrc(A.scales + (int64_t)row0 * nb - base, (uint32_t)tile_rows * nb + base);
+  // Loaded a group ahead (load_s), put into place when their group begins
+  // (place_s), so that nothing waits for them meanwhile.
+  uint32_t extra[RT];
+  auto load_s = [&](int g, uint4 (&sv)[RT]) __attribute__((always_inline)) {
+    const int blk = 16 * max(0, min(g, g1 - 1)), left = nb - blk;
+    if ((nb & 3) == 0) {  // words lie whole in a row
 #pragma unroll
-      for (int i = 0; i < RT; ++i) sv[i] = buf_load4(srs, srow[i] + (uint32_t)blk);
+      for (int i = 0; i < RT; ++i) sv[i] = buf_load16(srw, srow[i] + (uint32_t)blk);
+    } else if (left >= 19) {  // five aligned words hold them, and end inside the row
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const uint32_t to = (srow[i] + (uint32_t)(blk + base)) & ~3u;
+        sv[i] = buf_load16(srw, to);
+        extra[i] = buf_load4(srw, to + 16);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         uint32_t v[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = buf_load_u8(srs, srow[i] + (uint32_t)min(blk + u, nb - 1));
-        sv[i] = v[0] | (v[1] << 8) | (v[2] << 16) | (v[3] << 24);
+        for (int u = 0; u < 4; ++u) {
+          v[u] = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[u] |= buf_load_u8(srw, srow[i] + (uint32_t)(base + min(blk + 4 * u + e, nb - 1))) << (8 * e);
+        }
+        sv[i] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+  };
+  auto place_s = [&](int g, uint4 (&sv)[RT]) __attribute__((always_inline)) {
+    const int blk = 16 * max(0, min(g, g1 - 1)), left = nb - blk;
+    if ((nb & 3) == 0) {
+      if (left < 16) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          if (left <= 12) sv[i].w = 0x7F7F7F7Fu;
+          if (left <= 8) sv[i].z = 0x7F7F7F7Fu;
+          if (left <= 4) sv[i].y = 0x7F7F7F7Fu;
+        }
+      }
+    } else if (left >= 19) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const uint32_t by = (srow[i] + (uint32_t)(blk + base)) & 3u;
+        sv[i].x = __builtin_amdgcn_alignbyte(sv[i].y, sv[i].x, by);
+        sv[i].y = __builtin_amdgcn_alignbyte(sv[i].z, sv[i].y, by);
+        sv[i].z = __builtin_amdgcn_alignbyte(sv[i].w, sv[i].z, by);
+        sv[i].w = __builtin_amdgcn_alignbyte(extra[i], sv[i].w, by);
       }
     }
   };
 
-  // One step. `X` holds its activations; `far` is the stage that the step
-  // before read and the third one from here reads. Before the barrier the
-  // wavefront waits for the next step's codes `w1` (the empty asm uses them):
-  // loads return in order, and those were asked for a step after the next
-  // step's activations, so these lie in LDS. The operand reads of this step
-  // have long returned, since products used them.
-  auto step = [&](auto wide_c, int g, auto u_c, const uint8_t *X, uint8_t *far,
-                  const uint4 (&wv)[RT], const uint32_t (&sv)[RT], uint4 (&w1)[RT], uint4 (&w2)[RT])
+  // (places of the lane's operands in a stage: 32 rows further on the
+  // permutation is the same)
+  const uint32_t wbase = kw * kStage + kXBytes + w_off(rw * 32 * RT + l32, h);
+  uint32_t xbase[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) xbase[s] = kw * kStage + x_off(tw * 32 * NT + l32, 4 * h + s);
+  auto w_of = [&](const uint8_t *a, int i) __attribute__((always_inline)) {
+    return *reinterpret_cast<const uint4 *>(a + (wbase + 1024u * i));
+  };
+  auto x_of = [&](const uint8_t *a, int j, int s) __attribute__((always_inline)) {
+    return *reinterpret_cast<const uint4 *>(a + (xbase[s] + 4096u * j));
+  };
+
+  // Step t, the U-th of its group, from stage `a`; `next` is the stage of step
+  // t + 1 and `far` the one that the step before read, filled for step t + 3.
+  // A step begins with its codes and first activation operands in registers:
+  // they are read at the end of the step before, so that products go on right
+  // after the barrier. Before the barrier the wavefront waits until at most
+  // its loads of step t + 3 are under way: loads complete in order, so behind
+  // the barrier all of step t + 2 lies in LDS. The operand reads of this step
+  // have returned, since products used them.
+  constexpr int kLoads = kXLoads + (kAllW ? kWLoads : 0);  // of a wavefront and step, at least
+  uint4 sc[RT], sn[RT];
+  uint4 w[2][RT], b[2][NT];
+  auto step = [&](auto wide_c, int t, auto u_c, const uint8_t *a, const uint8_t *next, uint8_t *far)
                   __attribute__((always_inline)) {
     constexpr bool WIDE = decltype(wide_c)::value;
     constexpr int U = decltype(u_c)::value;
-    load_w(U < 2 ? g : g + 1, (U + 2) & 3, w2);
-    load_x(U < 1 ? g : g + 1, (U + 3) & 3, far);
+    fill(t + 3, far);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (!WIDE) {
-      uint4 b[2][NT];
-      auto reads = [&](int s) __attribute__((always_inline)) {
+    float sv[RT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          b[s & 1][j] = *reinterpret_cast<const uint4 *>(X + x_off(32 * j + l32, 4 * h + s));
-      };
-      reads(0);
-      __builtin_amdgcn_sched_group_barrier(0x100, NT, 0);
+    for (int i = 0; i < RT; ++i) {
+      const uint32_t word = U < 2 ? sc[i].x : U < 4 ? sc[i].y : U < 6 ? sc[i].z : sc[i].w;
+      sv[i] = mx_scale((word >> (16 * (U & 1) + 8 * h)) & 0xFFu);
+    }
+    if constexpr (WIDE) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (s < 3) reads(s + 1);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
-          const uint4 a = mx_decode8<T>(ww[s], mx_scale((sv[i] >> (8 * U)) & 0xFFu));
-#pragma unroll
-          for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma32<T>(a, b[s & 1][j], acc[i][j]);
-        }
-        if (s < 3) {  // the next instruction's operands are read before this one's products
-          __builtin_amdgcn_sched_group_barrier(0x100, NT, 0);
-          __builtin_amdgcn_sched_group_barrier(0x008, RT * NT, 0);
-        }
-      }
-    } else {
-#pragma unroll 1
       for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           uint4 hi, lo;
-          split_f16(*reinterpret_cast<const uint4 *>(X + x_off(32 * j + l32, 4 * h + s)), hi, lo);
+          split_f16(x_of(a, j, s), hi, lo);
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
-            const uint32_t word = s == 0 ? wv[i].x : s == 1 ? wv[i].y : s == 2 ? wv[i].z : wv[i].w;
-            const uint4 a =
-                mx_decode8<MxType::kBF16>(word, mx_scale((sv[i] >> (8 * U)) & 0xFFu));
-            acc[i][j] = mx_mfma32<MxType::kBF16>(a, hi, acc[i][j]);
-            acc[i][j] = mx_mfma32<MxType::kBF16>(a, lo, acc[i][j]);
+            const uint32_t ww[4] = {w[U & 1][i].x, w[U & 1][i].y, w[U & 1][i].z, w[U & 1][i].w};
+            const uint4 av = mx_decode8<MxType::kBF16>(ww[s], sv[i]);
+            acc[i][j] = mx_mfma32<MxType::kBF16>(av, hi, acc[i][j]);
+            acc[i][j] = mx_mfma32<MxType::kBF16>(av, lo, acc[i][j]);
           }
         }
     }
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < RT; ++i) asm volatile("" : "+v"(w1[i].x) : : "memory");
+    for (int s = 0; s < 4; ++s) {
+      if (s == 3) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) w[(U + 1) & 1][i] = w_of(next, i);
+      }
+      if (s == 3 || !WIDE) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          b[(s + 1) & 1][j] = s < 3 ? x_of(a, j, s + 1) : x_of(next, j, 0);
+      }
+      if constexpr (!WIDE) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const uint32_t ww[4] = {w[U & 1][i].x, w[U & 1][i].y, w[U & 1][i].z, w[U & 1][i].w};
+          const uint4 av = mx_decode8<T>(ww[s], sv[i]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma32<T>(av, b[s & 1][j], acc[i][j]);
+        }
+        // the next instruction's operands are read before this one's products
+        if (s == 3) __builtin_amdgcn_sched_group_barrier(0x100, NT + RT, 0);
+        else __builtin_amdgcn_sched_group_barrier(0x100, NT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, RT * NT, 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kLoads) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" : : : "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  uint4 w[4][RT];
-  uint32_t sc[RT], sn[RT];
   load_s(g0, sc);
-  load_x(g0, 0, xt0);
+  place_s(g0, sc);
+  fill(8 * g0, xa0);
   __builtin_amdgcn_sched_barrier(0);
-  load_w(g0, 0, w[0]);
-  load_x(g0, 1, xt1);
+  fill(8 * g0 + 1, xa1);
   __builtin_amdgcn_sched_barrier(0);
-  load_w(g0, 1, w[1]);
-  load_x(g0, 2, xt2);
-#pragma unroll
-  for (int i = 0; i < RT; ++i) asm volatile("" : "+v"(w[0][i].x) : : "memory");
+  fill(8 * g0 + 2, xa2);
+  asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kLoads) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" : : : "memory");
-  typedef std::integral_constant<int, 0> U0;
-  typedef std::integral_constant<int, 1> U1;
-  typedef std::integral_constant<int, 2> U2;
-  typedef std::integral_constant<int, 3> U3;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) w[0][i] = w_of(xa0, i);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) b[0][j] = x_of(xa0, j, 0);
   auto group = [&](auto wide_c, int g) __attribute__((always_inline)) {
     load_s(g + 1, sn);
-    step(wide_c, g, U0{}, xt0, xt3, w[0], sc, w[1], w[2]);
-    step(wide_c, g, U1{}, xt1, xt0, w[1], sc, w[2], w[3]);
-    step(wide_c, g, U2{}, xt2, xt1, w[2], sc, w[3], w[0]);
-    step(wide_c, g, U3{}, xt3, xt2, w[3], sc, w[0], w[1]);
+    const int t = 8 * g;
+    step(wide_c, t, std::integral_constant<int, 0>{}, xa0, xa1, xa3);
+    step(wide_c, t + 1, std::integral_constant<int, 1>{}, xa1, xa2, xa0);
+    step(wide_c, t + 2, std::integral_constant<int, 2>{}, xa2, xa3, xa1);
+    step(wide_c, t + 3, std::integral_constant<int, 3>{}, xa3, xa0, xa2);
+    step(wide_c, t + 4, std::integral_constant<int, 4>{}, xa0, xa1, xa3);
+    step(wide_c, t + 5, std::integral_constant<int, 5>{}, xa1, xa2, xa0);
+    step(wide_c, t + 6, std::integral_constant<int, 6>{}, xa2, xa3, xa1);
+    step(wide_c, t + 7, std::integral_constant<int, 7>{}, xa3, xa0, xa2);
+    place_s(g + 1, sn);
 #pragma unroll
     for (int i = 0; i < RT; ++i) sc[i] = sn[i];
   };
   int g = g0;
-  for (; g < g1; ++g) {
+  for (; g < gend; ++g) {
     if constexpr (T == MxType::kF16) {
       bool f = true;
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int i = 0; i < RT; ++i) {
+        const uint32_t v[4] = {sc[i].x, sc[i].y, sc[i].z, sc[i].w};
 #pragma unroll
-        for (int u = 0; u < 4; ++u) f = f & mx_fits_f16((sc[i] >> (8 * u)) & 0xFFu);
-      if (!__all(f) & (wave_rows > 0)) break;
+        for (int u = 0; u < 16; ++u) f = f & mx_fits_f16((v[u >> 2] >> (8 * (u & 3))) & 0xFFu);
+      }
+      if (!__all(f) & (my_rows > 0)) break;
     }
     group(std::false_type{}, g);
   }
@@ -245,43 +332,81 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tile_kernel(const TileArgs A) 
   // exactly in two. The barriers are those of the other loop, one a step, so
   // wavefronts in either meet.
   if constexpr (T == MxType::kF16)
-    for (; g < g1; ++g) group(std::true_type{}, g);
+    for (; g < gend; ++g) group(std::true_type{}, g);
   // the zeros past the last group are in LDS before the wavefront can end
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 
+  // the shares' sums, added in order: a quarter of the registers per array
+  if constexpr (KW > 1) {
+    auto slot = [&](uint8_t *a, int i, int j) __attribute__((always_inline)) {
+      return reinterpret_cast<float4_t *>(a + ((i * NT + j) * kWaves + wave) * 1024) + lane;
+    };
+#pragma unroll 1
+    for (int s = 1; s < KW; ++s) {
+      __syncthreads();
+      if (kw == s) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              *slot(q == 0 ? xa0 : q == 1 ? xa1 : q == 2 ? xa2 : xa3, i, j) =
+                  float4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                           acc[i][j][4 * q + 3]};
+      }
+      __syncthreads();
+      if (kw == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const float4_t v = *slot(q == 0 ? xa0 : q == 1 ? xa1 : q == 2 ? xa2 : xa3, i, j);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+            }
+      }
+    }
+    if (kw != 0) return;
+  }
+
   // register 4 g + e of a 32 x 32 tile: row 8 g + 4 h + e, token l32
   if (A.splits > 1) {
-    float4_t *p = A.part + (int64_t)job * (RT * NT * 4 * kThreads) + tid;
+    constexpr int kThreads = 64 * kWaves;
+    float4_t *p = A.part + (int64_t)job * (RT * NT * 4 * kThreads) + wave * 64 + lane;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          p[((i * NT + j) * 4 + g) * kThreads] = float4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1],
-                                                          acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        for (int q = 0; q < 4; ++q)
+          p[((i * NT + j) * 4 + q) * kThreads] = float4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                          acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     return;
   }
   const bool packed = (A.rows & 3) == 0;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int tok = tok0 + 32 * j + l32;
+    const int tok = tok0 + tw * 32 * NT + 32 * j + l32;
     if (tok >= A.batch) continue;
     uint16_t *row = A.y + (int64_t)tok * A.rows;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        store4<T>(row, row0 + 32 * i + 8 * g + 4 * h, A.rows,
-                  float4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                           acc[i][j][4 * g + 3]},
+      for (int q = 0; q < 4; ++q)
+        store4<T>(row, row0 + rw * 32 * RT + 32 * i + 8 * q + 4 * h, A.rows,
+                  float4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                           acc[i][j][4 * q + 3]},
                   packed);
   }
 }
 
 // Sums of the split parts, in order of the split, rounded and stored.
-template <MxType T, int RT, int NT>
-__global__ __launch_bounds__(kThreads) void mx_tile_sum_kernel(const TileArgs A) {
+template <MxType T, int RT, int NT, int TW>
+__global__ __launch_bounds__(64 * kRowWaves * TW) void mx_tile_sum_kernel(const TileArgs A) {
+  constexpr int kThreads = 64 * kRowWaves * TW;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int tiles = A.row_tiles * A.tok_tiles;
   const int slot = (int)blockIdx.x % (RT * NT * 4), tile = (int)blockIdx.x / (RT * NT * 4);
@@ -289,61 +414,69 @@ __global__ __launch_bounds__(kThreads) void mx_tile_sum_kernel(const TileArgs A)
   const int64_t stride = (int64_t)tiles * (RT * NT * 4) * kThreads;
   float4_t v = p[0];
   for (int s = 1; s < A.splits; ++s) v += p[s * stride];
-  const int g = slot & 3, j = (slot >> 2) % NT, i = (slot >> 2) / NT;
+  const int q = slot & 3, j = (slot >> 2) % NT, i = (slot >> 2) / NT;
   const int row_tile = tile / A.tok_tiles;
-  const int tok = (tile - row_tile * A.tok_tiles) * (32 * NT) + 32 * j + (lane & 31);
-  const int row = (row_tile * kWaves + wave) * (32 * RT) + 32 * i + 8 * g + 4 * (lane >> 5);
+  const int tok = (tile - row_tile * A.tok_tiles) * (32 * NT * TW) + (wave % TW) * 32 * NT + 32 * j +
+                  (lane & 31);
+  const int row = row_tile * (kRowWaves * 32 * RT) + (wave / TW) * 32 * RT + 32 * i + 8 * q +
+                  4 * (lane >> 5);
   if (tok < A.batch) store4<T>(A.y + (int64_t)tok * A.rows, row, A.rows, v, (A.rows & 3) == 0);
 }
 
-// Tile of a product: rows of W per wavefront in units of 32, tokens in units
-// of 32, workgroups K is split over.
+// Tile of a product (RT, NT, TW, KW as above) and the workgroups K is split
+// over: the choice with the shortest modelled time. The grid runs in rounds of
+// up to 256 workgroups, one per CU, and a step of each share of K takes a + b *
+// (workgroups of the round / 256) us: fitted to 4096 x 4096, 4096 x 11008 and
+// 11008 x 4096 from 32 to 2048 rows. 4 us pass around the steps; a split writes
+// and reads its sums at about 4 TB/s and launches a second kernel.
 struct Plan {
-  int rt, nt, splits, groups_per_split;
+  int rt, nt, tw, kw, splits, groups_per_split;
   int64_t row_tiles, tok_tiles;
 };
 
 Plan plan_of(int64_t rows, int64_t cols, int64_t batch) {
-  Plan p;
-  p.nt = batch <= 32 ? 1 : batch <= 64 ? 2 : batch <= 96 ? 3 : 4;
-  p.rt = 2;
-  p.tok_tiles = (batch + 32 * p.nt - 1) / (32 * p.nt);
-  p.row_tiles = (rows + 32 * kWaves * p.rt - 1) / (32 * kWaves * p.rt);
-  if (p.row_tiles * p.tok_tiles < 256) {
-    p.rt = 1;
-    p.row_tiles = (rows + 32 * kWaves - 1) / (32 * kWaves);
+  static constexpr struct { int rt, nt, tw, kw; double a, b; } kTiles[] = {
+      {2, 2, 2, 1, 0.33, 0.61}, {1, 2, 1, 2, 0.30, 0.36}, {1, 1, 1, 2, 0.25, 0.18}};
+  const int64_t groups = (cols / 32 + 15) / 16;
+  Plan best{};
+  double least = 0;
+  for (const auto &c : kTiles) {
+    Plan p = {c.rt, c.nt, c.tw, c.kw, 1, 0, 0, 0};
+    p.row_tiles = (rows + 32 * kRowWaves * p.rt - 1) / (32 * kRowWaves * p.rt);
+    p.tok_tiles = (batch + 32 * p.nt * p.tw - 1) / (32 * p.nt * p.tw);
+    const int64_t tiles = p.row_tiles * p.tok_tiles;
+    for (int s = 1; s <= 8; ++s) {
+      p.groups_per_split = (int)((groups + s - 1) / s);
+      p.splits = (int)((groups + p.groups_per_split - 1) / p.groups_per_split);
+      if (p.splits != s || (s > 1 && tiles * s > 256)) break;
+      const double whole = (double)(tiles * s / 256), rest = (double)(tiles * s % 256) / 256.0;
+      const double step = whole * (c.a + c.b) + (rest > 0 ? c.a + c.b * rest : 0.0);
+      double us = 4.0 + (double)((p.groups_per_split + p.kw - 1) / p.kw) * 8.0 * step;
+      if (s > 1) us += 2.5 + (double)(tiles * s * (p.rt * p.nt * p.tw * kRowWaves)) * 8192.0 / 4e6;
+      if (best.rt == 0 || us < least) {
+        least = us;
+        best = p;
+      }
+    }
   }
-  const int64_t groups = (cols / 32 + 7) / 8, tiles = p.row_tiles * p.tok_tiles;
-  // about two workgroups per CU, at least two groups of K steps each
-  int64_t s = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, groups / 2));
-  if (tiles >= 192) s = 1;
-  p.groups_per_split = (int)((groups + s - 1) / s);
-  p.splits = (int)((groups + p.groups_per_split - 1) / p.groups_per_split);
-  return p;
+  return best;
 }
 
-template <MxType T, int RT, int NT>
+template <MxType T, int RT, int NT, int TW, int KW>
 hipError_t launch_tile(const TileArgs &A, hipStream_t stream) {
   const unsigned tiles = (unsigned)(A.row_tiles * A.tok_tiles);
-  hipLaunchKernelGGL((mx_tile_kernel<T, RT, NT>), dim3(tiles * A.splits), dim3(kThreads), 0, stream,
-                     A);
+  hipLaunchKernelGGL((mx_tile_kernel<T, RT, NT, TW, KW>), dim3(tiles * A.splits),
+                     dim3(64 * kRowWaves * TW * KW), 0, stream, A);
   if (A.splits > 1)
-    hipLaunchKernelGGL((mx_tile_sum_kernel<T, RT, NT>), dim3(tiles * RT * NT * 4), dim3(kThreads), 0,
-                       stream, A);
+    hipLaunchKernelGGL((mx_tile_sum_kernel<T, RT, NT, TW>), dim3(tiles * RT * NT * 4),
+                       dim3(64 * kRowWaves * TW), 0, stream, A);
   return hipGetLastError();
 }
 
 template <MxType T> hipError_t tile_as(const Plan &p, const TileArgs &A, hipStream_t stream) {
-  switch (p.rt * 8 + p.nt) {
-    case 9: return launch_tile<T, 1, 1>(A, stream);
-    case 10: return launch_tile<T, 1, 2>(A, stream);
-    case 11: return launch_tile<T, 1, 3>(A, stream);
-    case 12: return launch_tile<T, 1, 4>(A, stream);
-    case 17: return launch_tile<T, 2, 1>(A, stream);
-    case 18: return launch_tile<T, 2, 2>(A, stream);
-    case 19: return launch_tile<T, 2, 3>(A, stream);
-    default: return launch_tile<T, 2, 4>(A, stream);
-  }
+  if (p.rt == 2) return launch_tile<T, 2, 2, 2, 1>(A, stream);
+  if (p.nt == 2) return launch_tile<T, 1, 2, 1, 2>(A, stream);
+  return launch_tile<T, 1, 1, 1, 2>(A, stream);
 }
 
 }  // namespace
@@ -351,7 +484,7 @@ template <MxType T> hipError_t tile_as(const Plan &p, const TileArgs &A, hipStre
 int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch) {
   const Plan p = plan_of(W.rows, W.cols, batch);
   if (p.splits == 1) return 0;
-  return p.row_tiles * p.tok_tiles * p.splits * (int64_t)(p.rt * p.nt * 4 * kThreads) *
+  return p.row_tiles * p.tok_tiles * p.splits * (int64_t)(p.rt * p.nt * 4 * 64 * kRowWaves * p.tw) *
          (int64_t)sizeof(float4_t);
 }
 
