@@ -54,8 +54,9 @@ struct TileArgs {
 };
 
 // Workgroup -> tile. Workgroups go round the 8 XCDs in turn, each with an L2
-// of its own: give every XCD one run of consecutive tiles, tokens fastest, so
-// that the workgroups at work on an XCD share rows of W and steps of x.
+// of its own: give every XCD one run of consecutive tiles, which go through the
+// rows of W in bands of eight tiles of tokens, so that the workgroups at work on
+// an XCD (4 x 8 tiles of its 32 CUs) share both rows of W and steps of x.
 __device__ __forceinline__ int xcd_tile(int b, int n) {
   const int per = n >> 3, rest = n & 7, xcd = b & 7, i = b >> 3;
   return xcd * per + min(xcd, rest) + i;
@@ -80,8 +81,10 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
   const int job = xcd_tile((int)blockIdx.x, tiles * A.splits);
   // (uniform, but divisions run on the vector unit: back to scalar registers)
   const int split = __builtin_amdgcn_readfirstlane(job / tiles), tile = job - split * tiles;
-  const int row_tile = __builtin_amdgcn_readfirstlane(tile / A.tok_tiles);
-  const int tok0 = (tile - row_tile * A.tok_tiles) * (32 * NT * TW);
+  const int band = __builtin_amdgcn_readfirstlane(tile / (8 * A.row_tiles));
+  const int width = min(8, A.tok_tiles - 8 * band), in_band = tile - 8 * band * A.row_tiles;
+  const int row_tile = __builtin_amdgcn_readfirstlane(in_band / width);
+  const int tok0 = (8 * band + in_band - row_tile * width) * (32 * NT * TW);
   const int row0 = row_tile * (kRowWaves * 32 * RT);
   const int nb = A.cols >> 5;
 
@@ -415,8 +418,10 @@ __global__ __launch_bounds__(64 * kRowWaves * TW) void mx_tile_sum_kernel(const 
   float4_t v = p[0];
   for (int s = 1; s < A.splits; ++s) v += p[s * stride];
   const int q = slot & 3, j = (slot >> 2) % NT, i = (slot >> 2) / NT;
-  const int row_tile = tile / A.tok_tiles;
-  const int tok = (tile - row_tile * A.tok_tiles) * (32 * NT * TW) + (wave % TW) * 32 * NT + 32 * j +
+  const int band = tile / (8 * A.row_tiles), in_band = tile - 8 * band * A.row_tiles;
+  const int width = min(8, A.tok_tiles - 8 * band), row_tile = in_band / width;
+  const int tok_tile = 8 * band + in_band - row_tile * width;
+  const int tok = tok_tile * (32 * NT * TW) + (wave % TW) * 32 * NT + 32 * j +
                   (lane & 31);
   const int row = row_tile * (kRowWaves * 32 * RT) + (wave / TW) * 32 * RT + 32 * i + 8 * q +
                   4 * (lane >> 5);
