@@ -24,7 +24,8 @@ LIB_NAME = "libaqlm_mi355x.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ("api.hip", "dequant.hip", "gemv.hip", "gemv_mfma.hip", "gemv_slice.hip", "gemm.hip",
            "gemm_mid.hip", "gemm_tile.hip", "general.hip", "encode.hip", "mx_api.hip",
-           "mx_convert.hip", "mx_gemm.hip", "mx_gemm_tile.hip", "mx_gemm_mx.hip", "mx_grad.hip")
+           "mx_convert.hip", "mx_gemm.hip", "mx_gemm_tile.hip", "mx_gemm_mx.hip", "mx_gemm_mx_tile.hip",
+           "mx_grad.hip")
 ARCH = "gfx950"
 HOST_SOURCE = "host_gemv.cpp"
 HOST_LIB_PATH = os.path.join(PKG_DIR, "libaqlm_host.so")

@@ -99,16 +99,18 @@ hipError_t launch_skinny(const MxDesc &W, const MxDesc &x, void *y, hipStream_t 
 
 template <MxType T>
 hipError_t gemm_mx_as(const MxDesc &W, const MxDesc &x, void *y, hipStream_t stream) {
-  if (x.rows <= 16) return launch_skinny<T, 1, 1, 8>(W, x, y, stream);
-  return launch_skinny<T, 4, 4, 2>(W, x, y, stream);
+  return launch_skinny<T, 1, 1, 8>(W, x, y, stream);
 }
 
 }  // namespace
 
-int64_t mx_gemm_mx_ws_bytes(const MxDesc &, int64_t) { return 0; }
+int64_t mx_gemm_mx_ws_bytes(const MxDesc &W, int64_t batch) {
+  return batch < kMxTileBatch ? 0 : mx_gemm_mx_tile_ws_bytes(W, batch);
+}
 
-hipError_t launch_mx_gemm_mx(const MxDesc &W, const MxDesc &x, void *y, MxType type, void *,
+hipError_t launch_mx_gemm_mx(const MxDesc &W, const MxDesc &x, void *y, MxType type, void *ws,
                              hipStream_t stream) {
+  if (x.rows >= kMxTileBatch) return launch_mx_gemm_mx_tile(W, x, y, type, ws, stream);
   return type == MxType::kF16 ? gemm_mx_as<MxType::kF16>(W, x, y, stream)
                               : gemm_mx_as<MxType::kBF16>(W, x, y, stream);
 }

@@ -27,12 +27,10 @@
 //     kernel adds them in a fixed order.
 #include <algorithm>
 
-#include "mx_device.hpp"
+#include "mx_tile.hpp"
 
 namespace aqlm {
 namespace {
-
-constexpr int kRowWaves = 4;
 
 // Byte offset of 16-byte chunk j (of 8) of activation row t in a stage.
 __device__ __forceinline__ uint32_t x_off(int t, int j) {
@@ -43,31 +41,12 @@ __device__ __forceinline__ uint32_t w_off(int r, int h) {
   return (uint32_t)r * 32u + (uint32_t)((h ^ ((r >> 3) & 1)) << 4);
 }
 
-struct TileArgs {
-  const uint8_t *codes;
-  const uint8_t *scales;
-  const uint16_t *x;
-  uint16_t *y;
-  float4_t *part;  // [splits][tiles][RT * NT * 4][threads], or null
-  int rows, cols, batch;
-  int row_tiles, tok_tiles, splits, groups_per_split;
-};
-
-// Workgroup -> tile. Workgroups go round the 8 XCDs in turn, each with an L2
-// of its own: give every XCD one run of consecutive tiles, which go through the
-// rows of W in bands of eight tiles of tokens, so that the workgroups at work on
-// an XCD (4 x 8 tiles of its 32 CUs) share both rows of W and steps of x.
-__device__ __forceinline__ int xcd_tile(int b, int n) {
-  const int per = n >> 3, rest = n & 7, xcd = b & 7, i = b >> 3;
-  return xcd * per + min(xcd, rest) + i;
-}
-
 template <MxType T, int RT, int NT, int TW, int KW>
 __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const TileArgs A) {
   constexpr int kWaves = kRowWaves * TW;             // of one share of K
   constexpr int kXBytes = TW * NT * 32 * 128, kWBytes = kRowWaves * RT * 32 * 32;
   constexpr int kStage = kXBytes + kWBytes;
-  constexpr int kSums = RT * NT * kWaves * 1024;     // a quarter of a share's sums
+  constexpr int kSums = tile_sums_bytes<RT, NT, TW>();
   constexpr int kArray = KW == 1 || KW * kStage > kSums ? KW * kStage : kSums;
   // one array per stage: the compiler then knows which loads into LDS a read
   // of LDS can depend on
@@ -78,14 +57,10 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
   const int rw = wave / TW, tw = wave % TW;
   const int l32 = lane & 31, h = lane >> 5;
   const int tiles = A.row_tiles * A.tok_tiles;
-  const int job = xcd_tile((int)blockIdx.x, tiles * A.splits);
-  // (uniform, but divisions run on the vector unit: back to scalar registers)
-  const int split = __builtin_amdgcn_readfirstlane(job / tiles), tile = job - split * tiles;
-  const int band = __builtin_amdgcn_readfirstlane(tile / (8 * A.row_tiles));
-  const int width = min(8, A.tok_tiles - 8 * band), in_band = tile - 8 * band * A.row_tiles;
-  const int row_tile = __builtin_amdgcn_readfirstlane(in_band / width);
-  const int tok0 = (8 * band + in_band - row_tile * width) * (32 * NT * TW);
-  const int row0 = row_tile * (kRowWaves * 32 * RT);
+  const int job = xcd_job((int)blockIdx.x, tiles * A.splits);
+  const int split = __builtin_amdgcn_readfirstlane(job / tiles);
+  const TilePlace at = tile_place(job - split * tiles, A.row_tiles, A.tok_tiles);
+  const int row0 = at.row_tile * (kRowWaves * 32 * RT), tok0 = at.tok_tile * (32 * NT * TW);
   const int nb = A.cols >> 5;
 
   // K goes in groups of eight steps, 16 blocks. The groups of this split, and
@@ -100,7 +75,8 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
   const int tile_rows = __builtin_amdgcn_readfirstlane(min(kRowWaves * 32 * RT, A.rows - row0));
   const int tile_toks = __builtin_amdgcn_readfirstlane(min(32 * NT * TW, A.batch - tok0));
   const Rsrc crs = make_rsrc(A.codes + (int64_t)row0 * half, (uint32_t)tile_rows * half);
-  const Rsrc xrs = make_rsrc(A.x + (int64_t)tok0 * A.cols, (uint32_t)tile_toks * A.cols * 2u);
+  const Rsrc xrs = make_rsrc(static_cast<const uint16_t *>(A.x) + (int64_t)tok0 * A.cols,
+                             (uint32_t)tile_toks * A.cols * 2u);
 
   float16_t acc[RT][NT];
 #pragma unroll
@@ -139,69 +115,9 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
             in ? (uint32_t)r * half + (uint32_t)t * 32u + 16u * j : kMxOOB, 0, 0, 0);
     }
   };
-  // The 16 scale bytes of a group for the lane's rows. Past the last row they
-  // are those of the last one; past the last block they are those of the last
-  // block or 127. (The codes there are zeros; a NaN of another row would
-  // still show.)
   const int my_rows = tile_rows - rw * 32 * RT;  // of this wavefront, where there are any
-  uint32_t srow[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-    srow[i] = (uint32_t)max(0, min(rw * 32 * RT + 32 * i + l32, tile_rows - 1)) * nb;
-  const int base = (int)(((int64_t)row0 * nb) & 3);  // of the tile's scales within a word
-  const Rsrc srw = make_rsrc(A.scales + (int64_t)row0 * nb - base, (uint32_t)tile_rows * nb + base);
-  // Loaded a group ahead (load_s), put into place when their group begins
-  // (place_s), so that nothing waits for them meanwhile.
-  uint32_t extra[RT];
-  auto load_s = [&](int g, uint4 (&sv)[RT]) __attribute__((always_inline)) {
-    const int blk = 16 * max(0, min(g, g1 - 1)), left = nb - blk;
-    if ((nb & 3) == 0) {  // words lie whole in a row
-#pragma unroll
-      for (int i = 0; i < RT; ++i) sv[i] = buf_load16(srw, srow[i] + (uint32_t)blk);
-    } else if (left >= 19) {  // five aligned words hold them, and end inside the row
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const uint32_t to = (srow[i] + (uint32_t)(blk + base)) & ~3u;
-        sv[i] = buf_load16(srw, to);
-        extra[i] = buf_load4(srw, to + 16);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        uint32_t v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          v[u] = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[u] |= buf_load_u8(srw, srow[i] + (uint32_t)(base + min(blk + 4 * u + e, nb - 1))) << (8 * e);
-        }
-        sv[i] = make_uint4(v[0], v[1], v[2], v[3]);
-      }
-    }
-  };
-  auto place_s = [&](int g, uint4 (&sv)[RT]) __attribute__((always_inline)) {
-    const int blk = 16 * max(0, min(g, g1 - 1)), left = nb - blk;
-    if ((nb & 3) == 0) {
-      if (left < 16) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          if (left <= 12) sv[i].w = 0x7F7F7F7Fu;
-          if (left <= 8) sv[i].z = 0x7F7F7F7Fu;
-          if (left <= 4) sv[i].y = 0x7F7F7F7Fu;
-        }
-      }
-    } else if (left >= 19) {
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const uint32_t by = (srow[i] + (uint32_t)(blk + base)) & 3u;
-        sv[i].x = __builtin_amdgcn_alignbyte(sv[i].y, sv[i].x, by);
-        sv[i].y = __builtin_amdgcn_alignbyte(sv[i].z, sv[i].y, by);
-        sv[i].z = __builtin_amdgcn_alignbyte(sv[i].w, sv[i].z, by);
-        sv[i].w = __builtin_amdgcn_alignbyte(extra[i], sv[i].w, by);
-      }
-    }
-  };
+  ScaleRows<RT> scales(A.scales, row0, tile_rows, nb, rw * 32 * RT + l32);
+  auto group_at = [&](int g) __attribute__((always_inline)) { return max(0, min(g, g1 - 1)); };
 
   // (places of the lane's operands in a stage: 32 rows further on the
   // permutation is the same)
@@ -287,8 +203,8 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  load_s(g0, sc);
-  place_s(g0, sc);
+  scales.load(group_at(g0), sc);
+  scales.place(group_at(g0), sc);
   fill(8 * g0, xa0);
   __builtin_amdgcn_sched_barrier(0);
   fill(8 * g0 + 1, xa1);
@@ -302,7 +218,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
 #pragma unroll
   for (int j = 0; j < NT; ++j) b[0][j] = x_of(xa0, j, 0);
   auto group = [&](auto wide_c, int g) __attribute__((always_inline)) {
-    load_s(g + 1, sn);
+    scales.load(group_at(g + 1), sn);
     const int t = 8 * g;
     step(wide_c, t, std::integral_constant<int, 0>{}, xa0, xa1, xa3);
     step(wide_c, t + 1, std::integral_constant<int, 1>{}, xa1, xa2, xa0);
@@ -312,7 +228,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
     step(wide_c, t + 5, std::integral_constant<int, 5>{}, xa1, xa2, xa0);
     step(wide_c, t + 6, std::integral_constant<int, 6>{}, xa2, xa3, xa1);
     step(wide_c, t + 7, std::integral_constant<int, 7>{}, xa3, xa0, xa2);
-    place_s(g + 1, sn);
+    scales.place(group_at(g + 1), sn);
 #pragma unroll
     for (int i = 0; i < RT; ++i) sc[i] = sn[i];
   };
@@ -339,132 +255,16 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
   // the zeros past the last group are in LDS before the wavefront can end
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 
-  // the shares' sums, added in order: a quarter of the registers per array
-  if constexpr (KW > 1) {
-    auto slot = [&](uint8_t *a, int i, int j) __attribute__((always_inline)) {
-      return reinterpret_cast<float4_t *>(a + ((i * NT + j) * kWaves + wave) * 1024) + lane;
-    };
-#pragma unroll 1
-    for (int s = 1; s < KW; ++s) {
-      __syncthreads();
-      if (kw == s) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              *slot(q == 0 ? xa0 : q == 1 ? xa1 : q == 2 ? xa2 : xa3, i, j) =
-                  float4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                           acc[i][j][4 * q + 3]};
-      }
-      __syncthreads();
-      if (kw == 0) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const float4_t v = *slot(q == 0 ? xa0 : q == 1 ? xa1 : q == 2 ? xa2 : xa3, i, j);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
-            }
-      }
-    }
-    if (kw != 0) return;
-  }
-
-  // register 4 g + e of a 32 x 32 tile: row 8 g + 4 h + e, token l32
-  if (A.splits > 1) {
-    constexpr int kThreads = 64 * kWaves;
-    float4_t *p = A.part + (int64_t)job * (RT * NT * 4 * kThreads) + wave * 64 + lane;
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          p[((i * NT + j) * 4 + q) * kThreads] = float4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1],
-                                                          acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-    return;
-  }
-  const bool packed = (A.rows & 3) == 0;
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int tok = tok0 + tw * 32 * NT + 32 * j + l32;
-    if (tok >= A.batch) continue;
-    uint16_t *row = A.y + (int64_t)tok * A.rows;
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        store4<T>(row, row0 + rw * 32 * RT + 32 * i + 8 * q + 4 * h, A.rows,
-                  float4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                           acc[i][j][4 * q + 3]},
-                  packed);
-  }
+  if (add_shares<RT, NT, TW, KW>(acc, kw, wave, lane, xa0, xa1, xa2, xa3)) return;
+  store_tile<T, RT, NT, TW>(A, acc, job, at, wave, lane);
 }
 
-// Sums of the split parts, in order of the split, rounded and stored.
-template <MxType T, int RT, int NT, int TW>
-__global__ __launch_bounds__(64 * kRowWaves * TW) void mx_tile_sum_kernel(const TileArgs A) {
-  constexpr int kThreads = 64 * kRowWaves * TW;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tiles = A.row_tiles * A.tok_tiles;
-  const int slot = (int)blockIdx.x % (RT * NT * 4), tile = (int)blockIdx.x / (RT * NT * 4);
-  const float4_t *p = A.part + ((int64_t)tile * (RT * NT * 4) + slot) * kThreads + tid;
-  const int64_t stride = (int64_t)tiles * (RT * NT * 4) * kThreads;
-  float4_t v = p[0];
-  for (int s = 1; s < A.splits; ++s) v += p[s * stride];
-  const int q = slot & 3, j = (slot >> 2) % NT, i = (slot >> 2) / NT;
-  const int band = tile / (8 * A.row_tiles), in_band = tile - 8 * band * A.row_tiles;
-  const int width = min(8, A.tok_tiles - 8 * band), row_tile = in_band / width;
-  const int tok_tile = 8 * band + in_band - row_tile * width;
-  const int tok = tok_tile * (32 * NT * TW) + (wave % TW) * 32 * NT + 32 * j +
-                  (lane & 31);
-  const int row = row_tile * (kRowWaves * 32 * RT) + (wave / TW) * 32 * RT + 32 * i + 8 * q +
-                  4 * (lane >> 5);
-  if (tok < A.batch) store4<T>(A.y + (int64_t)tok * A.rows, row, A.rows, v, (A.rows & 3) == 0);
-}
+// Fitted to 4096 x 4096, 4096 x 11008 and 11008 x 4096 from 32 to 2048 rows.
+constexpr TileShape kShapes[] = {
+    {2, 2, 2, 1, 2.64, 4.88}, {1, 2, 1, 2, 2.40, 2.88}, {1, 1, 1, 2, 2.00, 1.44}};
 
-// Tile of a product (RT, NT, TW, KW as above) and the workgroups K is split
-// over: the choice with the shortest modelled time. The grid runs in rounds of
-// up to 256 workgroups, one per CU, and a step of each share of K takes a + b *
-// (workgroups of the round / 256) us: fitted to 4096 x 4096, 4096 x 11008 and
-// 11008 x 4096 from 32 to 2048 rows. 4 us pass around the steps; a split writes
-// and reads its sums at about 4 TB/s and launches a second kernel.
-struct Plan {
-  int rt, nt, tw, kw, splits, groups_per_split;
-  int64_t row_tiles, tok_tiles;
-};
-
-Plan plan_of(int64_t rows, int64_t cols, int64_t batch) {
-  static constexpr struct { int rt, nt, tw, kw; double a, b; } kTiles[] = {
-      {2, 2, 2, 1, 0.33, 0.61}, {1, 2, 1, 2, 0.30, 0.36}, {1, 1, 1, 2, 0.25, 0.18}};
-  const int64_t groups = (cols / 32 + 15) / 16;
-  Plan best{};
-  double least = 0;
-  for (const auto &c : kTiles) {
-    Plan p = {c.rt, c.nt, c.tw, c.kw, 1, 0, 0, 0};
-    p.row_tiles = (rows + 32 * kRowWaves * p.rt - 1) / (32 * kRowWaves * p.rt);
-    p.tok_tiles = (batch + 32 * p.nt * p.tw - 1) / (32 * p.nt * p.tw);
-    const int64_t tiles = p.row_tiles * p.tok_tiles;
-    for (int s = 1; s <= 8; ++s) {
-      p.groups_per_split = (int)((groups + s - 1) / s);
-      p.splits = (int)((groups + p.groups_per_split - 1) / p.groups_per_split);
-      if (p.splits != s || (s > 1 && tiles * s > 256)) break;
-      const double whole = (double)(tiles * s / 256), rest = (double)(tiles * s % 256) / 256.0;
-      const double step = whole * (c.a + c.b) + (rest > 0 ? c.a + c.b * rest : 0.0);
-      double us = 4.0 + (double)((p.groups_per_split + p.kw - 1) / p.kw) * 8.0 * step;
-      if (s > 1) us += 2.5 + (double)(tiles * s * (p.rt * p.nt * p.tw * kRowWaves)) * 8192.0 / 4e6;
-      if (best.rt == 0 || us < least) {
-        least = us;
-        best = p;
-      }
-    }
-  }
-  return best;
+TilePlan plan_of(const MxDesc &W, int64_t batch) {
+  return plan_tiles(kShapes, W.rows, batch, (W.cols / 32 + 15) / 16);
 }
 
 template <MxType T, int RT, int NT, int TW, int KW>
@@ -478,39 +278,22 @@ hipError_t launch_tile(const TileArgs &A, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <MxType T> hipError_t tile_as(const Plan &p, const TileArgs &A, hipStream_t stream) {
-  if (p.rt == 2) return launch_tile<T, 2, 2, 2, 1>(A, stream);
-  if (p.nt == 2) return launch_tile<T, 1, 2, 1, 2>(A, stream);
+template <MxType T> hipError_t tile_as(const TileShape &c, const TileArgs &A, hipStream_t stream) {
+  if (c.rt == 2) return launch_tile<T, 2, 2, 2, 1>(A, stream);
+  if (c.nt == 2) return launch_tile<T, 1, 2, 1, 2>(A, stream);
   return launch_tile<T, 1, 1, 1, 2>(A, stream);
 }
 
 }  // namespace
 
-int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch) {
-  const Plan p = plan_of(W.rows, W.cols, batch);
-  if (p.splits == 1) return 0;
-  return p.row_tiles * p.tok_tiles * p.splits * (int64_t)(p.rt * p.nt * 4 * 64 * kRowWaves * p.tw) *
-         (int64_t)sizeof(float4_t);
-}
+int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch) { return plan_of(W, batch).ws_bytes(); }
 
 hipError_t launch_mx_gemm_tile(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
                                void *ws, hipStream_t stream) {
-  const Plan p = plan_of(W.rows, W.cols, batch);
-  TileArgs A;
-  A.codes = W.codes;
-  A.scales = W.scales;
-  A.x = static_cast<const uint16_t *>(x);
-  A.y = static_cast<uint16_t *>(y);
-  A.part = static_cast<float4_t *>(ws);
-  A.rows = (int)W.rows;
-  A.cols = (int)W.cols;
-  A.batch = (int)batch;
-  A.row_tiles = (int)p.row_tiles;
-  A.tok_tiles = (int)p.tok_tiles;
-  A.splits = p.splits;
-  A.groups_per_split = p.groups_per_split;
-  return type == MxType::kF16 ? tile_as<MxType::kF16>(p, A, stream)
-                              : tile_as<MxType::kBF16>(p, A, stream);
+  const TilePlan p = plan_of(W, batch);
+  const TileArgs A = tile_args(p, W, x, nullptr, batch, y, ws);
+  return type == MxType::kF16 ? tile_as<MxType::kF16>(p.shape, A, stream)
+                              : tile_as<MxType::kBF16>(p.shape, A, stream);
 }
 
 }  // namespace aqlm

@@ -29,7 +29,7 @@ hipError_t launch_mx_gemv_batched(const MxDesc *W, const void *const *x, void *c
 int64_t mx_gemm_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_gemm(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
                           void *ws, hipStream_t stream);
-// From kMxTileBatch rows on (mx_gemm_tile.hip).
+// From kMxTileBatch rows on (mx_gemm_tile.hip, mx_gemm_mx_tile.hip).
 constexpr int kMxTileBatch = 17;
 int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_gemm_tile(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
@@ -37,6 +37,9 @@ hipError_t launch_mx_gemm_tile(const MxDesc &W, const void *x, int64_t batch, vo
 int64_t mx_gemm_mx_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_gemm_mx(const MxDesc &W, const MxDesc &x, void *y, MxType type, void *ws,
                              hipStream_t stream);
+int64_t mx_gemm_mx_tile_ws_bytes(const MxDesc &W, int64_t batch);
+hipError_t launch_mx_gemm_mx_tile(const MxDesc &W, const MxDesc &x, void *y, MxType type, void *ws,
+                                  hipStream_t stream);
 int64_t mx_grad_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_grad(const MxDesc &W, const void *dy, int64_t batch, void *dx, MxType type,
                           void *ws, hipStream_t stream);

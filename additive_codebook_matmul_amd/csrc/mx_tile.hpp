@@ -1,0 +1,271 @@
+// What the tile kernels of microscaled products share: one workgroup per
+// [rows] x [tokens] tile of the result, 32 x 32 matrix instructions, K split
+// over wavefronts (KW shares) and over workgroups.
+//
+// A tile is kRowWaves wavefronts along the rows (32 RT each) times TW along the
+// tokens (32 NT each); each of the KW shares of K has such a set of them.
+#pragma once
+
+#include "mx_device.hpp"
+
+namespace aqlm {
+
+constexpr int kRowWaves = 4;
+
+struct TileArgs {
+  const uint8_t *codes;    // W
+  const uint8_t *scales;
+  const void *x;           // activations: halves, or codes
+  const uint8_t *xscales;  // and their scales
+  uint16_t *y;
+  float4_t *part;          // [splits][tiles][RT * NT * 4][64 kRowWaves TW], or null
+  int rows, cols, batch;   // of W and x (the result is [batch][rows])
+  int row_tiles, tok_tiles, splits, groups_per_split;
+};
+
+// Workgroup -> job. Workgroups go round the 8 XCDs in turn, each with an L2 of
+// its own: give every XCD one run of consecutive jobs.
+__device__ __forceinline__ int xcd_job(int b, int n) {
+  const int per = n >> 3, rest = n & 7, xcd = b & 7, i = b >> 3;
+  return xcd * per + min(xcd, rest) + i;
+}
+
+// Tile -> place. Tiles go through the rows in bands of eight tiles of tokens,
+// so that the workgroups at work on an XCD (4 x 8 tiles of its 32 CUs) share
+// both rows of W and steps of x. (Uniform, but divisions run on the vector
+// unit: the results go back to scalar registers.)
+struct TilePlace {
+  int row_tile, tok_tile;
+};
+__device__ __forceinline__ TilePlace tile_place(int tile, int row_tiles, int tok_tiles) {
+  const int band = __builtin_amdgcn_readfirstlane(tile / (8 * row_tiles));
+  const int width = min(8, tok_tiles - 8 * band), in_band = tile - 8 * band * row_tiles;
+  const int row_tile = __builtin_amdgcn_readfirstlane(in_band / width);
+  return {row_tile, 8 * band + in_band - row_tile * width};
+}
+
+// The scale bytes of N rows of a lane, 16 blocks (a group) at a time. Past the
+// last row they are those of the last one; past the last block they are those
+// of the last block or 127. (The codes there are zeros, but a NaN of another
+// row would still show.) Loaded a group ahead (load), put into place when their
+// group begins (place), so that nothing waits for them meanwhile.
+template <int N> struct ScaleRows {
+  Rsrc rs;
+  int nb, base;  // blocks of a row; the tile's first byte within its word
+  uint32_t at[N], extra[N];
+
+  // rows row0 .. row0 + rows - 1 of a matrix; `mine` of the tile's rows is the
+  // lane's first, the others follow every 32
+  __device__ __forceinline__ ScaleRows(const uint8_t *scales, int64_t row0, int rows, int nb_, int mine)
+      : nb(nb_) {
+    base = (int)((row0 * nb) & 3);
+    rs = make_rsrc(scales + row0 * nb - base, (uint32_t)rows * nb + base);
+#pragma unroll
+    for (int i = 0; i < N; ++i) at[i] = (uint32_t)max(0, min(mine + 32 * i, rows - 1)) * nb + base;
+  }
+  __device__ __forceinline__ void load(int group, uint4 (&sv)[N]) {
+    const int blk = 16 * group, left = nb - blk;
+    if ((nb & 3) == 0) {  // words lie whole in a row
+#pragma unroll
+      for (int i = 0; i < N; ++i) sv[i] = buf_load16(rs, at[i] + (uint32_t)blk);
+    } else if (left >= 19) {  // five aligned words hold them, and end inside the row
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t to = (at[i] + (uint32_t)blk) & ~3u;
+        sv[i] = buf_load16(rs, to);
+        extra[i] = buf_load4(rs, to + 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        uint32_t v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          v[u] = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[u] |= buf_load_u8(rs, at[i] + (uint32_t)min(blk + 4 * u + e, nb - 1)) << (8 * e);
+        }
+        sv[i] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+  }
+  __device__ __forceinline__ void place(int group, uint4 (&sv)[N]) {
+    const int blk = 16 * group, left = nb - blk;
+    if ((nb & 3) == 0) {
+      if (left < 16) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (left <= 12) sv[i].w = 0x7F7F7F7Fu;
+          if (left <= 8) sv[i].z = 0x7F7F7F7Fu;
+          if (left <= 4) sv[i].y = 0x7F7F7F7Fu;
+        }
+      }
+    } else if (left >= 19) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t by = (at[i] + (uint32_t)blk) & 3u;
+        sv[i].x = __builtin_amdgcn_alignbyte(sv[i].y, sv[i].x, by);
+        sv[i].y = __builtin_amdgcn_alignbyte(sv[i].z, sv[i].y, by);
+        sv[i].z = __builtin_amdgcn_alignbyte(sv[i].w, sv[i].z, by);
+        sv[i].w = __builtin_amdgcn_alignbyte(extra[i], sv[i].w, by);
+      }
+    }
+  }
+};
+
+// Registers 4 q .. 4 q + 3 of a 32 x 32 tile.
+__device__ __forceinline__ float4_t quarter(const float16_t &v, int q) {
+  return float4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+}
+
+// LDS bytes of one of the four arrays through which the shares' sums pass.
+template <int RT, int NT, int TW> constexpr int tile_sums_bytes() { return RT * NT * TW * kRowWaves * 1024; }
+
+// Adds the sums of K's shares, in order, to those of share 0: a quarter of the
+// registers through each array. True where the wavefront is done (it is not of
+// share 0).
+template <int RT, int NT, int TW, int KW>
+__device__ __forceinline__ bool add_shares(float16_t (&acc)[RT][NT], int kw, int wave, int lane,
+                                           uint8_t *a0, uint8_t *a1, uint8_t *a2, uint8_t *a3) {
+  if constexpr (KW > 1) {
+    auto slot = [&](uint8_t *a, int i, int j) __attribute__((always_inline)) {
+      return reinterpret_cast<float4_t *>(a + (((i * NT + j) * kRowWaves * TW + wave) * 64 + lane) * 16);
+    };
+#pragma unroll 1
+    for (int s = 1; s < KW; ++s) {
+      __syncthreads();
+      if (kw == s) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              *slot(q == 0 ? a0 : q == 1 ? a1 : q == 2 ? a2 : a3, i, j) = quarter(acc[i][j], q);
+      }
+      __syncthreads();
+      if (kw == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const float4_t v = *slot(q == 0 ? a0 : q == 1 ? a1 : q == 2 ? a2 : a3, i, j);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+            }
+      }
+    }
+    return kw != 0;
+  }
+  return false;
+}
+
+// The tile's results: to the workspace as the registers lie where K is split
+// over workgroups, else rounded into y. Register 4 q + e of a 32 x 32 tile is
+// row 8 q + 4 (lane / 32) + e, token lane % 32.
+template <MxType T, int RT, int NT, int TW>
+__device__ __forceinline__ void store_tile(const TileArgs &A, const float16_t (&acc)[RT][NT], int job,
+                                           const TilePlace &at, int wave, int lane) {
+  constexpr int kThreads = 64 * kRowWaves * TW;
+  if (A.splits > 1) {
+    float4_t *p = A.part + (int64_t)job * (RT * NT * 4 * kThreads) + wave * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) p[((i * NT + j) * 4 + q) * kThreads] = quarter(acc[i][j], q);
+    return;
+  }
+  const int rw = wave / TW, tw = wave % TW;
+  const bool packed = (A.rows & 3) == 0;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int tok = (at.tok_tile * TW + tw) * 32 * NT + 32 * j + (lane & 31);
+    if (tok >= A.batch) continue;
+    uint16_t *row = A.y + (int64_t)tok * A.rows;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        store4<T>(row, (at.row_tile * kRowWaves + rw) * 32 * RT + 32 * i + 8 * q + 4 * (lane >> 5),
+                  A.rows, quarter(acc[i][j], q), packed);
+  }
+}
+
+// Sums of the split parts, in order of the split, rounded and stored.
+template <MxType T, int RT, int NT, int TW>
+__global__ __launch_bounds__(64 * kRowWaves * TW) void mx_tile_sum_kernel(const TileArgs A) {
+  constexpr int kThreads = 64 * kRowWaves * TW;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tiles = A.row_tiles * A.tok_tiles;
+  const int slot = (int)blockIdx.x % (RT * NT * 4), tile = (int)blockIdx.x / (RT * NT * 4);
+  const float4_t *p = A.part + ((int64_t)tile * (RT * NT * 4) + slot) * kThreads + tid;
+  const int64_t stride = (int64_t)tiles * (RT * NT * 4) * kThreads;
+  float4_t v = p[0];
+  for (int s = 1; s < A.splits; ++s) v += p[s * stride];
+  const TilePlace at = tile_place(tile, A.row_tiles, A.tok_tiles);
+  const int q = slot & 3, j = (slot >> 2) % NT, i = (slot >> 2) / NT;
+  const int tok = (at.tok_tile * TW + wave % TW) * 32 * NT + 32 * j + (lane & 31);
+  const int row = (at.row_tile * kRowWaves + wave / TW) * 32 * RT + 32 * i + 8 * q + 4 * (lane >> 5);
+  if (tok < A.batch) store4<T>(A.y + (int64_t)tok * A.rows, row, A.rows, v, (A.rows & 3) == 0);
+}
+
+// Tile of a product and the workgroups K is split over: the choice with the
+// shortest modelled time. The grid runs in rounds of up to 256 workgroups, one
+// per CU, and a group of K takes a + b * (workgroups of the round / 256) us for
+// each share; 4 us pass around that; a split writes and reads its sums at about
+// 4 TB/s and launches a second kernel.
+struct TileShape {
+  int rt, nt, tw, kw;
+  double a, b;
+};
+
+struct TilePlan {
+  TileShape shape;
+  int splits, groups_per_split;
+  int64_t row_tiles, tok_tiles;
+  int64_t ws_bytes() const {
+    if (splits == 1) return 0;
+    return row_tiles * tok_tiles * splits * (int64_t)(shape.rt * shape.nt * shape.tw * kRowWaves) * 4096;
+  }
+};
+
+template <int N>
+TilePlan plan_tiles(const TileShape (&shapes)[N], int64_t rows, int64_t batch, int64_t groups) {
+  TilePlan best{};
+  double least = 0;
+  for (const TileShape &c : shapes) {
+    TilePlan p{};
+    p.shape = c;
+    p.row_tiles = (rows + 32 * kRowWaves * c.rt - 1) / (32 * kRowWaves * c.rt);
+    p.tok_tiles = (batch + 32 * c.nt * c.tw - 1) / (32 * c.nt * c.tw);
+    const int64_t tiles = p.row_tiles * p.tok_tiles;
+    for (int s = 1; s <= 8; ++s) {
+      p.groups_per_split = (int)((groups + s - 1) / s);
+      p.splits = (int)((groups + p.groups_per_split - 1) / p.groups_per_split);
+      if (p.splits != s || (s > 1 && tiles * s > 256)) break;
+      const double whole = (double)(tiles * s / 256), rest = (double)(tiles * s % 256) / 256.0;
+      const double group = whole * (c.a + c.b) + (rest > 0 ? c.a + c.b * rest : 0.0);
+      double us = 4.0 + (double)((p.groups_per_split + c.kw - 1) / c.kw) * group;
+      if (s > 1) us += 2.5 + (double)p.ws_bytes() * 2.0 / 4e6;
+      if (best.splits == 0 || us < least) {
+        least = us;
+        best = p;
+      }
+    }
+  }
+  return best;
+}
+
+inline TileArgs tile_args(const TilePlan &p, const MxDesc &W, const void *x, const uint8_t *xscales,
+                          int64_t batch, void *y, void *ws) {
+  return {W.codes, W.scales, x, xscales, static_cast<uint16_t *>(y), static_cast<float4_t *>(ws),
+          (int)W.rows, (int)W.cols, (int)batch, (int)p.row_tiles, (int)p.tok_tiles, p.splits,
+          p.groups_per_split};
+}
+
+}  // namespace aqlm
