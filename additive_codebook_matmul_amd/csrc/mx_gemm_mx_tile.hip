@@ -22,9 +22,9 @@
 namespace aqlm {
 namespace {
 
-// Byte offset of block c (of 4) of row r in its part of a stage.
+// Byte offset of block c (of 8) of row r in its part of a stage.
 __device__ __forceinline__ uint32_t row_off(int r, int c) {
-  return (uint32_t)r * 64u + (uint32_t)((c ^ ((r >> 2) & 3)) << 4);
+  return (uint32_t)r * 128u + (uint32_t)((c ^ ((r >> 1) & 7)) << 4);
 }
 
 template <int S>
@@ -38,13 +38,13 @@ __device__ __forceinline__ float16_t mfma_mx32(const uint4 &a, uint32_t sa, cons
 template <MxType T, int RT, int NT, int TW, int KW>
 __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(const TileArgs A) {
   constexpr int kWaves = kRowWaves * TW;  // of one share of K
-  constexpr int kWBytes = kRowWaves * RT * 32 * 64, kXBytes = TW * NT * 32 * 64;
+  constexpr int kWBytes = kRowWaves * RT * 32 * 128, kXBytes = TW * NT * 32 * 128;
   constexpr int kStage = kWBytes + kXBytes;
-  constexpr int kSums = tile_sums_bytes<RT, NT, TW>();
-  constexpr int kArray = KW == 1 || KW * kStage > kSums ? KW * kStage : kSums;
+  constexpr int kSums = tile_sums_bytes<RT, NT, TW>();  // two quarters of a share's sums an array
+  constexpr int kArray = KW == 1 || KW * kStage > 2 * kSums ? KW * kStage : 2 * kSums;
   // one array per stage: the compiler then knows which loads into LDS a read
   // of LDS can depend on
-  __shared__ __attribute__((aligned(16))) uint8_t xa0[kArray], xa1[kArray], xa2[kArray], xa3[kArray];
+  __shared__ __attribute__((aligned(16))) uint8_t xa0[kArray], xa1[kArray];
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = KW == 1 ? 0 : wave_all / kWaves, wave = KW == 1 ? wave_all : wave_all % kWaves;
@@ -80,40 +80,35 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  // Step t (of group t / 4) into a stage. One load of a wavefront fills 1 KiB,
-  // 16 rows, in lane order, so a chunk's place in its row is chosen by where
-  // the lane reads from. Blocks past the last one are zeros. Wavefront w of
-  // the share makes loads w, w + kWaves, .. of each side.
-  constexpr int kWLoads = 8 * RT / kWaves;                      // 8 RT of codes of W, all whole
-  constexpr int kXLoads = (2 * NT * TW + kWaves - 1) / kWaves;  // 2 NT TW of codes of x
-  constexpr bool kAllX = (2 * NT * TW) % kWaves == 0;
-  static_assert(8 * RT % kWaves == 0, "every wavefront loads as many codes of W");
-  constexpr int kLoads = kWLoads + (kAllX ? kXLoads : 0);       // of a wavefront and step, at least
-  // (every load's chunk of a lane is block j of its row: c is a multiple of
-  // four rows apart from the next)
-  const int j = (lane & 3) ^ ((lane >> 4) & 3);
+  // Step t (of group t / 2) into a stage. One load of a wavefront fills 1 KiB,
+  // eight rows, in lane order, so a chunk's place in its row is chosen by where
+  // the lane reads from. Blocks past the last one are zeros. Wavefront w of the
+  // share makes loads w, w + kWaves, .. of each side.
+  constexpr int kWLoads = 16 * RT / kWaves, kXLoads = 4 * NT * TW / kWaves;
+  static_assert(16 * RT % kWaves == 0 && 4 * NT * TW % kWaves == 0, "as many loads a wavefront");
   static_assert(kWLoads <= 4 && kXLoads <= 4, "places of a lane's loads");
+  // (every load's chunk of a lane is block j of its row, its rows being even
+  // multiples of eight apart)
   uint32_t woff[4], xoff[4];
+  int jb[4];
+  const int lr = lane >> 3;
 #pragma unroll
-  for (int i = 0; i < kWLoads; ++i)
-    woff[i] = (uint32_t)(16 * (wave + i * kWaves) + (lane >> 2)) * half + 16u * j;
-#pragma unroll
-  for (int i = 0; i < kXLoads; ++i)
-    xoff[i] = (uint32_t)(16 * (wave + i * kWaves) + (lane >> 2)) * half + 16u * j;
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * (wave + i * kWaves) + lr;
+    jb[i] = (lane & 7) ^ ((r >> 1) & 7);
+    woff[i] = xoff[i] = (uint32_t)r * half + 16u * jb[i];
+  }
   auto fill = [&](int t, uint8_t *a) __attribute__((always_inline)) {
-    const bool in = (t < 4 * g1) & (4 * t + j < nb);
-    const uint32_t step = in ? (uint32_t)t * 64u : kMxOOB;
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           crs, (__attribute__((address_space(3))) void *)(a + (kw * kStage + (wave + i * kWaves) * 1024)),
-          16, woff[i] + step, 0, 0, 0);
+          16, woff[i] + (((t < 2 * g1) & (8 * t + jb[i] < nb)) ? (uint32_t)t * 128u : kMxOOB), 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i)
-      if (kAllX || wave + i * kWaves < 2 * NT * TW)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            xrs, (__attribute__((address_space(3))) void *)(a + (kw * kStage + kWBytes + (wave + i * kWaves) * 1024)),
-            16, xoff[i] + step, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          xrs, (__attribute__((address_space(3))) void *)(a + (kw * kStage + kWBytes + (wave + i * kWaves) * 1024)),
+          16, xoff[i] + (((t < 2 * g1) & (8 * t + jb[i] < nb)) ? (uint32_t)t * 128u : kMxOOB), 0, 0, 0);
   };
 
   ScaleRows<RT> wscales(A.scales, row0, tile_rows, nb, rw * 32 * RT + l32);
@@ -122,66 +117,52 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
 
   // (places of the lane's operands in a stage: 32 rows further on the
   // permutation is the same)
-  uint32_t wbase[2], xbase[2];
+  uint32_t wbase[4], xbase[4];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
+  for (int s = 0; s < 4; ++s) {
     wbase[s] = kw * kStage + row_off(rw * 32 * RT + l32, 2 * s + h);
     xbase[s] = kw * kStage + kWBytes + row_off(tw * 32 * NT + l32, 2 * s + h);
   }
   uint4 w[2][RT], b[2][NT];
-  auto reads = [&](const uint8_t *a, auto s_c) __attribute__((always_inline)) {
-    constexpr int S = decltype(s_c)::value;
+  auto reads = [&](const uint8_t *a, int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) w[S][i] = *reinterpret_cast<const uint4 *>(a + (wbase[S] + 2048u * i));
+    for (int i = 0; i < RT; ++i) w[s & 1][i] = *reinterpret_cast<const uint4 *>(a + (wbase[s] + 4096u * i));
 #pragma unroll
-    for (int j = 0; j < NT; ++j) b[S][j] = *reinterpret_cast<const uint4 *>(a + (xbase[S] + 2048u * j));
+    for (int j = 0; j < NT; ++j) b[s & 1][j] = *reinterpret_cast<const uint4 *>(a + (xbase[s] + 4096u * j));
   };
-  typedef std::integral_constant<int, 0> S0;
-  typedef std::integral_constant<int, 1> S1;
-
-  // Step t, the U-th of its group, from stage `a`; `next` is the stage of step
-  // t + 1 and `far` the one that the step before read, filled for step t + 3.
-  // A step begins with its first operands in registers: they are read at the
-  // end of the step before, so that products go on right after the barrier.
-  // Before the barrier the wavefront waits until at most its loads of step t +
-  // 3 are under way: loads complete in order, so behind the barrier all of
-  // step t + 2 lies in LDS. The operand reads of this step have returned,
-  // since products used them.
   uint4 sw[RT], sx[NT], swn[RT], sxn[NT];
-  auto step = [&](int t, auto u_c, const uint8_t *a, const uint8_t *next, uint8_t *far)
-                  __attribute__((always_inline)) {
+  auto step = [&](int t, auto u_c, const uint8_t *a, uint8_t *next) __attribute__((always_inline)) {
     constexpr int U = decltype(u_c)::value;
-    fill(t + 3, far);
+    fill(t + 1, next);
     __builtin_amdgcn_sched_barrier(0);
-    uint32_t wsc[RT], xsc[NT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-      wsc[i] = (U == 0 ? sw[i].x : U == 1 ? sw[i].y : U == 2 ? sw[i].z : sw[i].w) >> (8 * h);
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      xsc[j] = (U == 0 ? sx[j].x : U == 1 ? sx[j].y : U == 2 ? sx[j].z : sx[j].w) >> (8 * h);
-    reads(a, S1{});
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mfma_mx32<0>(w[0][i], wsc[i], b[0][j], xsc[j], acc[i][j]);
-    // the next instruction's operands are read before this one's products
+    reads(a, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, RT + NT, 0);
-    __builtin_amdgcn_sched_group_barrier(0x008, RT * NT, 0);
-    reads(next, S0{});
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int s = 0; s < 4; ++s) {
+      if (s < 3) reads(a, s + 1);
+      uint32_t wsc[RT], xsc[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mfma_mx32<2>(w[1][i], wsc[i], b[1][j], xsc[j], acc[i][j]);
-    __builtin_amdgcn_sched_group_barrier(0x100, RT + NT, 0);
-    __builtin_amdgcn_sched_group_barrier(0x008, RT * NT, 0);
+      for (int i = 0; i < RT; ++i)
+        wsc[i] = (U == 0 ? s < 2 ? sw[i].x : sw[i].y : s < 2 ? sw[i].z : sw[i].w) >> (8 * h);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        xsc[j] = (U == 0 ? s < 2 ? sx[j].x : sx[j].y : s < 2 ? sx[j].z : sx[j].w) >> (8 * h);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] = s & 1 ? mfma_mx32<2>(w[1][i], wsc[i], b[1][j], xsc[j], acc[i][j])
+                            : mfma_mx32<0>(w[0][i], wsc[i], b[0][j], xsc[j], acc[i][j]);
+      if (s < 3) __builtin_amdgcn_sched_group_barrier(0x100, RT + NT, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, RT * NT, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);
     // (keeps the products in their step: nothing else ties them to a place)
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[i][j][0] = materialize(acc[i][j][0]);
-    asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kLoads) : "memory");
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" : : : "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -191,22 +172,15 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
   xscales.load(group_at(g0), sx);
   wscales.place(group_at(g0), sw);
   xscales.place(group_at(g0), sx);
-  fill(4 * g0, xa0);
-  __builtin_amdgcn_sched_barrier(0);
-  fill(4 * g0 + 1, xa1);
-  __builtin_amdgcn_sched_barrier(0);
-  fill(4 * g0 + 2, xa2);
-  asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kLoads) : "memory");
+  fill(2 * g0, xa0);
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" : : : "memory");
-  reads(xa0, S0{});
   for (int g = g0; g < gend; ++g) {
     wscales.load(group_at(g + 1), swn);
     xscales.load(group_at(g + 1), sxn);
-    step(4 * g, std::integral_constant<int, 0>{}, xa0, xa1, xa3);
-    step(4 * g + 1, std::integral_constant<int, 1>{}, xa1, xa2, xa0);
-    step(4 * g + 2, std::integral_constant<int, 2>{}, xa2, xa3, xa1);
-    step(4 * g + 3, std::integral_constant<int, 3>{}, xa3, xa0, xa2);
+    step(2 * g, std::integral_constant<int, 0>{}, xa0, xa1);
+    step(2 * g + 1, std::integral_constant<int, 1>{}, xa1, xa0);
     wscales.place(group_at(g + 1), swn);
     xscales.place(group_at(g + 1), sxn);
 #pragma unroll
@@ -217,7 +191,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
   // the zeros past the last group are in LDS before the wavefront can end
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 
-  if (add_shares<RT, NT, TW, KW>(acc, kw, wave, lane, xa0, xa1, xa2, xa3)) return;
+  if (add_shares<RT, NT, TW, KW>(acc, kw, wave, lane, xa0, xa0 + kSums, xa1, xa1 + kSums)) return;
   store_tile<T, RT, NT, TW>(A, acc, job, at, wave, lane);
 }
 

@@ -12,16 +12,17 @@
 //     activation operand is the 16 bytes of inputs 8 s of the same block of
 //     the lane's token. (The sum over K does not care which inputs meet in an
 //     instruction, so no code changes lanes after its load.)
-//   * Codes and activations go from memory straight to LDS, three steps ahead,
-//     into one of four stages. The loads read whole stretches of rows (32
-//     bytes of codes, 128 of activations, by neighbouring lanes): a lane that
-//     loads its own row's 16 bytes straight to registers costs the address
-//     unit a cache line a lane, which bounded an earlier form of this kernel
-//     (190 us; 178 with the activations alone through LDS three steps ahead; 174 now,
-//     for 2048 x 11008 x 4096).
-//   * Chunks of 16 bytes are permuted within a row on their way (x_off,
-//     w_off), so that the 16 lanes of an LDS pass touch 16 distinct groups of
-//     banks.
+//   * Codes, scales and activations reach the wavefronts through LDS, in whole
+//     128-byte lines: L2 gives about 30 TB/s in such segments, a half in ones
+//     of 64 bytes, a quarter of 32, an eighth of 16, since a request costs its
+//     line. (Each lane loading its own row's 16 bytes of codes and a byte of
+//     scales took 190 us for 2048 x 11008 x 4096, 32-byte segments of codes 174,
+//     this @@.) Activations go straight to LDS three steps ahead, one of four
+//     stages; codes four steps at a time, up to eight ahead, one of two;
+//     scales 64 steps at a time, through registers.
+//   * Chunks of 16 bytes are permuted within a row of 128 bytes on their way
+//     (row_off), so that the 16 lanes of an LDS pass touch 16 distinct groups
+//     of banks.
 //   * Where there are few tiles K is split over workgroups too, whose float32
 //     sums go to the workspace, as the accumulator registers lie, and a second
 //     kernel adds them in a fixed order.
@@ -32,25 +33,23 @@
 namespace aqlm {
 namespace {
 
-// Byte offset of 16-byte chunk j (of 8) of activation row t in a stage.
-__device__ __forceinline__ uint32_t x_off(int t, int j) {
-  return (uint32_t)t * 128u + (uint32_t)((j ^ ((t >> 1) & 7)) << 4);
-}
-// Byte offset of block h (of 2) of weight row r in a stage.
-__device__ __forceinline__ uint32_t w_off(int r, int h) {
-  return (uint32_t)r * 32u + (uint32_t)((h ^ ((r >> 3) & 1)) << 4);
+// Byte offset of 16-byte chunk j (of 8) of row r in a stage.
+__device__ __forceinline__ uint32_t row_off(int r, int j) {
+  return (uint32_t)r * 128u + (uint32_t)((j ^ ((r >> 1) & 7)) << 4);
 }
 
 template <MxType T, int RT, int NT, int TW, int KW>
 __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const TileArgs A) {
   constexpr int kWaves = kRowWaves * TW;             // of one share of K
-  constexpr int kXBytes = TW * NT * 32 * 128, kWBytes = kRowWaves * RT * 32 * 32;
-  constexpr int kStage = kXBytes + kWBytes;
+  constexpr int kRows = kRowWaves * RT * 32;         // of W in the tile
+  constexpr int kXBytes = TW * NT * 32 * 128, kWBytes = kRows * 128, kSBytes = kRows * 128;
   constexpr int kSums = tile_sums_bytes<RT, NT, TW>();
-  constexpr int kArray = KW == 1 || KW * kStage > kSums ? KW * kStage : kSums;
+  constexpr int kArray = KW == 1 || KW * kXBytes > kSums ? KW * kXBytes : kSums;
   // one array per stage: the compiler then knows which loads into LDS a read
   // of LDS can depend on
   __shared__ __attribute__((aligned(16))) uint8_t xa0[kArray], xa1[kArray], xa2[kArray], xa3[kArray];
+  __shared__ __attribute__((aligned(16))) uint8_t wa0[KW * kWBytes], wa1[KW * kWBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t sa[KW * kSBytes];
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = KW == 1 ? 0 : wave_all / kWaves, wave = KW == 1 ? wave_all : wave_all % kWaves;
@@ -86,47 +85,53 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  // Step t (of group t / 8) into a stage. One load of a wavefront fills 1 KiB
-  // in lane order, eight rows of activations or 32 rows of codes, so a chunk's
-  // place in its row is chosen by where the lane reads from. Blocks past the
-  // last one are zeros. Wavefront w of the share makes loads w, w + kWaves, ..
-  constexpr int kXLoads = NT, kWLoads = (kRowWaves * RT + kWaves - 1) / kWaves;
-  constexpr bool kAllW = (kRowWaves * RT) % kWaves == 0;  // every wavefront loads codes
-  const int xrow = lane >> 3, wrow = lane >> 1;
-  auto fill = [&](int t, uint8_t *a) __attribute__((always_inline)) {
-    const bool run = t < 8 * g1;
+  // Activations of step t (of group t / 8), and codes of steps 4 m .. 4 m + 3,
+  // into a stage. One load of a wavefront fills 1 KiB, eight rows, in lane
+  // order, so a chunk's place in its row is chosen by where the lane reads
+  // from. Blocks past the last one are zeros. Wavefront w of the share makes
+  // loads w, w + kWaves, .. of each kind.
+  constexpr int kXLoads = NT, kWLoads = 16 * RT / kWaves;
+  static_assert(16 * RT % kWaves == 0 && kXLoads <= 4 && kWLoads == 4, "loads of a wavefront");
+  const int lrow = lane >> 3;
+  uint32_t xoff[4], woff[4];
+  int xblk[4], wblk[4];  // block of the lane's chunk, from the step's first
 #pragma unroll
-    for (int i = 0; i < kXLoads; ++i) {
-      const int c = wave + i * kWaves, r = 8 * c + xrow;
-      const int j = (lane & 7) ^ ((r >> 1) & 7);
-      const bool in = run & (2 * t + (j >> 2) < nb);
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * (wave + i * kWaves) + lrow, j = (lane & 7) ^ ((r >> 1) & 7);
+    xblk[i] = j >> 2;
+    xoff[i] = (uint32_t)r * (uint32_t)A.cols * 2u + 16u * j;
+    wblk[i] = j;
+    woff[i] = (uint32_t)r * half + 16u * j;
+  }
+  auto fill_x = [&](int t, uint8_t *a) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          xrs, (__attribute__((address_space(3))) void *)(a + (kw * kStage + c * 1024)), 16,
-          in ? (uint32_t)r * (uint32_t)A.cols * 2u + (uint32_t)t * 128u + 16u * j : kMxOOB, 0, 0, 0);
-    }
+          xrs, (__attribute__((address_space(3))) void *)(a + (kw * kXBytes + (wave + i * kWaves) * 1024)), 16,
+          xoff[i] + (((t < 8 * g1) & (2 * t + xblk[i] < nb)) ? (uint32_t)t * 128u : kMxOOB), 0, 0, 0);
+  };
+  auto fill_w = [&](int m, auto part_c, uint8_t *a) __attribute__((always_inline)) {
+    constexpr int P = decltype(part_c)::value;  // half of the loads
 #pragma unroll
-    for (int i = 0; i < kWLoads; ++i) {
-      const int c = wave + i * kWaves, r = 32 * c + wrow;
-      const int j = (lane & 1) ^ ((r >> 3) & 1);
-      const bool in = run & (2 * t + j < nb);
-      if (kAllW || c < kRowWaves * RT)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            crs, (__attribute__((address_space(3))) void *)(a + (kw * kStage + kXBytes + c * 1024)), 16,
-            in ? (uint32_t)r * half + (uint32_t)t * 32u + 16u * j : kMxOOB, 0, 0, 0);
-    }
+    for (int i = 2 * P; i < 2 * P + 2; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          crs, (__attribute__((address_space(3))) void *)(a + (kw * kWBytes + (wave + i * kWaves) * 1024)), 16,
+          woff[i] + (((m < 2 * g1) & (8 * m + wblk[i] < nb)) ? (uint32_t)m * 128u : kMxOOB), 0, 0, 0);
   };
   const int my_rows = tile_rows - rw * 32 * RT;  // of this wavefront, where there are any
-  ScaleRows<RT> scales(A.scales, row0, tile_rows, nb, rw * 32 * RT + l32);
-  auto group_at = [&](int g) __attribute__((always_inline)) { return max(0, min(g, g1 - 1)); };
+  const int tid = wave * 64 + lane;              // of the share
+  ScaleStage<kRows, 64 * kWaves> scales(A.scales, row0, tile_rows, nb);
 
   // (places of the lane's operands in a stage: 32 rows further on the
   // permutation is the same)
-  const uint32_t wbase = kw * kStage + kXBytes + w_off(rw * 32 * RT + l32, h);
-  uint32_t xbase[4];
+  uint32_t wbase[4], xbase[4];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) xbase[s] = kw * kStage + x_off(tw * 32 * NT + l32, 4 * h + s);
-  auto w_of = [&](const uint8_t *a, int i) __attribute__((always_inline)) {
-    return *reinterpret_cast<const uint4 *>(a + (wbase + 1024u * i));
+  for (int s = 0; s < 4; ++s) {
+    wbase[s] = kw * kWBytes + row_off(rw * 32 * RT + l32, 2 * s + h);
+    xbase[s] = kw * kXBytes + row_off(tw * 32 * NT + l32, 4 * h + s);
+  }
+  auto w_of = [&](const uint8_t *a, int u, int i) __attribute__((always_inline)) {
+    return *reinterpret_cast<const uint4 *>(a + (wbase[u] + 4096u * i));
   };
   auto x_of = [&](const uint8_t *a, int j, int s) __attribute__((always_inline)) {
     return *reinterpret_cast<const uint4 *>(a + (xbase[s] + 4096u * j));
@@ -134,20 +139,25 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
 
   // Step t, the U-th of its group, from stage `a`; `next` is the stage of step
   // t + 1 and `far` the one that the step before read, filled for step t + 3.
+  // The codes of steps U = 0 .. 3 lie in wa0, of 4 .. 7 in wa1; each is filled
+  // for four steps further on by the first two steps that read the other.
   // A step begins with its codes and first activation operands in registers:
   // they are read at the end of the step before, so that products go on right
   // after the barrier. Before the barrier the wavefront waits until at most
-  // its loads of step t + 3 are under way: loads complete in order, so behind
-  // the barrier all of step t + 2 lies in LDS. The operand reads of this step
-  // have returned, since products used them.
-  constexpr int kLoads = kXLoads + (kAllW ? kWLoads : 0);  // of a wavefront and step, at least
-  uint4 sc[RT], sn[RT];
+  // its loads of this step are under way: loads complete in order, so behind
+  // the barrier all that was asked for in the steps before lies in LDS:
+  // activations of step t + 2, codes of step t + 2 too. The operand reads of
+  // this step have returned, since products used them.
+  uint4 sc[RT];
   uint4 w[2][RT], b[2][NT];
   auto step = [&](auto wide_c, int t, auto u_c, const uint8_t *a, const uint8_t *next, uint8_t *far)
                   __attribute__((always_inline)) {
     constexpr bool WIDE = decltype(wide_c)::value;
     constexpr int U = decltype(u_c)::value;
-    fill(t + 3, far);
+    uint8_t *const wother = U < 4 ? wa1 : wa0;
+    const uint8_t *const wnext = U < 3 || U == 7 ? wa0 : wa1;
+    fill_x(t + 3, far);
+    if constexpr (U % 4 < 2) fill_w((t >> 2) + 1, std::integral_constant<int, U % 4>{}, wother);
     __builtin_amdgcn_sched_barrier(0);
     float sv[RT];
 #pragma unroll
@@ -175,7 +185,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
     for (int s = 0; s < 4; ++s) {
       if (s == 3) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i) w[(U + 1) & 1][i] = w_of(next, i);
+        for (int i = 0; i < RT; ++i) w[(U + 1) & 1][i] = w_of(wnext, (U + 1) & 3, i);
       }
       if (s == 3 || !WIDE) {
 #pragma unroll
@@ -197,28 +207,42 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kLoads) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kXLoads + (U % 4 < 2 ? 2 : 0)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" : : : "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  scales.load(group_at(g0), sc);
-  scales.place(group_at(g0), sc);
-  fill(8 * g0, xa0);
+  scales.load(16 * g0, tid);
+  fill_w(2 * g0, std::integral_constant<int, 0>{}, wa0);
+  fill_w(2 * g0, std::integral_constant<int, 1>{}, wa0);
+  fill_x(8 * g0, xa0);
+  fill_x(8 * g0 + 1, xa1);
   __builtin_amdgcn_sched_barrier(0);
-  fill(8 * g0 + 1, xa1);
-  __builtin_amdgcn_sched_barrier(0);
-  fill(8 * g0 + 2, xa2);
-  asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kLoads) : "memory");
+  fill_x(8 * g0 + 2, xa2);
+  scales.store(sa + kw * kSBytes, tid);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"(kXLoads) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" : : : "memory");
+  scales.load(16 * g0 + 128, tid);
 #pragma unroll
-  for (int i = 0; i < RT; ++i) w[0][i] = w_of(xa0, i);
+  for (int i = 0; i < RT; ++i) w[0][i] = w_of(wa0, 0, i);
 #pragma unroll
   for (int j = 0; j < NT; ++j) b[0][j] = x_of(xa0, j, 0);
+  // a group's scales, every eighth time from new ones in LDS
+  auto group_scales = [&](int g) __attribute__((always_inline)) {
+    if (g > g0 && ((g - g0) & 7) == 0) {
+      scales.store(sa + kw * kSBytes, tid);
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" : : : "memory");
+      scales.load(16 * g + 128, tid);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      sc[i] = scales.read(sa + kw * kSBytes, rw * 32 * RT + 32 * i + l32, (g - g0) & 7);
+  };
   auto group = [&](auto wide_c, int g) __attribute__((always_inline)) {
-    scales.load(group_at(g + 1), sn);
     const int t = 8 * g;
     step(wide_c, t, std::integral_constant<int, 0>{}, xa0, xa1, xa3);
     step(wide_c, t + 1, std::integral_constant<int, 1>{}, xa1, xa2, xa0);
@@ -228,12 +252,10 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
     step(wide_c, t + 5, std::integral_constant<int, 5>{}, xa1, xa2, xa0);
     step(wide_c, t + 6, std::integral_constant<int, 6>{}, xa2, xa3, xa1);
     step(wide_c, t + 7, std::integral_constant<int, 7>{}, xa3, xa0, xa2);
-    scales.place(group_at(g + 1), sn);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) sc[i] = sn[i];
   };
   int g = g0;
   for (; g < gend; ++g) {
+    group_scales(g);
     if constexpr (T == MxType::kF16) {
       bool f = true;
 #pragma unroll
@@ -251,7 +273,10 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
   // exactly in two. The barriers are those of the other loop, one a step, so
   // wavefronts in either meet.
   if constexpr (T == MxType::kF16)
-    for (; g < gend; ++g) group(std::true_type{}, g);
+    for (bool again = false; g < gend; ++g, again = true) {
+      if (again) group_scales(g);
+      group(std::true_type{}, g);
+    }
   // the zeros past the last group are in LDS before the wavefront can end
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 

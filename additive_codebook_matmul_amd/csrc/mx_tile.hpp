@@ -44,73 +44,76 @@ __device__ __forceinline__ TilePlace tile_place(int tile, int row_tiles, int tok
   return {row_tile, 8 * band + in_band - row_tile * width};
 }
 
-// The scale bytes of N rows of a lane, 16 blocks (a group) at a time. Past the
-// last row they are those of the last one; past the last block they are those
-// of the last block or 127. (The codes there are zeros, but a NaN of another
-// row would still show.) Loaded a group ahead (load), put into place when their
-// group begins (place), so that nothing waits for them meanwhile.
-template <int N> struct ScaleRows {
+// The scale bytes of a tile's ROWS rows for 128 blocks (eight groups of 16) in
+// LDS, [row][128], 16-byte chunk g of row r at chunk g ^ ((r >> 1) & 7). Read
+// from memory by each lane for its own row they cost a 128-byte line for every
+// 16 bytes, which bounded the tile kernels; this way neighbouring lanes read a
+// row's 128 bytes at once. THREADS threads load them into registers early
+// (load) and write them when the ones before are done with (store).
+// Past the last row they are the last one's, past the last block 127: the codes
+// there are zeros, but a NaN of another row would still show.
+template <int ROWS, int THREADS> struct ScaleStage {
+  static constexpr int kChunks = ROWS * 8 / THREADS;
+  static_assert(ROWS * 8 % THREADS == 0, "whole turns");
   Rsrc rs;
-  int nb, base;  // blocks of a row; the tile's first byte within its word
-  uint32_t at[N], extra[N];
+  int nb, base, rows, blk;  // blocks of a row; first byte within its word; rows there are
+  uint4 v[kChunks];
+  uint32_t extra[kChunks];
 
-  // rows row0 .. row0 + rows - 1 of a matrix; `mine` of the tile's rows is the
-  // lane's first, the others follow every 32
-  __device__ __forceinline__ ScaleRows(const uint8_t *scales, int64_t row0, int rows, int nb_, int mine)
-      : nb(nb_) {
+  __device__ __forceinline__ ScaleStage(const uint8_t *scales, int64_t row0, int rows_, int nb_)
+      : nb(nb_), rows(rows_), blk(0) {
     base = (int)((row0 * nb) & 3);
     rs = make_rsrc(scales + row0 * nb - base, (uint32_t)rows * nb + base);
-#pragma unroll
-    for (int i = 0; i < N; ++i) at[i] = (uint32_t)max(0, min(mine + 32 * i, rows - 1)) * nb + base;
   }
-  __device__ __forceinline__ void load(int group, uint4 (&sv)[N]) {
-    const int blk = 16 * group, left = nb - blk;
-    if ((nb & 3) == 0) {  // words lie whole in a row
+  __device__ __forceinline__ uint32_t at(int id) const {  // of chunk id's first byte
+    return (uint32_t)min(id >> 3, rows - 1) * nb + base + (uint32_t)(blk + 16 * (id & 7));
+  }
+  // blocks first .. first + 127
+  __device__ __forceinline__ void load(int first, int tid) {
+    blk = first;
 #pragma unroll
-      for (int i = 0; i < N; ++i) sv[i] = buf_load16(rs, at[i] + (uint32_t)blk);
-    } else if (left >= 19) {  // five aligned words hold them, and end inside the row
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const uint32_t to = (at[i] + (uint32_t)blk) & ~3u;
-        sv[i] = buf_load16(rs, to);
-        extra[i] = buf_load4(rs, to + 16);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        uint32_t v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          v[u] = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[u] |= buf_load_u8(rs, at[i] + (uint32_t)min(blk + 4 * u + e, nb - 1)) << (8 * e);
-        }
-        sv[i] = make_uint4(v[0], v[1], v[2], v[3]);
-      }
+    for (int i = 0; i < kChunks; ++i) {
+      const int id = tid + i * THREADS;
+      const uint32_t to = at(id) & ~3u;
+      const bool in = blk + 16 * (id & 7) < nb;
+      v[i] = buf_load16(rs, in ? to : kMxOOB);
+      extra[i] = buf_load4(rs, in ? to + 16 : kMxOOB);
     }
   }
-  __device__ __forceinline__ void place(int group, uint4 (&sv)[N]) {
-    const int blk = 16 * group, left = nb - blk;
-    if ((nb & 3) == 0) {
-      if (left < 16) {
+  __device__ __forceinline__ void store(uint8_t *lds, int tid) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (left <= 12) sv[i].w = 0x7F7F7F7Fu;
-          if (left <= 8) sv[i].z = 0x7F7F7F7Fu;
-          if (left <= 4) sv[i].y = 0x7F7F7F7Fu;
+    for (int i = 0; i < kChunks; ++i) {
+      const int id = tid + i * THREADS, r = id >> 3, g = id & 7;
+      const int left = nb - (blk + 16 * g);  // blocks from the chunk's first on
+      const uint32_t from = at(id), by = from & 3u;
+      uint32_t d[5] = {v[i].x, v[i].y, v[i].z, v[i].w, extra[i]};
+      // A word that ends past the array reads zero; its bytes that exist are
+      // read one by one (the last row's end alone).
+      const uint32_t end = (uint32_t)rows * nb + base, word = end & ~3u, to = from & ~3u;
+      if (word != end && left > 0 && to + 20 > word) {
+        uint32_t tail = buf_load_u8(rs, word);
+        if ((end & 3u) > 1) tail |= buf_load_u8(rs, word + 1) << 8;
+        if ((end & 3u) > 2) tail |= buf_load_u8(rs, word + 2) << 16;
+#pragma unroll
+        for (int u = 0; u < 5; ++u) d[u] = to + 4 * u == word ? tail : d[u];
+      }
+      uint32_t w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        w[u] = __builtin_amdgcn_alignbyte(d[u + 1], d[u], by);
+        const int keep = left - 4 * u;  // bytes of the word that are blocks
+        if (keep < 4) {
+          const uint32_t m = keep <= 0 ? 0u : 0xFFFFFFFFu >> (32 - 8 * keep);
+          w[u] = (w[u] & m) | (0x7F7F7F7Fu & ~m);
         }
       }
-    } else if (left >= 19) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const uint32_t by = (at[i] + (uint32_t)blk) & 3u;
-        sv[i].x = __builtin_amdgcn_alignbyte(sv[i].y, sv[i].x, by);
-        sv[i].y = __builtin_amdgcn_alignbyte(sv[i].z, sv[i].y, by);
-        sv[i].z = __builtin_amdgcn_alignbyte(sv[i].w, sv[i].z, by);
-        sv[i].w = __builtin_amdgcn_alignbyte(extra[i], sv[i].w, by);
-      }
+      *reinterpret_cast<uint4 *>(lds + (r * 128 + ((g ^ ((r >> 1) & 7)) << 4))) =
+          make_uint4(w[0], w[1], w[2], w[3]);
     }
+  }
+  // the 16 bytes of group g (0 .. 7) of row r
+  static __device__ __forceinline__ uint4 read(const uint8_t *lds, int r, int g) {
+    return *reinterpret_cast<const uint4 *>(lds + (r * 128 + ((g ^ ((r >> 1) & 7)) << 4)));
   }
 };
 
