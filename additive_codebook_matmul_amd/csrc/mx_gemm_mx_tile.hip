@@ -5,13 +5,15 @@
 // 32, lane / 32) gives the 16 bytes of block h (32 codes) of row r of the
 // 64-input chunk and, in a byte of a register, that block's scale; W and x
 // alike, and both as they lie in memory.
-//   * A K step is 128 inputs, two such chunks. Both sides go from memory
-//     straight to LDS three steps ahead, into one of four stages of 64-byte
-//     rows; four neighbouring lanes load a row's 64 bytes. 16-byte chunk c of
-//     row r lies at chunk c ^ ((r >> 2) & 3), so that the 16 lanes of an LDS
-//     pass touch 16 distinct groups of banks.
-//   * A lane's scales of a step are one word of its row. Shifted by 8 h its
-//     bytes 0 and 2 are those of the two chunks, which the instruction selects.
+//   * A K step is 256 inputs, four such chunks: 128-byte rows, whole lines of
+//     L2 (in 64-byte rows, or with scales loaded by each lane for its own row,
+//     the requests cost as much again). Both sides go from memory straight to
+//     LDS a step ahead, into one of two stages; 16-byte chunk c of row r lies at
+//     chunk c ^ ((r >> 1) & 7), so that the 16 lanes of an LDS pass touch 16
+//     distinct groups of banks.
+//   * Scales go through LDS 128 blocks at a time; a lane's for two steps are
+//     four words of its row. Shifted by 8 h, bytes 0 and 2 of a word are those
+//     of two chunks, which the instruction selects.
 //   * A 32 x 32 x 64 product takes a SIMD as long as 32 x 32 x 16 of halves,
 //     with the same two operand reads of 1 KiB: with 64 x 64 per wavefront the
 //     reads keep LDS as long as the products keep the matrix cores.
@@ -38,13 +40,15 @@ __device__ __forceinline__ float16_t mfma_mx32(const uint4 &a, uint32_t sa, cons
 template <MxType T, int RT, int NT, int TW, int KW>
 __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(const TileArgs A) {
   constexpr int kWaves = kRowWaves * TW;  // of one share of K
-  constexpr int kWBytes = kRowWaves * RT * 32 * 128, kXBytes = TW * NT * 32 * 128;
+  constexpr int kRows = kRowWaves * RT * 32, kToks = TW * NT * 32;
+  constexpr int kWBytes = kRows * 128, kXBytes = kToks * 128;
   constexpr int kStage = kWBytes + kXBytes;
   constexpr int kSums = tile_sums_bytes<RT, NT, TW>();  // two quarters of a share's sums an array
   constexpr int kArray = KW == 1 || KW * kStage > 2 * kSums ? KW * kStage : 2 * kSums;
   // one array per stage: the compiler then knows which loads into LDS a read
   // of LDS can depend on
   __shared__ __attribute__((aligned(16))) uint8_t xa0[kArray], xa1[kArray];
+  __shared__ __attribute__((aligned(16))) uint8_t sa[KW * kStage];  // scales, [rows of W, tokens][128]
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = KW == 1 ? 0 : wave_all / kWaves, wave = KW == 1 ? wave_all : wave_all % kWaves;
@@ -57,7 +61,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
   const int row0 = at.row_tile * (kRowWaves * 32 * RT), tok0 = at.tok_tile * (32 * NT * TW);
   const int nb = A.cols >> 5;
 
-  // K goes in groups of four steps, 16 blocks. The groups of this split, and
+  // K goes in groups of two steps, 16 blocks. The groups of this split, and
   // of those the wavefront's: each of the KW shares takes as many turns as the
   // largest (past its end with zeros), so that all meet at every barrier.
   const int s0 = split * A.groups_per_split, s1 = min((nb + 15) >> 4, s0 + A.groups_per_split);
@@ -111,9 +115,10 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
           16, xoff[i] + (((t < 2 * g1) & (8 * t + jb[i] < nb)) ? (uint32_t)t * 128u : kMxOOB), 0, 0, 0);
   };
 
-  ScaleRows<RT> wscales(A.scales, row0, tile_rows, nb, rw * 32 * RT + l32);
-  ScaleRows<NT> xscales(A.xscales, tok0, tile_toks, nb, tw * 32 * NT + l32);
-  auto group_at = [&](int g) __attribute__((always_inline)) { return max(0, min(g, g1 - 1)); };
+  const int tid = wave * 64 + lane;  // of the share
+  ScaleStage<kRows, 64 * kWaves> wscales(A.scales, row0, tile_rows, nb);
+  ScaleStage<kToks, 64 * kWaves> xscales(A.xscales, tok0, tile_toks, nb);
+  uint8_t *const ws = sa + kw * kStage, *const xs = ws + kWBytes;
 
   // (places of the lane's operands in a stage: 32 rows further on the
   // permutation is the same)
@@ -130,7 +135,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
 #pragma unroll
     for (int j = 0; j < NT; ++j) b[s & 1][j] = *reinterpret_cast<const uint4 *>(a + (xbase[s] + 4096u * j));
   };
-  uint4 sw[RT], sx[NT], swn[RT], sxn[NT];
+  uint4 sw[RT], sx[NT];
   auto step = [&](int t, auto u_c, const uint8_t *a, uint8_t *next) __attribute__((always_inline)) {
     constexpr int U = decltype(u_c)::value;
     fill(t + 1, next);
@@ -168,25 +173,33 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  wscales.load(group_at(g0), sw);
-  xscales.load(group_at(g0), sx);
-  wscales.place(group_at(g0), sw);
-  xscales.place(group_at(g0), sx);
+  wscales.load(16 * g0, tid);
+  xscales.load(16 * g0, tid);
   fill(2 * g0, xa0);
-  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  wscales.store(ws, tid);
+  xscales.store(xs, tid);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" : : : "memory");
+  wscales.load(16 * g0 + 128, tid);
+  xscales.load(16 * g0 + 128, tid);
   for (int g = g0; g < gend; ++g) {
-    wscales.load(group_at(g + 1), swn);
-    xscales.load(group_at(g + 1), sxn);
+    const int turn = (g - g0) & 7;
+    if (g > g0 && turn == 0) {  // every eighth time new scales in LDS
+      wscales.store(ws, tid);
+      xscales.store(xs, tid);
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" : : : "memory");
+      wscales.load(16 * g + 128, tid);
+      xscales.load(16 * g + 128, tid);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) sw[i] = wscales.read(ws, rw * 32 * RT + 32 * i + l32, turn);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) sx[j] = xscales.read(xs, tw * 32 * NT + 32 * j + l32, turn);
     step(2 * g, std::integral_constant<int, 0>{}, xa0, xa1);
     step(2 * g + 1, std::integral_constant<int, 1>{}, xa1, xa0);
-    wscales.place(group_at(g + 1), swn);
-    xscales.place(group_at(g + 1), sxn);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) sw[i] = swn[i];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) sx[j] = sxn[j];
   }
   // the zeros past the last group are in LDS before the wavefront can end
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
