@@ -29,6 +29,8 @@ __device__ __forceinline__ uint32_t row_off(int r, int c) {
   return (uint32_t)r * 128u + (uint32_t)((c ^ ((r >> 1) & 7)) << 4);
 }
 
+constexpr int kTurns = 2;  // groups whose scales LDS holds
+
 template <int S>
 __device__ __forceinline__ float16_t mfma_mx32(const uint4 &a, uint32_t sa, const uint4 &b, uint32_t sb,
                                                float16_t c) {
@@ -43,12 +45,15 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
   constexpr int kRows = kRowWaves * RT * 32, kToks = TW * NT * 32;
   constexpr int kWBytes = kRows * 128, kXBytes = kToks * 128;
   constexpr int kStage = kWBytes + kXBytes;
+  typedef ScaleStage<kRows, 64 * kWaves, kTurns> WScales;
+  typedef ScaleStage<kToks, 64 * kWaves, kTurns> XScales;
+  constexpr int kScales = WScales::kBytes + XScales::kBytes;
   constexpr int kSums = tile_sums_bytes<RT, NT, TW>();  // two quarters of a share's sums an array
   constexpr int kArray = KW == 1 || KW * kStage > 2 * kSums ? KW * kStage : 2 * kSums;
   // one array per stage: the compiler then knows which loads into LDS a read
   // of LDS can depend on
-  __shared__ __attribute__((aligned(16))) uint8_t xa0[kArray], xa1[kArray];
-  __shared__ __attribute__((aligned(16))) uint8_t sa[KW * kStage];  // scales, [rows of W, tokens][128]
+  __shared__ __attribute__((aligned(16))) uint8_t xa0[kArray], xa1[kArray], xa2[kArray];
+  __shared__ __attribute__((aligned(16))) uint8_t sa[KW * kScales];
   const int lane = threadIdx.x & 63;
   const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = KW == 1 ? 0 : wave_all / kWaves, wave = KW == 1 ? wave_all : wave_all % kWaves;
@@ -116,9 +121,9 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
   };
 
   const int tid = wave * 64 + lane;  // of the share
-  ScaleStage<kRows, 64 * kWaves> wscales(A.scales, row0, tile_rows, nb);
-  ScaleStage<kToks, 64 * kWaves> xscales(A.xscales, tok0, tile_toks, nb);
-  uint8_t *const ws = sa + kw * kStage, *const xs = ws + kWBytes;
+  WScales wscales(A.scales, row0, tile_rows, nb);
+  XScales xscales(A.xscales, tok0, tile_toks, nb);
+  uint8_t *const ws = sa + kw * kScales, *const xs = ws + WScales::kBytes;
 
   // (places of the lane's operands in a stage: 32 rows further on the
   // permutation is the same)
@@ -136,9 +141,9 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
     for (int j = 0; j < NT; ++j) b[s & 1][j] = *reinterpret_cast<const uint4 *>(a + (xbase[s] + 4096u * j));
   };
   uint4 sw[RT], sx[NT];
-  auto step = [&](int t, auto u_c, const uint8_t *a, uint8_t *next) __attribute__((always_inline)) {
+  auto step = [&](int t, auto u_c, const uint8_t *a, uint8_t *far) __attribute__((always_inline)) {
     constexpr int U = decltype(u_c)::value;
-    fill(t + 1, next);
+    fill(t + 2, far);
     __builtin_amdgcn_sched_barrier(0);
     reads(a, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, RT + NT, 0);
@@ -167,7 +172,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[i][j][0] = materialize(acc[i][j][0]);
-    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" : : "i"(kWLoads + kXLoads) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" : : : "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -176,30 +181,40 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
   wscales.load(16 * g0, tid);
   xscales.load(16 * g0, tid);
   fill(2 * g0, xa0);
+  __builtin_amdgcn_sched_barrier(0);
+  fill(2 * g0 + 1, xa1);
   wscales.store(ws, tid);
   xscales.store(xs, tid);
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"(kWLoads + kXLoads) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" : : : "memory");
-  wscales.load(16 * g0 + 128, tid);
-  xscales.load(16 * g0 + 128, tid);
-  for (int g = g0; g < gend; ++g) {
-    const int turn = (g - g0) & 7;
-    if (g > g0 && turn == 0) {  // every eighth time new scales in LDS
+  wscales.load(16 * (g0 + kTurns), tid);
+  xscales.load(16 * (g0 + kTurns), tid);
+  auto group = [&](int g, const uint8_t *a0, uint8_t *a1, uint8_t *a2) __attribute__((always_inline)) {
+    const int turn = (g - g0) % kTurns;
+    if (g > g0 && turn == 0) {  // new scales in LDS
       wscales.store(ws, tid);
       xscales.store(xs, tid);
       asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" : : : "memory");
-      wscales.load(16 * g + 128, tid);
-      xscales.load(16 * g + 128, tid);
+      wscales.load(16 * (g + kTurns), tid);
+      xscales.load(16 * (g + kTurns), tid);
     }
 #pragma unroll
-    for (int i = 0; i < RT; ++i) sw[i] = wscales.read(ws, rw * 32 * RT + 32 * i + l32, turn);
+    for (int i = 0; i < RT; ++i) sw[i] = WScales::read(ws, rw * 32 * RT + 32 * i + l32, turn);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) sx[j] = xscales.read(xs, tw * 32 * NT + 32 * j + l32, turn);
-    step(2 * g, std::integral_constant<int, 0>{}, xa0, xa1);
-    step(2 * g + 1, std::integral_constant<int, 1>{}, xa1, xa0);
+    for (int j = 0; j < NT; ++j) sx[j] = XScales::read(xs, tw * 32 * NT + 32 * j + l32, turn);
+    step(2 * g, std::integral_constant<int, 0>{}, a0, a2);
+    step(2 * g + 1, std::integral_constant<int, 1>{}, a1, const_cast<uint8_t *>(a0));
+  };
+  for (int g = g0;;) {
+    group(g, xa0, xa1, xa2);
+    if (++g >= gend) break;
+    group(g, xa2, xa0, xa1);
+    if (++g >= gend) break;
+    group(g, xa1, xa2, xa0);
+    if (++g >= gend) break;
   }
   // the zeros past the last group are in LDS before the wavefront can end
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");

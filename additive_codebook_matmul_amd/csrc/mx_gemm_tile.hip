@@ -120,7 +120,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
   };
   const int my_rows = tile_rows - rw * 32 * RT;  // of this wavefront, where there are any
   const int tid = wave * 64 + lane;              // of the share
-  ScaleStage<kRows, 64 * kWaves> scales(A.scales, row0, tile_rows, nb);
+  ScaleStage<kRows, 64 * kWaves, 8> scales(A.scales, row0, tile_rows, nb);
 
   // (places of the lane's operands in a stage: 32 rows further on the
   // permutation is the same)

@@ -44,17 +44,18 @@ __device__ __forceinline__ TilePlace tile_place(int tile, int row_tiles, int tok
   return {row_tile, 8 * band + in_band - row_tile * width};
 }
 
-// The scale bytes of a tile's ROWS rows for 128 blocks (eight groups of 16) in
-// LDS, [row][128], 16-byte chunk g of row r at chunk g ^ ((r >> 1) & 7). Read
-// from memory by each lane for its own row they cost a 128-byte line for every
-// 16 bytes, which bounded the tile kernels; this way neighbouring lanes read a
-// row's 128 bytes at once. THREADS threads load them into registers early
-// (load) and write them when the ones before are done with (store).
+// The scale bytes of a tile's ROWS rows for GROUPS groups of 16 blocks in LDS,
+// [row][16 GROUPS], 16-byte chunk g of row r at a place that spreads the rows
+// over the banks. Read from memory by each lane for its own row they cost a
+// 128-byte line for every 16 bytes, which bounded the tile kernels; this way
+// neighbouring lanes read a row's bytes at once. THREADS threads load them into
+// registers early (load) and write them when the ones before are done with
+// (store).
 // Past the last row they are the last one's, past the last block 127: the codes
 // there are zeros, but a NaN of another row would still show.
-template <int ROWS, int THREADS> struct ScaleStage {
-  static constexpr int kChunks = ROWS * 8 / THREADS;
-  static_assert(ROWS * 8 % THREADS == 0, "whole turns");
+template <int ROWS, int THREADS, int GROUPS> struct ScaleStage {
+  static constexpr int kAll = ROWS * GROUPS, kChunks = (kAll + THREADS - 1) / THREADS;
+  static constexpr int kBytes = kAll * 16;
   Rsrc rs;
   int nb, base, rows, blk;  // blocks of a row; first byte within its word; rows there are
   uint4 v[kChunks];
@@ -66,16 +67,19 @@ template <int ROWS, int THREADS> struct ScaleStage {
     rs = make_rsrc(scales + row0 * nb - base, (uint32_t)rows * nb + base);
   }
   __device__ __forceinline__ uint32_t at(int id) const {  // of chunk id's first byte
-    return (uint32_t)min(id >> 3, rows - 1) * nb + base + (uint32_t)(blk + 16 * (id & 7));
+    return (uint32_t)min(id / GROUPS, rows - 1) * nb + base + (uint32_t)(blk + 16 * (id % GROUPS));
   }
-  // blocks first .. first + 127
+  static __device__ __forceinline__ uint32_t place(int r, int g) {
+    return (uint32_t)r * (16 * GROUPS) + (uint32_t)((g ^ ((r * GROUPS >> 4) & (GROUPS - 1))) << 4);
+  }
+  // blocks first .. first + 16 GROUPS - 1
   __device__ __forceinline__ void load(int first, int tid) {
     blk = first;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int id = tid + i * THREADS;
       const uint32_t to = at(id) & ~3u;
-      const bool in = blk + 16 * (id & 7) < nb;
+      const bool in = blk + 16 * (id % GROUPS) < nb && (kAll % THREADS == 0 || id < kAll);
       v[i] = buf_load16(rs, in ? to : kMxOOB);
       extra[i] = buf_load4(rs, in ? to + 16 : kMxOOB);
     }
@@ -83,7 +87,8 @@ template <int ROWS, int THREADS> struct ScaleStage {
   __device__ __forceinline__ void store(uint8_t *lds, int tid) {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      const int id = tid + i * THREADS, r = id >> 3, g = id & 7;
+      const int id = tid + i * THREADS, r = id / GROUPS, g = id % GROUPS;
+      if (kAll % THREADS != 0 && id >= kAll) break;
       const int left = nb - (blk + 16 * g);  // blocks from the chunk's first on
       const uint32_t from = at(id), by = from & 3u;
       uint32_t d[5] = {v[i].x, v[i].y, v[i].z, v[i].w, extra[i]};
@@ -107,13 +112,12 @@ template <int ROWS, int THREADS> struct ScaleStage {
           w[u] = (w[u] & m) | (0x7F7F7F7Fu & ~m);
         }
       }
-      *reinterpret_cast<uint4 *>(lds + (r * 128 + ((g ^ ((r >> 1) & 7)) << 4))) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(lds + place(r, g)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  // the 16 bytes of group g (0 .. 7) of row r
+  // the 16 bytes of group g of row r
   static __device__ __forceinline__ uint4 read(const uint8_t *lds, int r, int g) {
-    return *reinterpret_cast<const uint4 *>(lds + (r * 128 + ((g ^ ((r >> 1) & 7)) << 4)));
+    return *reinterpret_cast<const uint4 *>(lds + place(r, g));
   }
 };
 
