@@ -49,6 +49,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
   typedef ScaleStage<kToks, 64 * kWaves, kTurns> XScales;
   constexpr int kScales = WScales::kBytes + XScales::kBytes;
   constexpr int kSums = tile_sums_bytes<RT, NT, TW>();  // two quarters of a share's sums an array
+  static_assert(kStage >= kWaves * kStoreBytes<RT>, "room for the results");
   constexpr int kArray = KW == 1 || KW * kStage > 2 * kSums ? KW * kStage : 2 * kSums;
   // one array per stage: the compiler then knows which loads into LDS a read
   // of LDS can depend on
@@ -216,11 +217,12 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_mx_tile_kernel(co
     group(g, xa1, xa2, xa0);
     if (++g >= gend) break;
   }
-  // the zeros past the last group are in LDS before the wavefront can end
+  // the zeros past the last group are in LDS before it is used again
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  __syncthreads();
 
   if (add_shares<RT, NT, TW, KW>(acc, kw, wave, lane, xa0, xa0 + kSums, xa1, xa1 + kSums)) return;
-  store_tile<T, RT, NT, TW>(A, acc, job, at, wave, lane);
+  store_tile<T, RT, NT, TW>(A, acc, job, at, wave, lane, xa2);
 }
 
 constexpr TileShape kShapes[] = {

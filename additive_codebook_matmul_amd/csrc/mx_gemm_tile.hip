@@ -44,6 +44,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
   constexpr int kRows = kRowWaves * RT * 32;         // of W in the tile
   constexpr int kXBytes = TW * NT * 32 * 128, kWBytes = kRows * 128, kSBytes = kRows * 128;
   constexpr int kSums = tile_sums_bytes<RT, NT, TW>();
+  static_assert(kWBytes * KW >= kWaves * kStoreBytes<RT>, "room for the results");
   constexpr int kArray = KW == 1 || KW * kXBytes > kSums ? KW * kXBytes : kSums;
   // one array per stage: the compiler then knows which loads into LDS a read
   // of LDS can depend on
@@ -277,11 +278,12 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
       if (again) group_scales(g);
       group(std::true_type{}, g);
     }
-  // the zeros past the last group are in LDS before the wavefront can end
+  // the zeros past the last group are in LDS before it is used again
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  __syncthreads();
 
   if (add_shares<RT, NT, TW, KW>(acc, kw, wave, lane, xa0, xa1, xa2, xa3)) return;
-  store_tile<T, RT, NT, TW>(A, acc, job, at, wave, lane);
+  store_tile<T, RT, NT, TW>(A, acc, job, at, wave, lane, wa0);
 }
 
 // Fitted to 4096 x 4096, 4096 x 11008 and 11008 x 4096 from 32 to 2048 rows.

@@ -81,7 +81,7 @@ template <int ROWS, int THREADS, int GROUPS> struct ScaleStage {
       const uint32_t to = at(id) & ~3u;
       const bool in = blk + 16 * (id % GROUPS) < nb && (kAll % THREADS == 0 || id < kAll);
       v[i] = buf_load16(rs, in ? to : kMxOOB);
-      extra[i] = buf_load4(rs, in ? to + 16 : kMxOOB);
+      if ((nb & 3) != 0) extra[i] = buf_load4(rs, in ? to + 16 : kMxOOB);
     }
   }
   __device__ __forceinline__ void store(uint8_t *lds, int tid) {
@@ -90,25 +90,28 @@ template <int ROWS, int THREADS, int GROUPS> struct ScaleStage {
       const int id = tid + i * THREADS, r = id / GROUPS, g = id % GROUPS;
       if (kAll % THREADS != 0 && id >= kAll) break;
       const int left = nb - (blk + 16 * g);  // blocks from the chunk's first on
-      const uint32_t from = at(id), by = from & 3u;
-      uint32_t d[5] = {v[i].x, v[i].y, v[i].z, v[i].w, extra[i]};
-      // A word that ends past the array reads zero; its bytes that exist are
-      // read one by one (the last row's end alone).
-      const uint32_t end = (uint32_t)rows * nb + base, word = end & ~3u, to = from & ~3u;
-      if (word != end && left > 0 && to + 20 > word) {
-        uint32_t tail = buf_load_u8(rs, word);
-        if ((end & 3u) > 1) tail |= buf_load_u8(rs, word + 1) << 8;
-        if ((end & 3u) > 2) tail |= buf_load_u8(rs, word + 2) << 16;
+      uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      if ((nb & 3) != 0) {  // the bytes lie across words
+        const uint32_t from = at(id), by = from & 3u;
+        uint32_t d[5] = {w[0], w[1], w[2], w[3], extra[i]};
+        // A word that ends past the array reads zero; its bytes that exist are
+        // read one by one (the last row's end alone).
+        const uint32_t end = (uint32_t)rows * nb + base, word = end & ~3u, to = from & ~3u;
+        if (word != end && left > 0 && to + 20 > word) {
+          uint32_t tail = buf_load_u8(rs, word);
+          if ((end & 3u) > 1) tail |= buf_load_u8(rs, word + 1) << 8;
+          if ((end & 3u) > 2) tail |= buf_load_u8(rs, word + 2) << 16;
 #pragma unroll
-        for (int u = 0; u < 5; ++u) d[u] = to + 4 * u == word ? tail : d[u];
+          for (int u = 0; u < 5; ++u) d[u] = to + 4 * u == word ? tail : d[u];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = __builtin_amdgcn_alignbyte(d[u + 1], d[u], by);
       }
-      uint32_t w[4];
+      if (left < 16) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        w[u] = __builtin_amdgcn_alignbyte(d[u + 1], d[u], by);
-        const int keep = left - 4 * u;  // bytes of the word that are blocks
-        if (keep < 4) {
-          const uint32_t m = keep <= 0 ? 0u : 0xFFFFFFFFu >> (32 - 8 * keep);
+        for (int u = 0; u < 4; ++u) {
+          const int keep = left - 4 * u;  // bytes of the word that are blocks
+          const uint32_t m = keep <= 0 ? 0u : keep >= 4 ? ~0u : 0xFFFFFFFFu >> (32 - 8 * keep);
           w[u] = (w[u] & m) | (0x7F7F7F7Fu & ~m);
         }
       }
@@ -172,10 +175,17 @@ __device__ __forceinline__ bool add_shares(float16_t (&acc)[RT][NT], int kw, int
 
 // The tile's results: to the workspace as the registers lie where K is split
 // over workgroups, else rounded into y. Register 4 q + e of a 32 x 32 tile is
-// row 8 q + 4 (lane / 32) + e, token lane % 32.
+// row 8 q + 4 (lane / 32) + e, token lane % 32, so a lane's values are four rows
+// apart from the next lane's token; they pass through LDS (kStoreBytes of it a
+// wavefront, 32 tokens at a time), from where eight lanes store the 128 bytes of
+// 64 rows (four the 64 of 32) of a token: 8-byte stores from the registers took
+// 15 us of 76 with 2048 x 11008 results. The caller's barrier stands between
+// the last other use of that LDS and this.
+template <int RT> constexpr int kStoreBytes = RT * 2048;
+
 template <MxType T, int RT, int NT, int TW>
 __device__ __forceinline__ void store_tile(const TileArgs &A, const float16_t (&acc)[RT][NT], int job,
-                                           const TilePlace &at, int wave, int lane) {
+                                           const TilePlace &at, int wave, int lane, uint8_t *lds) {
   constexpr int kThreads = 64 * kRowWaves * TW;
   if (A.splits > 1) {
     float4_t *p = A.part + (int64_t)job * (RT * NT * 4 * kThreads) + wave * 64 + lane;
@@ -188,18 +198,44 @@ __device__ __forceinline__ void store_tile(const TileArgs &A, const float16_t (&
     return;
   }
   const int rw = wave / TW, tw = wave % TW;
+  const int row0 = (at.row_tile * kRowWaves + rw) * 32 * RT, tok0 = (at.tok_tile * TW + tw) * 32 * NT;
+  if ((A.rows & 7) == 0) {
+    constexpr int kChunks = 4 * RT;  // of 16 bytes, eight rows, for a token
+    uint8_t *const mine = lds + wave * kStoreBytes<RT>;
+    const int t = lane & 31;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = (4 * i + q) ^ (t & (kChunks - 1));
+          *reinterpret_cast<uint2 *>(mine + (t * kChunks + c) * 16 + 8 * (lane >> 5)) =
+              make_uint2(f2t<T>(acc[i][j][4 * q]) | (f2t<T>(acc[i][j][4 * q + 1]) << 16),
+                         f2t<T>(acc[i][j][4 * q + 2]) | (f2t<T>(acc[i][j][4 * q + 3]) << 16));
+        }
+#pragma unroll
+      for (int k = 0; k < kChunks / 2; ++k) {
+        const int id = 64 * k + lane, tt = id / kChunks, c = id % kChunks;
+        const uint4 v = *reinterpret_cast<const uint4 *>(mine + (tt * kChunks + (c ^ (tt & (kChunks - 1)))) * 16);
+        const int tok = tok0 + 32 * j + tt, row = row0 + 8 * c;
+        if (tok < A.batch && row < A.rows)
+          *reinterpret_cast<uint4 *>(A.y + (int64_t)tok * A.rows + row) = v;
+      }
+    }
+    return;
+  }
   const bool packed = (A.rows & 3) == 0;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int tok = (at.tok_tile * TW + tw) * 32 * NT + 32 * j + (lane & 31);
+    const int tok = tok0 + 32 * j + (lane & 31);
     if (tok >= A.batch) continue;
     uint16_t *row = A.y + (int64_t)tok * A.rows;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        store4<T>(row, (at.row_tile * kRowWaves + rw) * 32 * RT + 32 * i + 8 * q + 4 * (lane >> 5),
-                  A.rows, quarter(acc[i][j], q), packed);
+        store4<T>(row, row0 + 32 * i + 8 * q + 4 * (lane >> 5), A.rows, quarter(acc[i][j], q), packed);
   }
 }
 
