@@ -187,7 +187,6 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_grad_tile_kernel(
         for (int j = 0; j < NT; ++j) b[s & 1][j] = x_of(a, j, s);
       };
       reads(0);
-      __builtin_amdgcn_sched_barrier(0);
       put_w(blk[(U + 1) & 3], wfar, wide_c);
       if constexpr (kLook) {
         bad = bad | unfit(t + 1, blk[(U + 1) & 3]);
@@ -212,6 +211,15 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_grad_tile_kernel(
               acc[i][j] = mx_mfma32<T>(wv[s & 1][i], b[s & 1][j], acc[i][j]);
             }
           }
+        // the next instruction's operands are read before this one's products,
+        // a chunk of the next rows written between them
+        if constexpr (!WIDE || T != MxType::kF16) {
+          if (s == 0) __builtin_amdgcn_sched_group_barrier(0x100, 2 * (2 * RT + NT), 0);
+          else if (s < 3) __builtin_amdgcn_sched_group_barrier(0x100, 2 * RT + NT, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, (RT * NT + 1) / 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, RT * NT - (RT * NT + 1) / 2, 0);
+        }
       }
       // (keeps the products in their step: nothing else ties them to a place)
 #pragma unroll
@@ -219,7 +227,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_grad_tile_kernel(
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j][0] = materialize(acc[i][j][0]);
       __builtin_amdgcn_sched_barrier(0);
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"(2 * kXLoads) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"(2 * (kXLoads + 2)) : "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" : : : "memory");
       __builtin_amdgcn_sched_barrier(0);
@@ -232,9 +240,10 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_grad_tile_kernel(
     __builtin_amdgcn_sched_barrier(0);
     fill_x(4 * g0 + 2, xa2);
     load_w(4 * g0 + 2, blk[2]);
+    __builtin_amdgcn_sched_barrier(0);
     put_w(blk[0], wa0, wide_c);
     if constexpr (kLook) bad = unfit(4 * g0, blk[0]);
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"(2 * kXLoads) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"(2 * (kXLoads + 2)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" : : : "memory");
     bool good = true;
@@ -286,8 +295,9 @@ __global__ __launch_bounds__(256) void mx_pad_rows_kernel(const uint16_t *__rest
                                                     v[4] | (v[5] << 16), v[6] | (v[7] << 16));
 }
 
+// Fitted to 4096 x 4096, 4096 x 11008 and 11008 x 4096 from 32 to 2048 rows.
 constexpr TileShape kShapes[] = {
-    {2, 2, 2, 1, 2.0, 2.4}, {1, 2, 1, 2, 1.6, 1.2}, {1, 1, 1, 2, 1.4, 0.7}};
+    {2, 2, 2, 1, 3.0, 0.9}, {1, 2, 1, 2, 2.4, 1.2}, {1, 1, 1, 2, 2.1, 0.5}};
 
 TilePlan plan_of(const MxDesc &W, int64_t batch) {
   return plan_tiles(kShapes, W.cols, batch, (W.rows + 255) / 256);
