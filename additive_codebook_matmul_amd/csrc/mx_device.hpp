@@ -75,6 +75,33 @@ __device__ __forceinline__ void split_f16(const uint4 &x, uint4 &hi, uint4 &lo) 
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// Scale bytes of 16 consecutive blocks of a row, from block `blk` on: `at` is
+// the row's first byte in rs, whose base is a whole word and which ends with
+// the matrix's (or the tile's) last byte. Past the row's last block the bytes are
+// that block's or 127.
+__device__ __forceinline__ uint4 mx_scales16(Rsrc rs, uint32_t at, int blk, int nb) {
+  const int left = nb - blk;
+  const uint32_t from = at + (uint32_t)blk, to = from & ~3u;
+  if ((nb & 3) == 0) {  // words lie whole in a row
+    uint4 v = buf_load16(rs, from);
+    if (left <= 12) v.w = 0x7F7F7F7Fu;
+    if (left <= 8) v.z = 0x7F7F7F7Fu;
+    if (left <= 4) v.y = 0x7F7F7F7Fu;
+    return v;
+  }
+  if (left >= 19) {  // five words hold them, and end inside the row
+    const uint4 v = buf_load16(rs, to);
+    const uint32_t e = buf_load4(rs, to + 16), by = from & 3u;
+    return make_uint4(__builtin_amdgcn_alignbyte(v.y, v.x, by), __builtin_amdgcn_alignbyte(v.z, v.y, by),
+                      __builtin_amdgcn_alignbyte(v.w, v.z, by), __builtin_amdgcn_alignbyte(e, v.w, by));
+  }
+  uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int u = 0; u < 16; ++u)
+    v[u >> 2] |= buf_load_u8(rs, at + (uint32_t)max(0, min(blk + u, nb - 1))) << (8 * (u & 3));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // v_mfma_f32_16x16x32 / 32x32x16 on halves of type T.
 template <MxType T>
 __device__ __forceinline__ float4_t mx_mfma16(const uint4 &a, const uint4 &b, float4_t c) {

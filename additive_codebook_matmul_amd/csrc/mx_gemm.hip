@@ -1,14 +1,7 @@
-// Product of half activations with microscaled weights: y = x . W^T.
-//
-// A wavefront takes chunks of 128 inputs of 16-row tiles. Lane (r, q) = (lane
-// % 16, lane / 16) loads the 16 bytes that hold block q of the chunk of row r
-// (32 codes, one scale byte) and expands them with v_cvt_scalef32_pk into four
-// operands of v_mfma_f32_16x16x32: step s multiplies codes 8 s .. 8 s + 7 of
-// every block, so the activation operand of lane (t, q) is the 16 bytes of
-// inputs 32 q + 8 s of token t. The sum over K does not care which inputs meet
-// in one instruction, so no code ever changes lanes. The wavefronts of a
-// workgroup split the chunks and add their float32 sums through LDS in a fixed
-// order.
+// Product of half activations with microscaled weights: y = x . W^T, for the
+// batches of token generation. One row of activations: mx_rows_kernel; up to
+// sixteen: mx_skinny_kernel; where its tiles are faster, and above: the tile
+// kernels of mx_gemm_tile.hip.
 #include <algorithm>
 
 #include "mx_device.hpp"
@@ -28,120 +21,244 @@ struct Group {
   int n;
 };
 
-template <MxType T, int RT, int NT, int NW>
+// Up to 16 rows of activations against tiles of 16 rows of W, K shared by the
+// NW wavefronts of a workgroup in groups of 512 inputs (16 blocks, 256 bytes of
+// a row): lane (r, q) = (lane % 16, lane / 16) loads the 16 bytes that hold block
+// 4 c + q of the group for c = 0 .. 3, and the group's 16 scale bytes of row r,
+// and expands the codes into operands of v_mfma_f32_16x16x32: instruction s of
+// chunk c multiplies codes 8 s .. 8 s + 7 of every block, so its activation
+// operand is the 16 bytes of inputs 8 s of the same block of the lane's token.
+// (The sum over K does not care which inputs meet in one instruction, so no
+// code changes lanes.) The wavefronts' float32 sums meet in LDS in a fixed
+// order. What bounds it are requests, a 128-byte line each: scales byte by byte
+// cost as many as the codes (4096 x 4096 at 2 rows 5.1 us, 11008 x 4096 at 8
+// 14.9; this 4.5 and 14.4).
+template <MxType T, int NW>
 __global__ __launch_bounds__(NW * 64) void mx_skinny_kernel(const Group g, const int batch) {
-  extern __shared__ __attribute__((aligned(16))) float4_t red[];  // [NW][RT * NT][64]
+  __shared__ __attribute__((aligned(16))) float4_t red[NW * 64];
   int li = 0;
   while (li + 1 < g.n && (int)blockIdx.x >= g.first[li + 1]) ++li;
   const Group::Item &L = g.item[li];
-  const int row0 = ((int)blockIdx.x - g.first[li]) * (16 * RT);
-  const int tok0 = (int)blockIdx.y * (16 * NT);
+  const int row0 = ((int)blockIdx.x - g.first[li]) * 16;
   const int rows = L.rows, cols = L.cols;
   const int nb = cols >> 5;
+  const uint32_t half = (uint32_t)cols >> 1;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q = lane >> 4;
 
-  // resources that end with the tile's last row: rows past it read zero
-  const int tile_rows = min(16 * RT, rows - row0);
-  const int tile_toks = min(16 * NT, batch - tok0);
-  const Rsrc crs = make_rsrc(L.codes + (int64_t)row0 * (cols >> 1), (uint32_t)tile_rows * (cols >> 1));
-  const Rsrc srs = make_rsrc(L.scales + (int64_t)row0 * nb, (uint32_t)tile_rows * nb);
-  const Rsrc xrs = make_rsrc(L.x + (int64_t)tok0 * cols, (uint32_t)tile_toks * cols * 2u);
+  // resources that end with the tile's last row: rows past it read zero (their
+  // scales are those of the last one, and not stored results theirs)
+  const int tile_rows = __builtin_amdgcn_readfirstlane(min(16, rows - row0));
+  const int base = (int)(((int64_t)row0 * nb) & 3);
+  const Rsrc crs = make_rsrc(L.codes + (int64_t)row0 * half, (uint32_t)tile_rows * half);
+  const Rsrc srs = make_rsrc(L.scales + (int64_t)row0 * nb - base, (uint32_t)tile_rows * nb + base);
+  const Rsrc xrs = make_rsrc(L.x, (uint32_t)batch * cols * 2u);
+  const uint32_t srow = (uint32_t)min(r16, tile_rows - 1) * nb + base;
 
-  float4_t acc[RT][NT];
+  float4_t acc = {0.f, 0.f, 0.f, 0.f};
+  for (int gr = wave; 16 * gr < nb; gr += NW) {
+    uint4 w[4], x[4][4];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
-
-  const int chunks = (nb + 3) >> 2;
-  for (int c = wave; c < chunks; c += NW) {
-    const int blk = 4 * c + q;
-    const bool in = blk < nb;
-    uint4 w[RT];
-    uint32_t sb[RT];
-    uint4 xv[NT][4];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int r = 16 * i + r16;
-      w[i] = buf_load16(crs, in ? (uint32_t)r * (cols >> 1) + (uint32_t)blk * 16u : kMxOOB);
-      sb[i] = buf_load_u8(srs, in ? (uint32_t)r * nb + (uint32_t)blk : kMxOOB);
-      sb[i] = in && r < tile_rows ? sb[i] : 127u;
+    for (int c = 0; c < 4; ++c) {
+      const int blk = 16 * gr + 4 * c + q;
+      w[c] = buf_load16_nt(crs, blk < nb ? (uint32_t)r16 * half + (uint32_t)blk * 16u : kMxOOB);
     }
+    const uint4 sc = mx_scales16(srs, srow, 16 * gr, nb);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int c = 0; c < 4; ++c) {
+      const int blk = 16 * gr + 4 * c + q;
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        xv[j][s] = buf_load16(
-            xrs, in ? (uint32_t)(16 * j + r16) * cols * 2u + (uint32_t)blk * 64u + 16u * s : kMxOOB);
-    bool fits = true;
-    if constexpr (T == MxType::kF16) {
-#pragma unroll
-      for (int i = 0; i < RT; ++i) fits = fits && mx_fits_f16(sb[i]);
-      fits = __all(fits);
+        x[c][s] = buf_load16(xrs, blk < nb ? (uint32_t)r16 * cols * 2u + (uint32_t)blk * 64u + 16u * s : kMxOOB);
     }
-    if (fits) {
+    const uint32_t sb[4] = {(sc.x >> (8 * q)) & 0xFFu, (sc.y >> (8 * q)) & 0xFFu, (sc.z >> (8 * q)) & 0xFFu,
+                            (sc.w >> (8 * q)) & 0xFFu};
+    bool fits = true;
+    if constexpr (T == MxType::kF16)
+      fits = __all(mx_fits_f16(sb[0]) & mx_fits_f16(sb[1]) & mx_fits_f16(sb[2]) & mx_fits_f16(sb[3]));
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const float sc = mx_scale(sb[i]);
-        const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t ww[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+      const float sv = mx_scale(sb[c]);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const uint4 a = mx_decode8<T>(ww[s], sc);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma16<T>(a, xv[j][s], acc[i][j]);
+      for (int s = 0; s < 4; ++s) {
+        if (fits) {
+          acc = mx_mfma16<T>(mx_decode8<T>(ww[s], sv), x[c][s], acc);
+        } else {
+          // scales that float16 weights cannot take: the same product in
+          // bfloat16, which holds every weight, with x split exactly in two
+          uint4 hi, lo;
+          split_f16(x[c][s], hi, lo);
+          const uint4 a = mx_decode8<MxType::kBF16>(ww[s], sv);
+          acc = mx_mfma16<MxType::kBF16>(a, hi, acc);
+          acc = mx_mfma16<MxType::kBF16>(a, lo, acc);
         }
       }
-    } else {
-      // scales that float16 weights cannot take: the same product in
-      // bfloat16, which holds every weight, with x split exactly in two
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          uint4 hi, lo;
-          split_f16(xv[j][s], hi, lo);
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            const uint4 a = mx_decode8<MxType::kBF16>(ww[s], mx_scale(sb[i]));
-            acc[i][j] = mx_mfma16<MxType::kBF16>(a, hi, acc[i][j]);
-            acc[i][j] = mx_mfma16<MxType::kBF16>(a, lo, acc[i][j]);
-          }
-        }
     }
   }
 
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) red[(wave * (RT * NT) + i * NT + j) * 64 + lane] = acc[i][j];
+  red[threadIdx.x] = acc;
   __syncthreads();
-  // lane (t, q) of tile (i, j) holds rows 4 q .. 4 q + 3 of token t
-  const bool packed = (rows & 3) == 0;
-  for (int e = threadIdx.x; e < RT * NT * 64; e += NW * 64) {
-    float4_t v = red[e];
+  // lane (t, q) holds rows 4 q .. 4 q + 3 of token t
+  if (threadIdx.x < 64) {
+    float4_t v = red[lane];
 #pragma unroll
-    for (int u = 1; u < NW; ++u) v += red[u * (RT * NT * 64) + e];
-    const int l = e & 63, i = (e >> 6) / NT, j = (e >> 6) % NT;
-    const int tok = tok0 + 16 * j + (l & 15);
-    if (tok < batch) store4<T>(L.y + (int64_t)tok * rows, row0 + 16 * i + 4 * (l >> 4), rows, v, packed);
+    for (int u = 1; u < NW; ++u) v += red[u * 64 + lane];
+    if (r16 < batch) store4<T>(L.y + (int64_t)r16 * rows, row0 + 4 * q, rows, v, (rows & 3) == 0);
   }
 }
 
-template <MxType T, int RT, int NT, int NW>
-hipError_t launch_skinny(Group &g, int64_t batch, hipStream_t stream) {
+template <MxType T, int NW> hipError_t launch_skinny(Group &g, int batch, hipStream_t stream) {
   int blocks = 0;
   for (int i = 0; i < g.n; ++i) {
     g.first[i] = blocks;
-    blocks += (g.item[i].rows + 16 * RT - 1) / (16 * RT);
+    blocks += (g.item[i].rows + 15) / 16;
   }
   g.first[g.n] = blocks;
-  const dim3 grid((unsigned)blocks, (unsigned)((batch + 16 * NT - 1) / (16 * NT)));
-  hipLaunchKernelGGL((mx_skinny_kernel<T, RT, NT, NW>), grid, dim3(NW * 64),
-                     NW * RT * NT * 64 * sizeof(float4_t), stream, g, (int)batch);
+  hipLaunchKernelGGL((mx_skinny_kernel<T, NW>), dim3((unsigned)blocks), dim3(NW * 64), 0, stream, g, batch);
   return hipGetLastError();
+}
+
+// One row of activations: the weights' bytes bound the product, so a wavefront
+// reads whole rows, R at a time, 1 KiB of codes (64 blocks of 32, a block a lane) and
+// their 64 scale bytes each (28672 x 8192 27 us, 4.6 TB/s; in 16-row tiles whose
+// wavefronts read 64-byte pieces of rows 42).
+//   * x lies in LDS, up to kSegment inputs of it, read by all wavefronts of the
+//     workgroup; a lane takes the 64 bytes of its own block for every row.
+//   * v_mfma_f32_16x16x32 sums over the lanes as well: lane (m, q) = (lane % 16,
+//     lane / 16) gives eight codes of its block and eight inputs of the same
+//     block, so that the result's diagonal (m, m) holds the sums of the four
+//     lanes m, 16 + m, ..; the rest of the result is of no use, and the
+//     instruction still outruns the loads (64 bytes of codes a clock and CU). The 16 diagonal places are added at the end of a row.
+// Chunks of x are permuted (x_place), so that the 16 lanes of an LDS pass touch
+// 16 distinct groups of banks.
+constexpr int kRowThreads = 256;
+constexpr int kSegment = 16384;  // inputs in LDS
+__device__ __forceinline__ uint32_t x_place(int blk, int s) {
+  return (uint32_t)blk * 64u + (uint32_t)((s ^ ((blk >> 2) & 3)) << 4);
+}
+
+template <MxType T, int R>
+__global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g) {
+  constexpr int kBlocks = kSegment / 32, kChunks = kBlocks / 64;
+  __shared__ __attribute__((aligned(16))) uint8_t xs[kSegment * 2];  // [kBlocks][64 bytes]
+  int li = 0;
+  while (li + 1 < g.n && (int)blockIdx.x >= g.first[li + 1]) ++li;
+  const Group::Item &L = g.item[li];
+  const int rows = L.rows, nb = L.cols >> 5;
+  const uint32_t half = (uint32_t)L.cols >> 1;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row0 = (((int)blockIdx.x - g.first[li]) * (kRowThreads / 64) + wave) * R;
+  // resources that end with the wavefront's last row: rows past it read zero
+  const int mine = __builtin_amdgcn_readfirstlane(max(0, min(R, rows - row0)));
+  const Rsrc crs = make_rsrc(L.codes + (int64_t)(mine ? row0 : 0) * half, (uint32_t)mine * half);
+  const Rsrc srs = make_rsrc(L.scales + (int64_t)(mine ? row0 : 0) * nb, (uint32_t)mine * nb);
+
+  float4_t acc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r] = float4_t{0.f, 0.f, 0.f, 0.f};
+  uint4 w[2][R];
+  uint32_t sb[2][R];
+  auto load = [&](int c, uint4 (&wv)[R], uint32_t (&sv)[R]) __attribute__((always_inline)) {
+    const int blk = 64 * c + lane;
+    const bool in = blk < nb;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      wv[r] = buf_load16_nt(crs, in ? (uint32_t)r * half + (uint32_t)blk * 16u : kMxOOB);
+      sv[r] = buf_load_u8(srs, in ? (uint32_t)r * nb + (uint32_t)blk : kMxOOB);
+    }
+  };
+  auto compute = [&](int c, const uint4 (&wv)[R], const uint32_t (&sv)[R]) __attribute__((always_inline)) {
+    const int lb = (c % kChunks) * 64 + lane;  // block of the segment
+    bool fits = true;
+    if constexpr (T == MxType::kF16) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) fits = fits & (mx_fits_f16(sv[r]) | (64 * c + lane >= nb) | (r >= mine));
+      fits = __all(fits);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(xs + x_place(lb, s));
+      if (fits) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t ww[4] = {wv[r].x, wv[r].y, wv[r].z, wv[r].w};
+          acc[r] = mx_mfma16<T>(mx_decode8<T>(ww[s], mx_scale(sv[r])), x, acc[r]);
+        }
+      } else {
+        // scales that float16 weights cannot take: the same product in
+        // bfloat16, which holds every weight, with x split exactly in two
+        uint4 hi, lo;
+        split_f16(x, hi, lo);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t ww[4] = {wv[r].x, wv[r].y, wv[r].z, wv[r].w};
+          const uint4 a = mx_decode8<MxType::kBF16>(ww[s], mx_scale(sv[r]));
+          acc[r] = mx_mfma16<MxType::kBF16>(a, hi, acc[r]);
+          acc[r] = mx_mfma16<MxType::kBF16>(a, lo, acc[r]);
+        }
+      }
+    }
+  };
+
+  const int chunks = (nb + 63) >> 6;
+  load(0, w[0], sb[0]);
+  for (int c0 = 0; c0 < chunks; c0 += kChunks) {  // a segment of x
+    if (c0 > 0) __syncthreads();
+    const int blocks = min(kBlocks, ((nb - 64 * c0 + 63) >> 6) << 6);  // whole chunks of it
+    for (int k = threadIdx.x; k < blocks * 4; k += kRowThreads) {
+      const int blk = 64 * c0 + (k >> 2);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (blk < nb) v = *reinterpret_cast<const uint4 *>(L.x + (int64_t)blk * 32 + 8 * (k & 3));
+      *reinterpret_cast<uint4 *>(xs + x_place(k >> 2, k & 3)) = v;
+    }
+    __syncthreads();
+    const int c1 = min(chunks, c0 + kChunks);
+    for (int c = c0; c < c1; ++c) {
+      load(c + 1, w[1], sb[1]);
+      compute(c, w[0], sb[0]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        w[0][r] = w[1][r];
+        sb[0][r] = sb[1][r];
+      }
+    }
+  }
+
+  // the diagonal: place (m, m) is register m % 4 of lane 16 (m / 4) + m
+  const bool diagonal = ((lane >> 2) & 3) == (lane >> 4);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float4_t a = acc[r];
+    const float v = (lane & 2) ? ((lane & 1) ? a[3] : a[2]) : ((lane & 1) ? a[1] : a[0]);
+    const float sum = wave_sum_to_lane63(diagonal ? v : 0.0f);
+    if (lane == 63 && r < mine) L.y[row0 + r] = (uint16_t)f2t<T>(sum);
+  }
+}
+
+template <MxType T, int R> hipError_t launch_rows(Group &g, hipStream_t stream) {
+  constexpr int kRows = R * (kRowThreads / 64);
+  int blocks = 0;
+  for (int i = 0; i < g.n; ++i) {
+    g.first[i] = blocks;
+    blocks += (g.item[i].rows + kRows - 1) / kRows;
+  }
+  g.first[g.n] = blocks;
+  hipLaunchKernelGGL((mx_rows_kernel<T, R>), dim3((unsigned)blocks), dim3(kRowThreads), 0, stream, g);
+  return hipGetLastError();
+}
+
+// Rows of W a wavefront reads at a time: more keep more bytes under way, fewer
+// spread a short matrix over the chip (1, 2, 4 rows: 1024 x 8192 5.2, 5.6, 6.1
+// us; 4096 x 4096 4.9, 4.7, 5.0; three of them at once 11.6, 8.9, 7.5).
+template <MxType T> hipError_t rows_as(Group &g, hipStream_t stream) {
+  int64_t rows = 0;
+  for (int i = 0; i < g.n; ++i) rows += g.item[i].rows;
+  if (rows >= 8192) return launch_rows<T, 4>(g, stream);
+  if (rows >= 2048) return launch_rows<T, 2>(g, stream);
+  return launch_rows<T, 1>(g, stream);
 }
 
 Group::Item item_of(const MxDesc &W, const void *x, void *y) {
@@ -149,12 +266,31 @@ Group::Item item_of(const MxDesc &W, const void *x, void *y) {
           (int)W.rows, (int)W.cols};
 }
 
-template <MxType T>
-hipError_t gemm_as(const MxDesc &W, const void *x, int64_t batch, void *y, hipStream_t stream) {
-  Group g;
-  g.n = 1;
-  g.item[0] = item_of(W, x, y);
-  return launch_skinny<T, 1, 1, 8>(g, batch, stream);
+constexpr int kSkinnyWaves = 8;
+
+// From two rows on, where the tile kernel is the faster: the skinny one takes
+// 1.1 ns and 0.1 ns a row of activations for 16 rows of W and a group of K,
+// spread over the chip, or, with few rows, 1.8 us and 0.2 us a row for each turn
+// of its wavefronts (fitted to 1024 x 8192 .. 28672 x 8192 from 2 to 16 rows:
+// 4096 x 4096 at 8 rows 6.3 us against 9.6, 28672 x 8192 59 against 35).
+bool tiles_pay(const MxDesc &W, int64_t batch) {
+  if (batch > 16) return true;
+  if (batch == 1) return false;
+  const double groups = (double)((W.cols / 32 + 15) / 16), tiles = (double)((W.rows + 15) / 16);
+  const double turns = (double)(int64_t)((groups + kSkinnyWaves - 1) / kSkinnyWaves);
+  const double us = std::max(3.0 + tiles * groups * (1.1e-3 + 0.1e-3 * (double)batch),
+                             2.5 + turns * (1.8 + 0.2 * (double)batch));
+  return mx_gemm_tile_us(W, batch) < us;
+}
+
+// Up to 16 rows of activations, without the tile kernel.
+template <MxType T> hipError_t few_as(Group &g, int batch, hipStream_t stream) {
+  return batch == 1 ? rows_as<T>(g, stream) : launch_skinny<T, kSkinnyWaves>(g, batch, stream);
+}
+
+hipError_t launch_few(Group &g, int batch, MxType type, hipStream_t stream) {
+  if (g.n == 0) return hipSuccess;
+  return type == MxType::kF16 ? few_as<MxType::kF16>(g, batch, stream) : few_as<MxType::kBF16>(g, batch, stream);
 }
 
 }  // namespace
@@ -162,21 +298,29 @@ hipError_t gemm_as(const MxDesc &W, const void *x, int64_t batch, void *y, hipSt
 hipError_t launch_mx_gemv_batched(const MxDesc *W, const void *const *x, void *const *y, int n,
                                   int batch, MxType type, hipStream_t stream) {
   Group g;
-  g.n = n;
-  for (int i = 0; i < n; ++i) g.item[i] = item_of(W[i], x[i], y[i]);
-  return type == MxType::kF16 ? launch_skinny<MxType::kF16, 1, 1, 8>(g, batch, stream)
-                              : launch_skinny<MxType::kBF16, 1, 1, 8>(g, batch, stream);
+  g.n = 0;
+  for (int i = 0; i < n; ++i) {
+    if (tiles_pay(W[i], batch)) {
+      const hipError_t e = launch_mx_gemm_tile(W[i], x[i], batch, y[i], type, nullptr, stream);
+      if (e != hipSuccess) return e;
+    } else {
+      g.item[g.n++] = item_of(W[i], x[i], y[i]);
+    }
+  }
+  return launch_few(g, batch, type, stream);
 }
 
 int64_t mx_gemm_ws_bytes(const MxDesc &W, int64_t batch) {
-  return batch < kMxTileBatch ? 0 : mx_gemm_tile_ws_bytes(W, batch);
+  return tiles_pay(W, batch) ? mx_gemm_tile_ws_bytes(W, batch) : 0;
 }
 
 hipError_t launch_mx_gemm(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
                           void *ws, hipStream_t stream) {
-  if (batch >= kMxTileBatch) return launch_mx_gemm_tile(W, x, batch, y, type, ws, stream);
-  return type == MxType::kF16 ? gemm_as<MxType::kF16>(W, x, batch, y, stream)
-                              : gemm_as<MxType::kBF16>(W, x, batch, y, stream);
+  if (tiles_pay(W, batch)) return launch_mx_gemm_tile(W, x, batch, y, type, ws, stream);
+  Group g;
+  g.n = 1;
+  g.item[0] = item_of(W, x, y);
+  return launch_few(g, (int)batch, type, stream);
 }
 
 }  // namespace aqlm

@@ -251,6 +251,10 @@ template <MxType T> hipError_t tile_as(const TileShape &c, const TileArgs &A, hi
 
 }  // namespace
 
+double mx_gemm_mx_tile_us(const MxDesc &W, int64_t batch) {
+  return std::max(plan_of(W, batch).us, mx_read_us(W));
+}
+
 int64_t mx_gemm_mx_tile_ws_bytes(const MxDesc &W, int64_t batch) { return plan_of(W, batch).ws_bytes(); }
 
 hipError_t launch_mx_gemm_mx_tile(const MxDesc &W, const MxDesc &x, void *y, MxType type, void *ws,

@@ -16,8 +16,8 @@
 //     128-byte lines: L2 gives about 30 TB/s in such segments, a half in ones
 //     of 64 bytes, a quarter of 32, an eighth of 16, since a request costs its
 //     line. (Each lane loading its own row's 16 bytes of codes and a byte of
-//     scales took 190 us for 2048 x 11008 x 4096, 32-byte segments of codes 174,
-//     this @@.) Activations go straight to LDS three steps ahead, one of four
+//     scales took 190 us for 2048 x 11008 x 4096, 32-byte segments of codes
+//     179, this 158.) Activations go straight to LDS three steps ahead, one of four
 //     stages; codes four steps at a time, up to eight ahead, one of two;
 //     scales 64 steps at a time, through registers.
 //   * Chunks of 16 bytes are permuted within a row of 128 bytes on their way
@@ -291,7 +291,7 @@ constexpr TileShape kShapes[] = {
     {2, 2, 2, 1, 2.64, 4.88}, {1, 2, 1, 2, 2.40, 2.88}, {1, 1, 1, 2, 2.00, 1.44}};
 
 TilePlan plan_of(const MxDesc &W, int64_t batch) {
-  return plan_tiles(kShapes, W.rows, batch, (W.cols / 32 + 15) / 16);
+  return plan_tiles(kShapes, W.rows, batch, (W.cols / 32 + 15) / 16, batch <= 8 ? 1 : 8);
 }
 
 template <MxType T, int RT, int NT, int TW, int KW>
@@ -312,6 +312,10 @@ template <MxType T> hipError_t tile_as(const TileShape &c, const TileArgs &A, hi
 }
 
 }  // namespace
+
+double mx_gemm_tile_us(const MxDesc &W, int64_t batch) {
+  return std::max(plan_of(W, batch).us, mx_read_us(W));
+}
 
 int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch) { return plan_of(W, batch).ws_bytes(); }
 

@@ -15,6 +15,12 @@ struct MxDesc {
   const uint8_t *scales;  // [rows][cols/32]
 };
 
+// Modelled time (us) that reading the weights takes any kernel: about 5.2 TB/s
+// and what passes around that.
+inline double mx_read_us(const MxDesc &W) {
+  return 3.0 + (double)(W.rows * (W.cols / 2 + W.cols / 32)) / 5.2e6;
+}
+
 // Most layers of one grouped launch.
 constexpr int kMxGroup = 16;
 
@@ -29,14 +35,17 @@ hipError_t launch_mx_gemv_batched(const MxDesc *W, const void *const *x, void *c
 int64_t mx_gemm_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_gemm(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
                           void *ws, hipStream_t stream);
-// From kMxTileBatch rows on (mx_gemm_tile.hip, mx_gemm_mx_tile.hip).
-constexpr int kMxTileBatch = 17;
-int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch);
-hipError_t launch_mx_gemm_tile(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
-                               void *ws, hipStream_t stream);
 int64_t mx_gemm_mx_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_gemm_mx(const MxDesc &W, const MxDesc &x, void *y, MxType type, void *ws,
                              hipStream_t stream);
+// Their tile kernels (mx_gemm_tile.hip, mx_gemm_mx_tile.hip): modelled duration
+// in us, workspace, launch. Up to 8 rows of half activations K is not split
+// and no workspace needed.
+double mx_gemm_tile_us(const MxDesc &W, int64_t batch);
+int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch);
+hipError_t launch_mx_gemm_tile(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
+                               void *ws, hipStream_t stream);
+double mx_gemm_mx_tile_us(const MxDesc &W, int64_t batch);
 int64_t mx_gemm_mx_tile_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_gemm_mx_tile(const MxDesc &W, const MxDesc &x, void *y, MxType type, void *ws,
                                   hipStream_t stream);

@@ -271,23 +271,25 @@ struct TilePlan {
   TileShape shape;
   int splits, groups_per_split;
   int64_t row_tiles, tok_tiles;
+  double us;  // modelled
   int64_t ws_bytes() const {
     if (splits == 1) return 0;
     return row_tiles * tok_tiles * splits * (int64_t)(shape.rt * shape.nt * shape.tw * kRowWaves) * 4096;
   }
 };
 
+// `most`: the largest number of splits (1: no workspace).
 template <int N>
-TilePlan plan_tiles(const TileShape (&shapes)[N], int64_t rows, int64_t batch, int64_t groups) {
+TilePlan plan_tiles(const TileShape (&shapes)[N], int64_t rows, int64_t batch, int64_t groups,
+                    int most = 8) {
   TilePlan best{};
-  double least = 0;
   for (const TileShape &c : shapes) {
     TilePlan p{};
     p.shape = c;
     p.row_tiles = (rows + 32 * kRowWaves * c.rt - 1) / (32 * kRowWaves * c.rt);
     p.tok_tiles = (batch + 32 * c.nt * c.tw - 1) / (32 * c.nt * c.tw);
     const int64_t tiles = p.row_tiles * p.tok_tiles;
-    for (int s = 1; s <= 8; ++s) {
+    for (int s = 1; s <= most; ++s) {
       p.groups_per_split = (int)((groups + s - 1) / s);
       p.splits = (int)((groups + p.groups_per_split - 1) / p.groups_per_split);
       if (p.splits != s || (s > 1 && tiles * s > 256)) break;
@@ -295,10 +297,8 @@ TilePlan plan_tiles(const TileShape (&shapes)[N], int64_t rows, int64_t batch, i
       const double group = whole * (c.a + c.b) + (rest > 0 ? c.a + c.b * rest : 0.0);
       double us = 4.0 + (double)((p.groups_per_split + c.kw - 1) / c.kw) * group;
       if (s > 1) us += 2.5 + (double)p.ws_bytes() * 2.0 / 4e6;
-      if (best.splits == 0 || us < least) {
-        least = us;
-        best = p;
-      }
+      p.us = us;
+      if (best.splits == 0 || us < best.us) best = p;
     }
   }
   return best;
