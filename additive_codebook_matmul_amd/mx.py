@@ -18,7 +18,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._lib import _check, _stream_handle, load_library
+from ._lib import _check, load_library
 
 MX_BLOCK = 32
 MX_MAX_DIM = 1 << 21
@@ -61,25 +61,27 @@ def _lib() -> ctypes.CDLL:
     return _ready
 
 
-class _on:
-    """The tensors' device as the current one for the call (no work if it is already)."""
-    __slots__ = ("index", "before")
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, device: torch.device):
-        self.index = device.index
 
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _call(device: torch.device, fn, *args) -> None:
+    """fn(*args, stream) on the device's current stream, with the device current."""
+    index, before = device.index, _current_device()
+    if before == index:
+        status = fn(*args, _current_stream(index))
+    else:
+        torch.cuda.set_device(index)
+        try:
+            status = fn(*args, _current_stream(index))
+        finally:
+            torch.cuda.set_device(before)
+    if status:
+        _check(status)
 
 
 def _check_dense(t: torch.Tensor, what: str, dtypes, shape=None) -> None:
-    if t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous():
+    if t.dtype not in dtypes or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
         names = ", ".join(str(d).replace("torch.", "") for d in dtypes)
         raise ValueError(f"{what} must be a contiguous 2-D tensor on the GPU, of type {names}")
     if shape is not None and tuple(t.shape) != tuple(shape):
@@ -123,10 +125,8 @@ def mx_quantize(x: torch.Tensor, rule: str = "floor",
         raise ValueError("cols must be a multiple of 32")
     codes = _output(None if out is None else out[0], (rows, cols // 2), torch.uint8, x.device)
     scales = _output(None if out is None else out[1], (rows, cols // MX_BLOCK), torch.uint8, x.device)
-    with _on(x.device):
-        _check(_lib().aqlm_mx_quantize(x.data_ptr(), MX_TYPES[x.dtype], rows, cols, MX_RULES[rule],
-                                       codes.data_ptr(), scales.data_ptr(),
-                                       _stream_handle(x.device)))
+    _call(x.device, _lib().aqlm_mx_quantize, x.data_ptr(), MX_TYPES[x.dtype], rows, cols,
+          MX_RULES[rule], codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -138,9 +138,7 @@ def mx_dequant(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = t
         raise ValueError("dtype must be float16, bfloat16 or float32")
     W = _output(out, (rows, cols), dtype, codes.device)
     m = MxMatrixStruct(rows, cols, codes.data_ptr(), scales.data_ptr())
-    with _on(codes.device):
-        _check(_lib().aqlm_mx_dequant(ctypes.byref(m), MX_TYPES[dtype], W.data_ptr(),
-                                      _stream_handle(codes.device)))
+    _call(codes.device, _lib().aqlm_mx_dequant, ctypes.byref(m), MX_TYPES[dtype], W.data_ptr())
     return W
 
 
@@ -159,6 +157,7 @@ class MxLayer:
         self.device = codes.device
         self._struct = MxMatrixStruct(rows, cols, codes.data_ptr(), scales.data_ptr())
         self._ref = ctypes.byref(self._struct)
+        self._ws_bytes = {}  # (operator, batch) -> bytes: a rule of sizes alone
 
     @classmethod
     def quantize(cls, W: torch.Tensor, rule: str = "floor") -> "MxLayer":
@@ -178,9 +177,15 @@ class MxLayer:
 
     def workspace_bytes(self, batch: int, op: str = "gemm") -> int:
         """Device workspace of gemm, gemm_mx or grad_input at this batch (0: none)."""
-        n = ctypes.c_int64(0)
-        _check(getattr(_lib(), f"aqlm_mx_{op}_workspace_size")(self._ref, batch, ctypes.byref(n)))
-        return n.value
+        need = self._ws_bytes.get((op, batch))
+        if need is None:
+            n = ctypes.c_int64(0)
+            _check(getattr(_lib(), f"aqlm_mx_{op}_workspace_size")(self._ref, batch, ctypes.byref(n)))
+            need = n.value
+            if len(self._ws_bytes) >= 1024:
+                self._ws_bytes.clear()
+            self._ws_bytes[(op, batch)] = need
+        return need
 
     def _workspace(self, batch: int, op: str) -> Tuple[Optional[torch.Tensor], Optional[int], int]:
         need = self.workspace_bytes(batch, op)
@@ -199,10 +204,9 @@ class MxLayer:
         self._check_half(x, "x", self.in_features)
         batch = x.shape[0]
         y = _output(out, (batch, self.out_features), x.dtype, self.device)
-        with _on(self.device):
-            ws, ptr, need = self._workspace(batch, "gemm")
-            _check(_lib().aqlm_mx_gemm(self._ref, x.data_ptr(), batch, y.data_ptr(),
-                                       MX_TYPES[x.dtype], ptr, need, _stream_handle(self.device)))
+        ws, ptr, need = self._workspace(batch, "gemm")
+        _call(self.device, _lib().aqlm_mx_gemm, self._ref, x.data_ptr(), batch, y.data_ptr(),
+              MX_TYPES[x.dtype], ptr, need)
         return y
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
@@ -221,17 +225,33 @@ class MxLayer:
             raise ValueError("dtype must be float16 or bfloat16")
         y = _output(out, (batch, self.out_features), dtype, self.device)
         xs = MxMatrixStruct(batch, cols, codes.data_ptr(), scales.data_ptr())
-        with _on(self.device):
-            ws, ptr, need = self._workspace(batch, "gemm_mx")
-            _check(_lib().aqlm_mx_gemm_mx(self._ref, ctypes.byref(xs), y.data_ptr(),
-                                          MX_TYPES[dtype], ptr, need, _stream_handle(self.device)))
+        ws, ptr, need = self._workspace(batch, "gemm_mx")
+        _call(self.device, _lib().aqlm_mx_gemm_mx, self._ref, ctypes.byref(xs), y.data_ptr(),
+              MX_TYPES[dtype], ptr, need)
         return y
 
     def forward_mx(self, x: torch.Tensor, rule: str = "floor") -> torch.Tensor:
         """y = Q(x) . W^T: the activations quantised by mx_quantize, then gemm_mx."""
         self._check_half(x, "x", self.in_features)
-        codes, scales = mx_quantize(x, rule)
-        return self.gemm_mx(codes, scales, x.dtype)
+        if rule not in MX_RULES:
+            raise ValueError(f"rule must be one of {sorted(MX_RULES)}")
+        batch, cols = x.shape
+        y = torch.empty((batch, self.out_features), dtype=x.dtype, device=self.device)
+        # one buffer: codes, scales (both a multiple of 16 bytes from the start
+        # or to the next), the product's workspace
+        n_codes = batch * (cols // 2)
+        at_ws = (n_codes + batch * (cols // MX_BLOCK) + 255) // 256 * 256
+        need = self.workspace_bytes(batch, "gemm_mx")
+        buf = torch.empty(at_ws + need, dtype=torch.uint8, device=self.device)
+        codes = buf.data_ptr()
+        kind = MX_TYPES[x.dtype]
+        lib = _lib()
+        _call(self.device, lib.aqlm_mx_quantize, x.data_ptr(), kind, batch, cols, MX_RULES[rule],
+              codes, codes + n_codes)
+        xs = MxMatrixStruct(batch, cols, codes, codes + n_codes)
+        _call(self.device, lib.aqlm_mx_gemm_mx, self._ref, ctypes.byref(xs), y.data_ptr(), kind,
+              codes + at_ws if need else None, need)
+        return y
 
     def grad_input(self, dy: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """dx = dy . W: the gradient of forward(x) with respect to x, and the
@@ -239,11 +259,9 @@ class MxLayer:
         self._check_half(dy, "dy", self.out_features)
         batch = dy.shape[0]
         dx = _output(out, (batch, self.in_features), dy.dtype, self.device)
-        with _on(self.device):
-            ws, ptr, need = self._workspace(batch, "grad_input")
-            _check(_lib().aqlm_mx_grad_input(self._ref, dy.data_ptr(), batch, dx.data_ptr(),
-                                             MX_TYPES[dy.dtype], ptr, need,
-                                             _stream_handle(self.device)))
+        ws, ptr, need = self._workspace(batch, "grad_input")
+        _call(self.device, _lib().aqlm_mx_grad_input, self._ref, dy.data_ptr(), batch, dx.data_ptr(),
+              MX_TYPES[dy.dtype], ptr, need)
         return dx
 
 
@@ -268,7 +286,5 @@ def mx_gemv_batched(layers, xs, outs=None):
     structs = (MxMatrixStruct * n)(*[L._struct for L in layers])
     xp = (ctypes.c_void_p * n)(*[x.data_ptr() for x in xs])
     yp = (ctypes.c_void_p * n)(*[y.data_ptr() for y in ys])
-    with _on(device):
-        _check(_lib().aqlm_mx_gemv_batched(structs, xp, yp, n, batch, MX_TYPES[dtype],
-                                           _stream_handle(device)))
+    _call(device, _lib().aqlm_mx_gemv_batched, structs, xp, yp, n, batch, MX_TYPES[dtype])
     return ys
