@@ -270,19 +270,29 @@ def mx_gemv_batched(layers, xs, outs=None):
 
     layers: sequence of MxLayer; xs: one [batch, in_i] tensor per layer (batch 0
     to 8 and type shared, may repeat); outs: optional [batch, out_i] tensors.
-    Returns the list of outputs."""
+    Returns the list of outputs; without outs, those of layers of one size are
+    parts of one allocation."""
     n = len(layers)
     if len(xs) != n or (outs is not None and len(outs) != n):
         raise ValueError("one x (and one out) per layer")
     if n == 0:
         return []
     batch, dtype, device = xs[0].shape[0], xs[0].dtype, layers[0].device
-    ys = []
-    for i, (L, x) in enumerate(zip(layers, xs)):
+    seen, seen_cols = None, 0
+    for L, x in zip(layers, xs):
+        if x is seen and L.in_features == seen_cols and L.device == device:
+            continue  # the x of the layer before, as with query, key and value
         L._check_half(x, "x", L.in_features)
         if x.shape[0] != batch or x.dtype != dtype or L.device != device:
             raise ValueError("all layers share the batch size, the type and the device")
-        ys.append(_output(None if outs is None else outs[i], (batch, L.out_features), dtype, device))
+        seen, seen_cols = x, L.in_features
+    sizes = [L.out_features for L in layers]
+    if outs is not None:
+        ys = [_output(o, (batch, k), dtype, device) for o, k in zip(outs, sizes)]
+    elif n > 1 and min(sizes) == max(sizes):
+        ys = list(torch.empty((n, batch, sizes[0]), dtype=dtype, device=device).unbind(0))
+    else:
+        ys = [torch.empty((batch, k), dtype=dtype, device=device) for k in sizes]
     structs = (MxMatrixStruct * n)(*[L._struct for L in layers])
     xp = (ctypes.c_void_p * n)(*[x.data_ptr() for x in xs])
     yp = (ctypes.c_void_p * n)(*[y.data_ptr() for y in ys])
