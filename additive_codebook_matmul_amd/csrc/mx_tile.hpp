@@ -187,18 +187,20 @@ template <MxType T, int RT, int NT, int TW>
 __device__ __forceinline__ void store_tile(const TileArgs &A, const float16_t (&acc)[RT][NT], int job,
                                            const TilePlace &at, int wave, int lane, uint8_t *lds) {
   constexpr int kThreads = 64 * kRowWaves * TW;
+  const int rw = wave / TW, tw = wave % TW;
+  const int row0 = (at.row_tile * kRowWaves + rw) * 32 * RT, tok0 = (at.tok_tile * TW + tw) * 32 * NT;
   if (A.splits > 1) {
     float4_t *p = A.part + (int64_t)job * (RT * NT * 4 * kThreads) + wave * 64 + lane;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
+        if (tok0 + 32 * j + (lane & 31) < A.batch) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) p[((i * NT + j) * 4 + q) * kThreads] = quarter(acc[i][j], q);
+          for (int q = 0; q < 4; ++q) p[((i * NT + j) * 4 + q) * kThreads] = quarter(acc[i][j], q);
+        }
     return;
   }
-  const int rw = wave / TW, tw = wave % TW;
-  const int row0 = (at.row_tile * kRowWaves + rw) * 32 * RT, tok0 = (at.tok_tile * TW + tw) * 32 * NT;
   if ((A.rows & 7) == 0) {
     constexpr int kChunks = 4 * RT;  // of 16 bytes, eight rows, for a token
     uint8_t *const mine = lds + wave * kStoreBytes<RT>;
@@ -248,13 +250,21 @@ __global__ __launch_bounds__(64 * kRowWaves * TW) void mx_tile_sum_kernel(const 
   const int slot = (int)blockIdx.x % (RT * NT * 4), tile = (int)blockIdx.x / (RT * NT * 4);
   const float4_t *p = A.part + ((int64_t)tile * (RT * NT * 4) + slot) * kThreads + tid;
   const int64_t stride = (int64_t)tiles * (RT * NT * 4) * kThreads;
-  float4_t v = p[0];
-  for (int s = 1; s < A.splits; ++s) v += p[s * stride];
   const TilePlace at = tile_place(tile, A.row_tiles, A.tok_tiles);
   const int q = slot & 3, j = (slot >> 2) % NT, i = (slot >> 2) / NT;
   const int tok = (at.tok_tile * TW + wave % TW) * 32 * NT + 32 * j + (lane & 31);
   const int row = (at.row_tile * kRowWaves + wave / TW) * 32 * RT + 32 * i + 8 * q + 4 * (lane >> 5);
-  if (tok < A.batch) store4<T>(A.y + (int64_t)tok * A.rows, row, A.rows, v, (A.rows & 3) == 0);
+  if (tok >= A.batch) return;
+  float4_t v = p[0];
+  for (int s = 1; s < A.splits; s += 4) {  // four loads under way
+    float4_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[k] = p[min(s + k, A.splits - 1) * stride];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s + k < A.splits) v += u[k];
+  }
+  store4<T>(A.y + (int64_t)tok * A.rows, row, A.rows, v, (A.rows & 3) == 0);
 }
 
 // Tile of a product and the workgroups K is split over: the choice with the
