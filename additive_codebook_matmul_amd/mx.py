@@ -277,8 +277,10 @@ def mx_gemv_batched(layers, xs, outs=None):
         raise ValueError("one x (and one out) per layer")
     if n == 0:
         return []
-    batch, dtype, device = xs[0].shape[0], xs[0].dtype, layers[0].device
-    seen, seen_cols = None, 0
+    device = layers[0].device
+    layers[0]._check_half(xs[0], "x", layers[0].in_features)
+    batch, dtype = xs[0].shape[0], xs[0].dtype
+    seen, seen_cols = xs[0], layers[0].in_features
     for L, x in zip(layers, xs):
         if x is seen and L.in_features == seen_cols and L.device == device:
             continue  # the x of the layer before, as with query, key and value
@@ -289,7 +291,7 @@ def mx_gemv_batched(layers, xs, outs=None):
     sizes = [L.out_features for L in layers]
     if outs is not None:
         ys = [_output(o, (batch, k), dtype, device) for o, k in zip(outs, sizes)]
-    elif n > 1 and min(sizes) == max(sizes):
+    elif n > 1 and min(sizes) == max(sizes) and batch * sizes[0] % 8 == 0:  # (16-byte parts)
         ys = list(torch.empty((n, batch, sizes[0]), dtype=dtype, device=device).unbind(0))
     else:
         ys = [torch.empty((batch, k), dtype=dtype, device=device) for k in sizes]
