@@ -121,16 +121,17 @@ template <MxType T, int NW> hipError_t launch_skinny(Group &g, int batch, hipStr
 }
 
 // One row of activations: the weights' bytes bound the product, so a wavefront
-// reads whole rows, R at a time, 1 KiB of codes (64 blocks of 32, a block a lane) and
-// their 64 scale bytes each (28672 x 8192 27 us, 4.6 TB/s; in 16-row tiles whose
-// wavefronts read 64-byte pieces of rows 42).
+// reads whole rows, R at a time, 1 KiB of codes (64 blocks of 32, a block a
+// lane) and their 64 scale bytes each (28672 x 8192 27 us, 4.6 TB/s; in 16-row
+// tiles whose wavefronts read 64-byte pieces of rows 42).
 //   * x lies in LDS, up to kSegment inputs of it, read by all wavefronts of the
 //     workgroup; a lane takes the 64 bytes of its own block for every row.
 //   * v_mfma_f32_16x16x32 sums over the lanes as well: lane (m, q) = (lane % 16,
 //     lane / 16) gives eight codes of its block and eight inputs of the same
 //     block, so that the result's diagonal (m, m) holds the sums of the four
 //     lanes m, 16 + m, ..; the rest of the result is of no use, and the
-//     instruction still outruns the loads (64 bytes of codes a clock and CU). The 16 diagonal places are added at the end of a row.
+//     instruction still outruns the loads (64 bytes of codes a clock and CU).
+//     The 16 diagonal places are added at the end of a row.
 // Chunks of x are permuted (x_place), so that the 16 lanes of an LDS pass touch
 // 16 distinct groups of banks.
 constexpr int kRowThreads = 256;
@@ -172,16 +173,17 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g) {
   };
   auto compute = [&](int c, const uint4 (&wv)[R], const uint32_t (&sv)[R]) __attribute__((always_inline)) {
     const int lb = (c % kChunks) * 64 + lane;  // block of the segment
-    bool fits = true;
-    if constexpr (T == MxType::kF16) {
+    // (by row, so that a row's sums do not depend on its neighbours)
+    bool fits[R], all = true;
 #pragma unroll
-      for (int r = 0; r < R; ++r) fits = fits & (mx_fits_f16(sv[r]) | (64 * c + lane >= nb) | (r >= mine));
-      fits = __all(fits);
+    for (int r = 0; r < R; ++r) {
+      fits[r] = T != MxType::kF16 || __all(mx_fits_f16(sv[r]) | (64 * c + lane >= nb) | (r >= mine));
+      all = all & fits[r];
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const uint4 x = *reinterpret_cast<const uint4 *>(xs + x_place(lb, s));
-      if (fits) {
+      if (all) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const uint32_t ww[4] = {wv[r].x, wv[r].y, wv[r].z, wv[r].w};
@@ -195,9 +197,13 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const uint32_t ww[4] = {wv[r].x, wv[r].y, wv[r].z, wv[r].w};
-          const uint4 a = mx_decode8<MxType::kBF16>(ww[s], mx_scale(sv[r]));
-          acc[r] = mx_mfma16<MxType::kBF16>(a, hi, acc[r]);
-          acc[r] = mx_mfma16<MxType::kBF16>(a, lo, acc[r]);
+          if (fits[r]) {
+            acc[r] = mx_mfma16<T>(mx_decode8<T>(ww[s], mx_scale(sv[r])), x, acc[r]);
+          } else {
+            const uint4 a = mx_decode8<MxType::kBF16>(ww[s], mx_scale(sv[r]));
+            acc[r] = mx_mfma16<MxType::kBF16>(a, hi, acc[r]);
+            acc[r] = mx_mfma16<MxType::kBF16>(a, lo, acc[r]);
+          }
         }
       }
     }

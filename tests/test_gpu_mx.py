@@ -314,6 +314,43 @@ def test_grouped_layers(batch, dtype):
     assert torch.equal(shared[0], shared[1])
 
 
+@pytest.mark.parametrize("batch", [1, 2, 8])
+def test_grouped_layers_with_far_scales(batch):
+    """The bits of single calls too where some rows have scales that float16 weights cannot take
+    (their neighbours' sums must not depend on which rows a launch puts together)."""
+    rng = np.random.default_rng(batch)
+    layers, xs = [], []
+    for k, (out, n_in) in enumerate([(1000, 2080), (1100, 2080), (16001, 1056), (20, 4128)]):
+        w = MO.pack(rng.integers(0, 16, (out, n_in), dtype=np.uint8))
+        scales = rng.integers(110, 125, (out, n_in // 32)).astype(np.uint8)
+        far = rng.random(scales.shape) < 0.01
+        scales[far] = rng.integers(85, 104, int(far.sum()))
+        layers.append(MxLayer(dev(w), dev(scales)))
+        xs.append(torch.from_numpy(rng.standard_normal((batch, n_in)).astype(np.float16)).to(DEV))
+    alone = [layer.gemv(x) for layer, x in zip(layers, xs)]
+    for n in (2, 3, 4):
+        for got, want in zip(mx_gemv_batched(layers[:n], xs[:n]), alone):
+            assert torch.equal(got, want)
+    for layer, x, want in zip(layers, xs, alone):
+        assert torch.equal(layer.gemm(x), want)
+
+
+@pytest.mark.parametrize("batch", [1, 3, 8])
+@pytest.mark.parametrize("out", [1, 20, 33, 64])
+def test_grouped_layers_of_one_size(out, batch):
+    """Query, key and value of one input, the results allocated by the call."""
+    layers = [_layer(out, 96, k)[0] for k in range(3)]
+    x = rounded(whole(batch, 96, 5), torch.float16).to(DEV)
+    got = mx_gemv_batched(layers, [x, x, x])
+    for y, layer in zip(got, layers):
+        assert y.is_contiguous() and y.data_ptr() % 16 == 0
+        assert torch.equal(y, layer.gemv(x))
+    with pytest.raises(ValueError):
+        mx_gemv_batched(layers, [x, x, x[:, :64]])
+    with pytest.raises(ValueError):
+        mx_gemv_batched(layers[:1], [torch.zeros((), dtype=torch.float16, device=DEV)])
+
+
 def test_codebook_layer_to_microscaled_and_back():
     """A codebook layer's weights expanded, microscaled, and run as a step of adapter training: the
     forward products, and the gradient against differences of the forward (exact numbers)."""
