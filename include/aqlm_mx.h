@@ -94,7 +94,9 @@ AQLM_API int aqlm_mx_dequant(const aqlm_mx_matrix *m, int32_t type, void *W, voi
  * 0 <= batch <= 8 activation rows each. W, x and y are HOST arrays of
  * num_layers entries (at most 4096); x[i] is [batch][cols_i] and y[i]
  * [batch][rows_i], both of `type` (F16 or BF16). x[i] may be shared. Up to 16
- * layers go into one launch. Results are bit-identical to calls with one layer.
+ * layers go into one launch, but large ones that a tile kernel serves better
+ * (from two rows on) into one each. Results are bit-identical to calls with one
+ * layer.
  */
 AQLM_API int aqlm_mx_gemv_batched(const aqlm_mx_matrix *W, const void *const *x, void *const *y,
                                   int32_t num_layers, int64_t batch, int32_t type, void *stream);

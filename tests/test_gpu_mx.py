@@ -211,6 +211,77 @@ def test_grad_input_exact(batch, out, n_in, dtype):
     ok()
 
 
+# Whole grids of the larger tiles with ragged ends on every side, more than 128
+# blocks a row (scales staged again), rows whose blocks and scales end inside
+# words and lines, K split over workgroups, and batches on the border of the
+# kernels for few rows.
+LARGE = [(1030, 3075, 4256), (700, 5000, 4192), (300, 4099, 4256), (64, 2050, 8288),
+         (12, 9000, 4256), (16, 28672, 1056), (2, 28672, 4128), (8, 20011, 4160), (1500, 2104, 4384)]
+
+
+@pytest.mark.parametrize("batch,out,n_in", LARGE)
+def test_large_products_and_gradients_exact(batch, out, n_in):
+    packed, scales, w = whole_weights(out, n_in, batch + out)
+    xp, xs, xm = whole_weights(batch, n_in, 7 * batch + n_in, 127, 128)
+    x, dy = whole(batch, n_in, n_in + batch), whole(batch, out, n_in + batch)
+    assert (np.abs(xm) @ np.abs(w).T).max() * 16 < 1 << 24
+    layer = MxLayer(dev(packed), dev(scales))
+    want_y, want_mx, want_dx = x @ w.T, xm @ w.T, dy @ w
+    for dtype in HALVES:
+        y, ok_y = guarded((batch, out), dtype)
+        same(layer.gemm(rounded(x, dtype).to(DEV), out=y), rounded(want_y, dtype))
+        ok_y()
+        y, ok_y = guarded((batch, out), dtype)
+        same(layer.gemm_mx(dev(xp), dev(xs), dtype, out=y), rounded(want_mx, dtype))
+        ok_y()
+        dx, ok_dx = guarded((batch, n_in), dtype)
+        same(layer.grad_input(rounded(dy, dtype).to(DEV), out=dx), rounded(want_dx, dtype))
+        ok_dx()
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+def test_arrays_past_32_bit_offsets(dtype):
+    """Codes, activations and results above 4 GiB: the far end's results are those of the far end
+    alone. Whole numbers: exact whatever the kernels' order."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(3)
+
+    def packed(rows, cols):
+        codes = torch.randint(0, 256, (rows, cols // 2), generator=gen, device=DEV, dtype=torch.uint8)
+        return codes, torch.full((rows, cols // 32), 127, device=DEV, dtype=torch.uint8)
+
+    def halves(rows, cols):
+        return torch.randint(-2, 3, (rows, cols), generator=gen, device=DEV, dtype=torch.int8).to(dtype)
+
+    rows, cols, end = 600_000, 16384, 1000                # 4.9 GB of codes
+    codes, scales = packed(rows, cols)
+    layer = MxLayer(codes, scales)
+    far = MxLayer(codes[-end:].clone(), scales[-end:].clone())
+    for batch in (1, 3, 40):
+        x = halves(batch, cols)
+        assert torch.equal(layer.gemm(x)[:, -end:], far.gemm(x))
+        mx = mx_quantize(x)
+        assert torch.equal(layer.gemm_mx(*mx, dtype)[:, -end:], far.gemm_mx(*mx, dtype))
+        dy = torch.zeros((batch, rows), dtype=dtype, device=DEV)
+        dy[:, -end:] = halves(batch, end)
+        assert torch.equal(layer.grad_input(dy), far.grad_input(dy[:, -end:].contiguous()))
+    del codes, scales, layer, far, dy
+
+    batch, cols = 1 << 20, 2080                           # 4.4 GB of activations and of results
+    layer = MxLayer(*packed(2088, cols))
+    x = halves(batch, cols)
+    tail = x[-end:].clone()
+    assert torch.equal(layer.gemm(x)[-end:], layer.gemm(tail))
+    dy = halves(batch, 2088)
+    assert torch.equal(layer.grad_input(dy)[-end:], layer.grad_input(dy[-end:].clone()))
+    del dy
+    mx = mx_quantize(x)
+    small = mx_quantize(tail)
+    assert torch.equal(mx[0][-end:], small[0]) and torch.equal(mx[1][-end:], small[1])
+    assert torch.equal(layer.gemm_mx(*mx, dtype)[-end:], layer.gemm_mx(*small, dtype))
+    assert torch.equal(mx_dequant(*mx, dtype)[-end:], tail)
+
+
 # --- products, real data ------------------------------------------------------
 REAL = [(1, 300, 4096), (4, 129, 11008), (16, 257, 1056), (50, 200, 4096), (130, 300, 2048),
         (300, 520, 1024)]
