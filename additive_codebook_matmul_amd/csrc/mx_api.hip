@@ -149,6 +149,28 @@ int aqlm_mx_gemm_mx(const aqlm_mx_matrix *W, const aqlm_mx_matrix *x, void *y, i
                                           static_cast<hipStream_t>(stream)));
 }
 
+int aqlm_mx_gemm_quant_workspace_size(const aqlm_mx_matrix *W, int64_t batch, int64_t *bytes) {
+  return workspace_size(aqlm::mx_gemm_quant_ws_bytes, W, batch, bytes);
+}
+
+int aqlm_mx_gemm_quant(const aqlm_mx_matrix *W, const void *x, int64_t batch, int32_t rule, void *y,
+                       int32_t type, void *workspace, int64_t workspace_bytes, void *stream) {
+  aqlm::MxDesc d;
+  int st = check_matrix(W, &d, true, false);
+  if (st != AQLM_OK) return st;
+  if (!half_type(type)) return AQLM_ERR_TYPE;
+  if (rule != AQLM_MX_SCALE_FLOOR && rule != AQLM_MX_SCALE_CEIL) return AQLM_ERR_TYPE;
+  if (batch < 0 || batch > AQLM_MX_MAX_DIM) return AQLM_ERR_BATCH;
+  if (batch == 0) return AQLM_OK;
+  st = check_io(x, y);
+  if (st == AQLM_OK)
+    st = check_workspace(aqlm::mx_gemm_quant_ws_bytes(d, batch), workspace, workspace_bytes);
+  if (st != AQLM_OK) return st;
+  return from_hip(aqlm::launch_mx_gemm_quant(d, x, batch, rule == AQLM_MX_SCALE_CEIL, y,
+                                             static_cast<aqlm::MxType>(type), workspace,
+                                             static_cast<hipStream_t>(stream)));
+}
+
 int aqlm_mx_grad_input_workspace_size(const aqlm_mx_matrix *W, int64_t batch, int64_t *bytes) {
   return workspace_size(aqlm::mx_grad_ws_bytes, W, batch, bytes);
 }

@@ -14,82 +14,6 @@ namespace {
 constexpr int kCThreads = 256;
 constexpr int kCUnroll = 4;  // octets per thread, a block's threads apart
 
-// Eight consecutive elements, as loaded.
-template <MxType T> struct Octet {
-  uint32_t w[T == MxType::kF32 ? 8 : 4];
-};
-
-template <MxType T> __device__ __forceinline__ Octet<T> load_octet(const void *x, int64_t i) {
-  Octet<T> o;
-  const u32x4_t *p = static_cast<const u32x4_t *>(x) + i * (T == MxType::kF32 ? 2 : 1);
-#pragma unroll
-  for (int k = 0; k < (T == MxType::kF32 ? 2 : 1); ++k) {
-    const u32x4_t v = p[k];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o.w[4 * k + e] = v[e];
-  }
-  return o;
-}
-
-// Largest magnitude of a block as float32 bits, from the octets of its four
-// lanes. Magnitudes order like their bits read as integers, with NaN above
-// infinity above the numbers, so the maximum is taken on integers.
-template <MxType T> __device__ __forceinline__ uint32_t block_max(const Octet<T> &o) {
-  uint32_t m = 0;
-  if constexpr (T == MxType::kF32) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, o.w[e] & 0x7FFFFFFFu);
-  } else {
-    u16x2_t p = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      p = __builtin_elementwise_max(p, __builtin_bit_cast(u16x2_t, o.w[e] & 0x7FFF7FFFu));
-    m = max((uint32_t)p.x, (uint32_t)p.y);
-  }
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadXor1, 0xF, 0xF, false));
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadXor2, 0xF, 0xF, false));
-  if constexpr (T == MxType::kF16) return __builtin_bit_cast(uint32_t, h2f(m));  // exact
-  if constexpr (T == MxType::kBF16) return m << 16;
-  return m;
-}
-
-// E8M0 byte of a block from its largest magnitude m * 2^e (float32 bits). With
-// 1 <= m < 2, m * 2^e / 2^(e-2) = 4 m: at most 6 up to m = 1.5 (mantissa bits
-// 0x400000), which is where the ceil rule takes the next power. Exponent
-// fields below 3 (subnormals among them) give scales under 2^-127, held as
-// 2^-127.
-template <bool CEIL> __device__ __forceinline__ uint32_t scale_byte(uint32_t bits) {
-  if (bits >= 0x7F800000u) return 255u;
-  if (bits == 0u) return 127u;
-  int b = (int)(bits >> 23) - 2;
-  if (CEIL) b += (bits & 0x7FFFFFu) > 0x400000u;
-  return (uint32_t)max(b, 0);
-}
-
-// Eight codes of an octet: v_cvt_scalef32_pk_fp4 divides by the scale, rounds
-// to nearest even and saturates at 6.
-template <MxType T> __device__ __forceinline__ uint32_t encode8(const Octet<T> &o, float s) {
-  uint32_t r = 0;
-  if constexpr (T == MxType::kF16) {
-#define AQLM_ENC(i) \
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(half2_t, o.w[i]), s, i);
-    AQLM_ENC(0) AQLM_ENC(1) AQLM_ENC(2) AQLM_ENC(3)
-#undef AQLM_ENC
-  } else if constexpr (T == MxType::kBF16) {
-#define AQLM_ENC(i) \
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bhalf2_t, o.w[i]), s, i);
-    AQLM_ENC(0) AQLM_ENC(1) AQLM_ENC(2) AQLM_ENC(3)
-#undef AQLM_ENC
-  } else {
-#define AQLM_ENC(i)                                                                              \
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __builtin_bit_cast(float, o.w[2 * i]),         \
-                                               __builtin_bit_cast(float, o.w[2 * i + 1]), s, i);
-    AQLM_ENC(0) AQLM_ENC(1) AQLM_ENC(2) AQLM_ENC(3)
-#undef AQLM_ENC
-  }
-  return r;
-}
-
 template <MxType T, bool CEIL>
 __global__ __launch_bounds__(kCThreads) void mx_quantize_kernel(const void *__restrict__ x,
                                                                 uint32_t *__restrict__ codes,

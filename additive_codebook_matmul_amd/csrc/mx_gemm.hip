@@ -76,7 +76,7 @@ __global__ __launch_bounds__(NW * 64) void mx_skinny_kernel(const Group g, const
                             (sc.w >> (8 * q)) & 0xFFu};
     bool fits = true;
     if constexpr (T == MxType::kF16)
-      fits = __all(mx_fits_f16(sb[0]) & mx_fits_f16(sb[1]) & mx_fits_f16(sb[2]) & mx_fits_f16(sb[3]));
+      fits = __all(mx_fits_f16(sb[0]) && mx_fits_f16(sb[1]) && mx_fits_f16(sb[2]) && mx_fits_f16(sb[3]));
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const uint32_t ww[4] = {w[c].x, w[c].y, w[c].z, w[c].w};

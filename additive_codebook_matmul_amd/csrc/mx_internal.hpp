@@ -38,6 +38,9 @@ hipError_t launch_mx_gemm(const MxDesc &W, const void *x, int64_t batch, void *y
 int64_t mx_gemm_mx_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_gemm_mx(const MxDesc &W, const MxDesc &x, void *y, MxType type, void *ws,
                              hipStream_t stream);
+int64_t mx_gemm_quant_ws_bytes(const MxDesc &W, int64_t batch);
+hipError_t launch_mx_gemm_quant(const MxDesc &W, const void *x, int64_t batch, bool ceil_rule, void *y,
+                                MxType type, void *ws, hipStream_t stream);
 // Their tile kernels (mx_gemm_tile.hip, mx_gemm_mx_tile.hip): modelled duration
 // in us, workspace, launch. Up to 8 rows of half activations K is not split
 // and no workspace needed.

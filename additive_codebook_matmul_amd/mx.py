@@ -26,7 +26,8 @@ MX_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 MX_RULES = {"floor": 0, "ceil": 1}
 MX_SYMBOLS = ("aqlm_mx_quantize", "aqlm_mx_dequant", "aqlm_mx_gemv_batched",
               "aqlm_mx_gemm_workspace_size", "aqlm_mx_gemm", "aqlm_mx_gemm_mx_workspace_size",
-              "aqlm_mx_gemm_mx", "aqlm_mx_grad_input_workspace_size", "aqlm_mx_grad_input")
+              "aqlm_mx_gemm_mx", "aqlm_mx_gemm_quant_workspace_size", "aqlm_mx_gemm_quant",
+              "aqlm_mx_grad_input_workspace_size", "aqlm_mx_grad_input")
 
 _HALVES = (torch.float16, torch.bfloat16)
 
@@ -50,11 +51,12 @@ def _lib() -> ctypes.CDLL:
         lib.aqlm_mx_dequant.argtypes = [M, I32, P, P]
         lib.aqlm_mx_gemv_batched.argtypes = [M, ctypes.POINTER(P), ctypes.POINTER(P), I32, I64, I32,
                                              P]
-        for name in ("gemm", "gemm_mx", "grad_input"):
+        for name in ("gemm", "gemm_mx", "gemm_quant", "grad_input"):
             getattr(lib, f"aqlm_mx_{name}_workspace_size").argtypes = [M, I64, ctypes.POINTER(I64)]
         lib.aqlm_mx_gemm.argtypes = [M, P, I64, P, I32, P, I64, P]
         lib.aqlm_mx_grad_input.argtypes = [M, P, I64, P, I32, P, I64, P]
         lib.aqlm_mx_gemm_mx.argtypes = [M, M, P, I32, P, I64, P]
+        lib.aqlm_mx_gemm_quant.argtypes = [M, P, I64, I32, P, I32, P, I64, P]
         for name in MX_SYMBOLS:
             getattr(lib, name).restype = ctypes.c_int
         _ready = lib
@@ -176,7 +178,7 @@ class MxLayer:
             raise ValueError(f"{what} must be on the layer's device")
 
     def workspace_bytes(self, batch: int, op: str = "gemm") -> int:
-        """Device workspace of gemm, gemm_mx or grad_input at this batch (0: none)."""
+        """Device workspace of gemm, gemm_mx, gemm_quant or grad_input at this batch (0: none)."""
         need = self._ws_bytes.get((op, batch))
         if need is None:
             n = ctypes.c_int64(0)
@@ -230,27 +232,18 @@ class MxLayer:
               MX_TYPES[dtype], ptr, need)
         return y
 
-    def forward_mx(self, x: torch.Tensor, rule: str = "floor") -> torch.Tensor:
-        """y = Q(x) . W^T: the activations quantised by mx_quantize, then gemm_mx."""
+    def forward_mx(self, x: torch.Tensor, rule: str = "floor",
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """y = Q(x) . W^T: the activations quantised by mx_quantize's rule, then the product of
+        gemm_mx, in one call."""
         self._check_half(x, "x", self.in_features)
         if rule not in MX_RULES:
             raise ValueError(f"rule must be one of {sorted(MX_RULES)}")
-        batch, cols = x.shape
-        y = torch.empty((batch, self.out_features), dtype=x.dtype, device=self.device)
-        # one buffer: codes, scales (both a multiple of 16 bytes from the start
-        # or to the next), the product's workspace
-        n_codes = batch * (cols // 2)
-        at_ws = (n_codes + batch * (cols // MX_BLOCK) + 255) // 256 * 256
-        need = self.workspace_bytes(batch, "gemm_mx")
-        buf = torch.empty(at_ws + need, dtype=torch.uint8, device=self.device)
-        codes = buf.data_ptr()
-        kind = MX_TYPES[x.dtype]
-        lib = _lib()
-        _call(self.device, lib.aqlm_mx_quantize, x.data_ptr(), kind, batch, cols, MX_RULES[rule],
-              codes, codes + n_codes)
-        xs = MxMatrixStruct(batch, cols, codes, codes + n_codes)
-        _call(self.device, lib.aqlm_mx_gemm_mx, self._ref, ctypes.byref(xs), y.data_ptr(), kind,
-              codes + at_ws if need else None, need)
+        batch = x.shape[0]
+        y = _output(out, (batch, self.out_features), x.dtype, self.device)
+        ws, ptr, need = self._workspace(batch, "gemm_quant")
+        _call(self.device, _lib().aqlm_mx_gemm_quant, self._ref, x.data_ptr(), batch,
+              MX_RULES[rule], y.data_ptr(), MX_TYPES[x.dtype], ptr, need)
         return y
 
     def grad_input(self, dy: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:

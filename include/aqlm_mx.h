@@ -129,6 +129,19 @@ AQLM_API int aqlm_mx_gemm_mx(const aqlm_mx_matrix *W, const aqlm_mx_matrix *x, v
                              void *stream);
 
 /*
+ * aqlm_mx_gemm_quant: y [batch][rows] = Q(x) . W^T with x [batch][cols] of
+ * `type` (F16 or BF16) quantised by aqlm_mx_quantize's `rule` on the way, y of
+ * the same type: aqlm_mx_quantize and aqlm_mx_gemm_mx in one call, with
+ * their bits. batch == 0 is a no-op. Workspace as above, the activations' codes
+ * and scales among it (never 0 bytes for a batch of 1 or more).
+ */
+AQLM_API int aqlm_mx_gemm_quant_workspace_size(const aqlm_mx_matrix *W, int64_t batch,
+                                               int64_t *bytes);
+AQLM_API int aqlm_mx_gemm_quant(const aqlm_mx_matrix *W, const void *x, int64_t batch,
+                                int32_t rule, void *y, int32_t type, void *workspace,
+                                int64_t workspace_bytes, void *stream);
+
+/*
  * aqlm_mx_grad_input: dx [batch][cols] = dy [batch][rows] . W, the gradient of
  * y = x . W^T with respect to x through the (constant) weights; dy and dx of
  * `type` (F16 or BF16). It is also the straight-through gradient of

@@ -211,6 +211,18 @@ def test_grad_input_exact(batch, out, n_in, dtype):
     ok()
 
 
+@pytest.mark.parametrize("rule", ["floor", "ceil"])
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("batch,out,n_in", [(1, 40, 32), (3, 129, 2080), (9, 65, 4128), (77, 301, 1376), (300, 520, 1024)])
+def test_forward_mx_gives_the_bits_of_its_parts(batch, out, n_in, dtype, rule):
+    layer, _ = _layer(out, n_in, 2)
+    x = rounded(np.random.default_rng(batch).standard_normal((batch, n_in)) * 3, dtype).to(DEV)
+    y, ok = guarded((batch, out), dtype)
+    layer.forward_mx(x, rule, out=y)
+    ok()
+    assert torch.equal(y, layer.gemm_mx(*mx_quantize(x, rule), dtype))
+
+
 # Whole grids of the larger tiles with ragged ends on every side, more than 128
 # blocks a row (scales staged again), rows whose blocks and scales end inside
 # words and lines, K split over workgroups, and batches on the border of the

@@ -100,6 +100,33 @@ def test_gemm_mx_refusals():
     assert f(M(), X(rows=0, codes=0, scales=0), None, 0, None, 0, None) == 0
 
 
+def test_gemm_quant_refusals():
+    f = mx._lib().aqlm_mx_gemm_quant  # W, x, batch, rule, y, type, ws, bytes, stream
+    size = mx._lib().aqlm_mx_gemm_quant_workspace_size
+    big = 1 << 40
+    assert f(None, FAKE, 1, 0, FAKE, 0, FAKE, big, None) == NULL
+    assert f(M(rows=0), FAKE, 1, 0, FAKE, 0, FAKE, big, None) == SHAPE
+    assert f(M(cols=100), FAKE, 1, 0, FAKE, 0, FAKE, big, None) == SHAPE
+    assert f(M(), FAKE, 1, 0, FAKE, 2, FAKE, big, None) == TYPE
+    assert f(M(), FAKE, 1, 2, FAKE, 0, FAKE, big, None) == TYPE
+    assert f(M(), FAKE, 1, -1, FAKE, 0, FAKE, big, None) == TYPE
+    assert f(M(), FAKE, -1, 0, FAKE, 0, FAKE, big, None) == BATCH
+    assert f(M(), FAKE, (1 << 21) + 1, 0, FAKE, 0, FAKE, big, None) == BATCH
+    assert f(M(), None, 1, 0, FAKE, 0, FAKE, big, None) == NULL
+    assert f(M(), FAKE, 1, 0, None, 0, FAKE, big, None) == NULL
+    assert f(M(), MISALIGNED, 1, 0, FAKE, 0, FAKE, big, None) == ALIGN
+    assert f(M(), FAKE, 1, 0, MISALIGNED, 0, FAKE, big, None) == ALIGN
+    assert f(M(), None, 0, 0, None, 0, None, 0, None) == 0
+    n, own = ctypes.c_int64(-1), ctypes.c_int64(-1)
+    for rows, cols, batch in ((1, 32, 1), (4096, 11008, 77), (300, 1 << 15, 300)):
+        assert size(M(rows, cols), batch, ctypes.byref(n)) == 0
+        assert mx._lib().aqlm_mx_gemm_mx_workspace_size(M(rows, cols), batch, ctypes.byref(own)) == 0
+        assert n.value >= batch * cols * 17 // 32 + own.value
+        for ws, given, st in ((None, n.value, NULL), (MISALIGNED, n.value, ALIGN),
+                              (FAKE, n.value - 1, WORKSPACE)):
+            assert f(M(rows, cols), FAKE, batch, 0, FAKE, 0, ws, given, None) == st
+
+
 def test_gemv_batched_refusals():
     f = mx._lib().aqlm_mx_gemv_batched  # W, x, y, n, batch, type, stream
     ok = mx.MxMatrixStruct(64, 128, FAKE, FAKE)
