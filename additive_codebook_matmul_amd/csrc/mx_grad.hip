@@ -12,8 +12,8 @@
 //     of 4 rows x 16 columns and each receives four rows of one column, so two
 //     reads make an operand of v_mfma_f32_32x32x16. Rows are 64 bytes longer
 //     than their 256 RT of weights, which spreads four rows x 32 columns over
-//     all banks; the threads that write permute the four chunks of a block so
-//     that 16 of them hit 16 groups of banks.
+//     all banks; the threads that write take the four chunks of a block in
+//     different orders, so that eight of them hit all banks.
 //   * dy goes from memory straight to LDS three steps ahead, into one of four
 //     stages of 128-byte rows, permuted as in the other tile kernels.
 //   * float16: a workgroup that meets a scale that float16 weights cannot take
@@ -120,8 +120,10 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_grad_tile_kernel(
     b.c = buf_load16(make_rsrc(A.codes + (rows > 0 ? o * half : 0), (uint32_t)rows * half), cplace);
     b.s = buf_load_u8(make_rsrc(A.scales + (rows > 0 ? o * nb : 0), (uint32_t)rows * nb), splace);
   };
-  // (chunk c of the block at place c ^ turn: the words change places first)
-  const int turn = ((wb >> 2) & 1) | ((wo & 1) << 1);
+  // (A write takes the chunks of eight lanes at once, which are to lie in eight
+  // places of 128 bytes: lanes two blocks apart write their four chunks in
+  // another order, turned by `turn`; the words change places first.)
+  const int turn = kCols == 256 ? (wb >> 1) & 3 : ((wb >> 1) & 1) | ((wo & 1) << 1);
   const uint32_t turn1 = turn & 1 ? ~0u : 0u, turn2 = turn & 2 ? ~0u : 0u;
   const uint32_t wplace = kw * kWBytes + wo * kRowBytes + wb * 64;
   auto put_w = [&](const Block &b, uint8_t *a, auto wide_c) __attribute__((always_inline)) {
