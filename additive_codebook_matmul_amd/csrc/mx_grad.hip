@@ -175,20 +175,43 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_grad_tile_kernel(
     constexpr bool kLook = T == MxType::kF16 && !WIDE;
     Block blk[4];
     bool bad = false;
+    // Operands of instruction s of a step, and its products. Those of a step's
+    // last instruction come in the next step, while its first reads are under
+    // way behind the barrier. (The first step's are zeros.)
+    uint4 wv[2][RT], b[2][NT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) wv[1][i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) b[1][j] = make_uint4(0, 0, 0, 0);
+    auto reads = [&](int s, const uint8_t *a, const uint8_t *w) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) wv[s & 1][i] = w_of(w, i, s);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) b[s & 1][j] = x_of(a, j, s);
+    };
+    auto products = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if constexpr (WIDE && T == MxType::kF16) {
+            uint4 hi, lo;
+            split_f16(b[s & 1][j], hi, lo);
+            acc[i][j] = mx_mfma32<MxType::kBF16>(wv[s & 1][i], hi, acc[i][j]);
+            acc[i][j] = mx_mfma32<MxType::kBF16>(wv[s & 1][i], lo, acc[i][j]);
+          } else {
+            acc[i][j] = mx_mfma32<T>(wv[s & 1][i], b[s & 1][j], acc[i][j]);
+          }
+        }
+    };
     auto step = [&](int t, auto u_c, uint8_t *a, uint8_t *far, uint8_t *w, uint8_t *wfar)
                     __attribute__((always_inline)) {
       constexpr int U = decltype(u_c)::value;
       fill_x(t + 3, far);
       load_w(t + 3, blk[(U + 3) & 3]);
       __builtin_amdgcn_sched_barrier(0);
-      uint4 wv[2][RT], b[2][NT];
-      auto reads = [&](int s) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i) wv[s & 1][i] = w_of(w, i, s);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) b[s & 1][j] = x_of(a, j, s);
-      };
-      reads(0);
+      reads(0, a, w);
+      products(3);
       put_w(blk[(U + 1) & 3], wfar, wide_c);
       if constexpr (kLook) {
         bad = bad | unfit(t + 1, blk[(U + 1) & 3]);
@@ -197,27 +220,20 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_grad_tile_kernel(
           if (lane == 0) flags[wave_all] = any != 0;
         }
       }
+      if constexpr (!WIDE || T != MxType::kF16) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * RT + NT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, (RT * NT + 1) / 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, RT * NT - (RT * NT + 1) / 2, 0);
+      }
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (s < 3) reads(s + 1);
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            if constexpr (WIDE && T == MxType::kF16) {
-              uint4 hi, lo;
-              split_f16(b[s & 1][j], hi, lo);
-              acc[i][j] = mx_mfma32<MxType::kBF16>(wv[s & 1][i], hi, acc[i][j]);
-              acc[i][j] = mx_mfma32<MxType::kBF16>(wv[s & 1][i], lo, acc[i][j]);
-            } else {
-              acc[i][j] = mx_mfma32<T>(wv[s & 1][i], b[s & 1][j], acc[i][j]);
-            }
-          }
+      for (int s = 0; s < 3; ++s) {
+        reads(s + 1, a, w);
+        products(s);
         // the next instruction's operands are read before this one's products,
         // a chunk of the next rows written between them
         if constexpr (!WIDE || T != MxType::kF16) {
-          if (s == 0) __builtin_amdgcn_sched_group_barrier(0x100, 2 * (2 * RT + NT), 0);
-          else if (s < 3) __builtin_amdgcn_sched_group_barrier(0x100, 2 * RT + NT, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 2 * RT + NT, 0);
           __builtin_amdgcn_sched_group_barrier(0x008, (RT * NT + 1) / 2, 0);
           __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
           __builtin_amdgcn_sched_group_barrier(0x008, RT * NT - (RT * NT + 1) / 2, 0);
@@ -263,6 +279,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_grad_tile_kernel(
         if (!good) break;
       }
     }
+    products(3);
     // what is under way has arrived before LDS is used again
     asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
     __syncthreads();
