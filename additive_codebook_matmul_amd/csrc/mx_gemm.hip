@@ -284,7 +284,7 @@ bool tiles_pay(const MxDesc &W, int64_t batch) {
   if (batch == 1) return false;
   const double groups = (double)((W.cols / 32 + 15) / 16), tiles = (double)((W.rows + 15) / 16);
   const double turns = (double)(int64_t)((groups + kSkinnyWaves - 1) / kSkinnyWaves);
-  const double us = std::max(3.0 + tiles * groups * (1.1e-3 + 0.1e-3 * (double)batch),
+  const double us = std::max(2.5 + tiles * groups * (1.1e-3 + 0.1e-3 * (double)batch),
                              2.5 + turns * (1.8 + 0.2 * (double)batch));
   return mx_gemm_tile_us(W, batch) < us;
 }

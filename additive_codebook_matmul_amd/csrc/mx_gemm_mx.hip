@@ -93,7 +93,7 @@ bool tiles_pay(const MxDesc &W, int64_t batch) {
   if (batch > 16) return true;
   const double groups = (double)((W.cols / 32 + 15) / 16), tiles = (double)((W.rows + 15) / 16);
   const double turns = (double)(int64_t)((groups + kSkinnyWaves - 1) / kSkinnyWaves);
-  const double us = std::max(3.0 + tiles * groups * (0.9e-3 + 0.02e-3 * (double)batch),
+  const double us = std::max(2.5 + tiles * groups * (0.9e-3 + 0.02e-3 * (double)batch),
                              2.5 + turns * (1.1 + 0.07 * (double)batch));
   return mx_gemm_mx_tile_us(W, batch) < us;
 }

@@ -286,9 +286,12 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
   store_tile<T, RT, NT, TW>(A, acc, job, at, wave, lane, wa0);
 }
 
-// Fitted to 4096 x 4096, 4096 x 11008 and 11008 x 4096 from 32 to 2048 rows.
+// Fitted, with the constants of plan_tiles, to 4096 x 4096, 4096 x 11008, 11008 x
+// 4096 and 28672 x 8192 from 24 to 2048 rows, each shape measured at each: at
+// 64 x 11008 x 4096 the three take 28.6, 16.1 and 12.7 us, at 400 x 4096 x 4096
+// 41.5, 18.4 and 23.3, at 2048 x 11008 x 4096 155, 198 and 246.
 constexpr TileShape kShapes[] = {
-    {2, 2, 2, 1, 2.64, 4.88}, {1, 2, 1, 2, 2.40, 2.88}, {1, 1, 1, 2, 2.00, 1.44}};
+    {2, 2, 2, 1, 3.96, 2.17}, {1, 2, 1, 2, 2.83, 1.55}, {1, 1, 1, 2, 2.07, 0.73}};
 
 TilePlan plan_of(const MxDesc &W, int64_t batch) {
   return plan_tiles(kShapes, W.rows, batch, (W.cols / 32 + 15) / 16, batch <= 8 ? 1 : 8);

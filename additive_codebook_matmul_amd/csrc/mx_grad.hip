@@ -314,9 +314,12 @@ __global__ __launch_bounds__(256) void mx_pad_rows_kernel(const uint16_t *__rest
                                                     v[4] | (v[5] << 16), v[6] | (v[7] << 16));
 }
 
-// Fitted to 4096 x 4096, 4096 x 11008 and 11008 x 4096 from 32 to 2048 rows.
+// Fitted, with the constants of plan_tiles, to 4096 x 4096, 4096 x 11008, 11008 x
+// 4096 and 28672 x 8192 from 24 to 2048 rows, each shape measured at each: at
+// 24 x 4096 x 4096 the three take 18.2, 12.3 and 10.8 us, at 100 x 11008 x 4096
+// 29.3, 25.0 and 31.3, at 2048 x 11008 x 4096 164, 256 and 396.
 constexpr TileShape kShapes[] = {
-    {2, 2, 2, 1, 3.0, 0.9}, {1, 2, 1, 2, 2.4, 1.2}, {1, 1, 1, 2, 2.1, 0.5}};
+    {2, 2, 2, 1, 2.45, 0.89}, {1, 2, 1, 2, 2.38, 0.68}, {1, 1, 1, 2, 2.01, 0.43}};
 
 TilePlan plan_of(const MxDesc &W, int64_t batch) {
   return plan_tiles(kShapes, W.cols, batch, (W.rows + 255) / 256);

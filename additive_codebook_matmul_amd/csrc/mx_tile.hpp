@@ -270,7 +270,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW) void mx_tile_sum_kernel(const 
 // Tile of a product and the workgroups K is split over: the choice with the
 // shortest modelled time. The grid runs in rounds of up to 256 workgroups, one
 // per CU, and a group of K takes a + b * (workgroups of the round / 256) us for
-// each share; 4 us pass around that; a split writes and reads its sums at about
+// each share; 2.7 us pass around that; a split writes and reads its sums at about
 // 4 TB/s and launches a second kernel.
 struct TileShape {
   int rt, nt, tw, kw;
@@ -305,8 +305,8 @@ TilePlan plan_tiles(const TileShape (&shapes)[N], int64_t rows, int64_t batch, i
       if (p.splits != s || (s > 1 && tiles * s > 256)) break;
       const double whole = (double)(tiles * s / 256), rest = (double)(tiles * s % 256) / 256.0;
       const double group = whole * (c.a + c.b) + (rest > 0 ? c.a + c.b * rest : 0.0);
-      double us = 4.0 + (double)((p.groups_per_split + c.kw - 1) / c.kw) * group;
-      if (s > 1) us += 2.5 + (double)p.ws_bytes() * 2.0 / 4e6;
+      double us = 2.7 + (double)((p.groups_per_split + c.kw - 1) / c.kw) * group;
+      if (s > 1) us += 2.3 + (double)p.ws_bytes() * 2.0 / 4e6;
       p.us = us;
       if (best.splits == 0 || us < best.us) best = p;
     }
