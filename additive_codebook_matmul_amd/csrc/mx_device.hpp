@@ -125,6 +125,21 @@ template <MxType T> __device__ __forceinline__ uint32_t encode8(const Octet<T> &
 // 0.5 * 2^(s-127) >= 2^-24 and 6 * 2^(s-127) <= 65504 (NaN needs no care).
 __device__ __forceinline__ bool mx_fits_f16(uint32_t s) { return (s - 104u <= 36u) | (s == 255u); }
 
+// The same of 16 scale bytes at once: none of them is more than 36 above 104
+// (modulo 2^16) if both halves here are 36 or less. (NaN counts as unfit; either
+// way gives NaN.)
+__device__ __forceinline__ u16x2_t mx_above_f16(const uint4 &s) {
+  const uint32_t w[4] = {s.x, s.y, s.z, s.w};
+  u16x2_t m = {0, 0};
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const u16x2_t low = {104, 104};
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[u] & 0x00FF00FFu) - low);
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, (w[u] >> 8) & 0x00FF00FFu) - low);
+  }
+  return m;
+}
+
 // Eight float16 activations as the exact sum hi + lo of two bfloat16 vectors
 // (11 significant bits: hi takes the nearest 8, what is left has 3 or fewer
 // and a magnitude bfloat16 holds). Infinities and NaN stay in hi alone.

@@ -258,13 +258,10 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
   for (; g < gend; ++g) {
     group_scales(g);
     if constexpr (T == MxType::kF16) {
-      bool f = true;
+      u16x2_t m = {0, 0};
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const uint32_t v[4] = {sc[i].x, sc[i].y, sc[i].z, sc[i].w};
-#pragma unroll
-        for (int u = 0; u < 16; ++u) f = f & mx_fits_f16((v[u >> 2] >> (8 * (u & 3))) & 0xFFu);
-      }
+      for (int i = 0; i < RT; ++i) m = __builtin_elementwise_max(m, mx_above_f16(sc[i]));
+      const bool f = (m.x <= 36) & (m.y <= 36);
       if (!__all(f) & (my_rows > 0)) break;
     }
     group(std::false_type{}, g);
