@@ -122,7 +122,8 @@ template <MxType T, int NW> hipError_t launch_skinny(Group &g, int batch, hipStr
 
 // One row of activations: the weights' bytes bound the product, so a wavefront
 // reads whole rows, R at a time, 1 KiB of codes (64 blocks of 32, a block a
-// lane) and their 64 scale bytes each (28672 x 8192 27 us, 4.6 TB/s; in 16-row
+// lane) and their 64 scale bytes each (28672 x 8192 25.7 us, 4.9 TB/s; with
+// workgroups of four wavefronts instead of eight, four rows each, 27; in 16-row
 // tiles whose wavefronts read 64-byte pieces of rows 42).
 //   * x lies in LDS, up to kSegment inputs of it, read by all wavefronts of the
 //     workgroup; a lane takes the 64 bytes of its own block for every row.
@@ -134,7 +135,7 @@ template <MxType T, int NW> hipError_t launch_skinny(Group &g, int batch, hipStr
 //     The 16 diagonal places are added at the end of a row.
 // Chunks of x are permuted (x_place), so that the 16 lanes of an LDS pass touch
 // 16 distinct groups of banks.
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 512;
 constexpr int kSegment = 16384;  // inputs in LDS
 __device__ __forceinline__ uint32_t x_place(int blk, int s) {
   return (uint32_t)blk * 64u + (uint32_t)((s ^ ((blk >> 2) & 3)) << 4);
@@ -256,15 +257,19 @@ template <MxType T, int R> hipError_t launch_rows(Group &g, hipStream_t stream) 
   return hipGetLastError();
 }
 
-// Rows of W a wavefront reads at a time: more keep more bytes under way, fewer
-// spread a short matrix over the chip (1, 2, 4 rows: 1024 x 8192 5.2, 5.6, 6.1
-// us; 4096 x 4096 4.9, 4.7, 5.0; three of them at once 11.6, 8.9, 7.5).
+// Rows of W a wavefront reads at a time: one while all its workgroups find room
+// at once (four of them a CU) and x one segment, else two, which keep more bytes
+// under way (one, two rows: 4096 x 4096 4.0, 4.1 us, 8192 x 8192 8.2, 9.2; 11008 x
+// 4096 7.4, 6.5, three of 4096 x 4096 at once 8.3, 7.3, 8192 x 28672 24.6, 23.1).
 template <MxType T> hipError_t rows_as(Group &g, hipStream_t stream) {
   int64_t rows = 0;
-  for (int i = 0; i < g.n; ++i) rows += g.item[i].rows;
-  if (rows >= 8192) return launch_rows<T, 4>(g, stream);
-  if (rows >= 2048) return launch_rows<T, 2>(g, stream);
-  return launch_rows<T, 1>(g, stream);
+  int cols = 0;
+  for (int i = 0; i < g.n; ++i) {
+    rows += g.item[i].rows;
+    cols = std::max(cols, g.item[i].cols);
+  }
+  return rows <= 1024 * (kRowThreads / 64) && cols <= kSegment ? launch_rows<T, 1>(g, stream)
+                                                               : launch_rows<T, 2>(g, stream);
 }
 
 Group::Item item_of(const MxDesc &W, const void *x, void *y) {
