@@ -178,30 +178,34 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g) {
     bool fits[R], all = true;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      fits[r] = T != MxType::kF16 || __all(mx_fits_f16(sv[r]) | (64 * c + lane >= nb) | (r >= mine));
+      fits[r] = T != MxType::kF16 || r >= mine || __ballot((sv[r] - 104u > 36u) & (64 * c + lane < nb)) == 0;
       all = all & fits[r];
     }
+    if (all) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(xs + x_place(lb, s));
-      if (all) {
+      for (int s = 0; s < 4; ++s) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(xs + x_place(lb, s));
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const uint32_t ww[4] = {wv[r].x, wv[r].y, wv[r].z, wv[r].w};
           acc[r] = mx_mfma16<T>(mx_decode8<T>(ww[s], mx_scale(sv[r])), x, acc[r]);
         }
-      } else {
-        // scales that float16 weights cannot take: the same product in
-        // bfloat16, which holds every weight, with x split exactly in two
+      }
+    } else {
+      // scales that float16 weights cannot take: the same product in bfloat16,
+      // which holds every weight, with x split exactly in two
+#pragma unroll 1
+      for (int s = 0; s < 4; ++s) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(xs + x_place(lb, s));
         uint4 hi, lo;
         split_f16(x, hi, lo);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const uint32_t ww[4] = {wv[r].x, wv[r].y, wv[r].z, wv[r].w};
+          const uint32_t w = s == 0 ? wv[r].x : s == 1 ? wv[r].y : s == 2 ? wv[r].z : wv[r].w;
           if (fits[r]) {
-            acc[r] = mx_mfma16<T>(mx_decode8<T>(ww[s], mx_scale(sv[r])), x, acc[r]);
+            acc[r] = mx_mfma16<T>(mx_decode8<T>(w, mx_scale(sv[r])), x, acc[r]);
           } else {
-            const uint4 a = mx_decode8<MxType::kBF16>(ww[s], mx_scale(sv[r]));
+            const uint4 a = mx_decode8<MxType::kBF16>(w, mx_scale(sv[r]));
             acc[r] = mx_mfma16<MxType::kBF16>(a, hi, acc[r]);
             acc[r] = mx_mfma16<MxType::kBF16>(a, lo, acc[r]);
           }
