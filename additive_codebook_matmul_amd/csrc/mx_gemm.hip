@@ -1,6 +1,6 @@
 // Product of half activations with microscaled weights: y = x . W^T, for the
-// batches of token generation. One row of activations: mx_rows_kernel; up to
-// sixteen: mx_skinny_kernel; where its tiles are faster, and above: the tile
+// batches of token generation. One or two rows of activations: mx_rows_kernel; up
+// to sixteen: mx_skinny_kernel; where its tiles are faster, and above: the tile
 // kernels of mx_gemm_tile.hip.
 #include <algorithm>
 
@@ -120,12 +120,12 @@ template <MxType T, int NW> hipError_t launch_skinny(Group &g, int batch, hipStr
   return hipGetLastError();
 }
 
-// One row of activations: the weights' bytes bound the product, so a wavefront
+// One or two rows of activations (B): the weights' bytes bound the product, so a wavefront
 // reads whole rows, R at a time, 1 KiB of codes (64 blocks of 32, a block a
 // lane) and their 64 scale bytes each (28672 x 8192 25.7 us, 4.9 TB/s; with
 // workgroups of four wavefronts instead of eight, four rows each, 27; in 16-row
 // tiles whose wavefronts read 64-byte pieces of rows 42).
-//   * x lies in LDS, up to kSegment inputs of it, read by all wavefronts of the
+//   * x lies in LDS, up to kSegment inputs of it at a time (of both rows), read by all wavefronts of the
 //     workgroup; a lane takes the 64 bytes of its own block for every row.
 //   * v_mfma_f32_16x16x32 sums over the lanes as well: lane (m, q) = (lane % 16,
 //     lane / 16) gives eight codes of its block and eight inputs of the same
@@ -141,10 +141,10 @@ __device__ __forceinline__ uint32_t x_place(int blk, int s) {
   return (uint32_t)blk * 64u + (uint32_t)((s ^ ((blk >> 2) & 3)) << 4);
 }
 
-template <MxType T, int R>
-__global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g) {
-  constexpr int kBlocks = kSegment / 32, kChunks = kBlocks / 64;
-  __shared__ __attribute__((aligned(16))) uint8_t xs[kSegment * 2];  // [kBlocks][64 bytes]
+template <MxType T, int R, int B>
+__global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g, const int batch) {
+  constexpr int kBlocks = kSegment / 32 / B, kChunks = kBlocks / 64;
+  __shared__ __attribute__((aligned(16))) uint8_t xs[kSegment * 2];  // [B][kBlocks][64 bytes]
   int li = 0;
   while (li + 1 < g.n && (int)blockIdx.x >= g.first[li + 1]) ++li;
   const Group::Item &L = g.item[li];
@@ -158,9 +158,11 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g) {
   const Rsrc crs = make_rsrc(L.codes + (int64_t)(mine ? row0 : 0) * half, (uint32_t)mine * half);
   const Rsrc srs = make_rsrc(L.scales + (int64_t)(mine ? row0 : 0) * nb, (uint32_t)mine * nb);
 
-  float4_t acc[R];
+  float4_t acc[R][B];
 #pragma unroll
-  for (int r = 0; r < R; ++r) acc[r] = float4_t{0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int b = 0; b < B; ++b) acc[r][b] = float4_t{0.f, 0.f, 0.f, 0.f};
   uint4 w[2][R];
   uint32_t sb[2][R];
   auto load = [&](int c, uint4 (&wv)[R], uint32_t (&sv)[R]) __attribute__((always_inline)) {
@@ -184,11 +186,15 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g) {
     if (all) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(xs + x_place(lb, s));
+        uint4 x[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) x[b] = *reinterpret_cast<const uint4 *>(xs + (b * kBlocks * 64 + x_place(lb, s)));
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const uint32_t ww[4] = {wv[r].x, wv[r].y, wv[r].z, wv[r].w};
-          acc[r] = mx_mfma16<T>(mx_decode8<T>(ww[s], mx_scale(sv[r])), x, acc[r]);
+          const uint4 a = mx_decode8<T>(ww[s], mx_scale(sv[r]));
+#pragma unroll
+          for (int b = 0; b < B; ++b) acc[r][b] = mx_mfma16<T>(a, x[b], acc[r][b]);
         }
       }
     } else {
@@ -196,18 +202,21 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g) {
       // which holds every weight, with x split exactly in two
 #pragma unroll 1
       for (int s = 0; s < 4; ++s) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(xs + x_place(lb, s));
-        uint4 hi, lo;
-        split_f16(x, hi, lo);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const uint32_t w = s == 0 ? wv[r].x : s == 1 ? wv[r].y : s == 2 ? wv[r].z : wv[r].w;
-          if (fits[r]) {
-            acc[r] = mx_mfma16<T>(mx_decode8<T>(w, mx_scale(sv[r])), x, acc[r]);
-          } else {
-            const uint4 a = mx_decode8<MxType::kBF16>(w, mx_scale(sv[r]));
-            acc[r] = mx_mfma16<MxType::kBF16>(a, hi, acc[r]);
-            acc[r] = mx_mfma16<MxType::kBF16>(a, lo, acc[r]);
+        for (int b = 0; b < B; ++b) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(xs + (b * kBlocks * 64 + x_place(lb, s)));
+          uint4 hi, lo;
+          split_f16(x, hi, lo);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const uint32_t w = s == 0 ? wv[r].x : s == 1 ? wv[r].y : s == 2 ? wv[r].z : wv[r].w;
+            if (fits[r]) {
+              acc[r][b] = mx_mfma16<T>(mx_decode8<T>(w, mx_scale(sv[r])), x, acc[r][b]);
+            } else {
+              const uint4 a = mx_decode8<MxType::kBF16>(w, mx_scale(sv[r]));
+              acc[r][b] = mx_mfma16<MxType::kBF16>(a, hi, acc[r][b]);
+              acc[r][b] = mx_mfma16<MxType::kBF16>(a, lo, acc[r][b]);
+            }
           }
         }
       }
@@ -219,12 +228,15 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g) {
   for (int c0 = 0; c0 < chunks; c0 += kChunks) {  // a segment of x
     if (c0 > 0) __syncthreads();
     const int blocks = min(kBlocks, ((nb - 64 * c0 + 63) >> 6) << 6);  // whole chunks of it
-    for (int k = threadIdx.x; k < blocks * 4; k += kRowThreads) {
-      const int blk = 64 * c0 + (k >> 2);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (blk < nb) v = *reinterpret_cast<const uint4 *>(L.x + (int64_t)blk * 32 + 8 * (k & 3));
-      *reinterpret_cast<uint4 *>(xs + x_place(k >> 2, k & 3)) = v;
-    }
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      for (int k = threadIdx.x; k < blocks * 4; k += kRowThreads) {
+        const int blk = 64 * c0 + (k >> 2);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (blk < nb && b < batch)
+          v = *reinterpret_cast<const uint4 *>(L.x + ((int64_t)b * L.cols + blk * 32 + 8 * (k & 3)));
+        *reinterpret_cast<uint4 *>(xs + (b * kBlocks * 64 + x_place(k >> 2, k & 3))) = v;
+      }
     __syncthreads();
     const int c1 = min(chunks, c0 + kChunks);
     for (int c = c0; c < c1; ++c) {
@@ -241,15 +253,17 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g) {
   // the diagonal: place (m, m) is register m % 4 of lane 16 (m / 4) + m
   const bool diagonal = ((lane >> 2) & 3) == (lane >> 4);
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const float4_t a = acc[r];
-    const float v = (lane & 2) ? ((lane & 1) ? a[3] : a[2]) : ((lane & 1) ? a[1] : a[0]);
-    const float sum = wave_sum_to_lane63(diagonal ? v : 0.0f);
-    if (lane == 63 && r < mine) L.y[row0 + r] = (uint16_t)f2t<T>(sum);
-  }
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const float4_t a = acc[r][b];
+      const float v = (lane & 2) ? ((lane & 1) ? a[3] : a[2]) : ((lane & 1) ? a[1] : a[0]);
+      const float sum = wave_sum_to_lane63(diagonal ? v : 0.0f);
+      if (lane == 63 && r < mine && b < batch) L.y[(int64_t)b * rows + row0 + r] = (uint16_t)f2t<T>(sum);
+    }
 }
 
-template <MxType T, int R> hipError_t launch_rows(Group &g, hipStream_t stream) {
+template <MxType T, int R, int B> hipError_t launch_rows(Group &g, int batch, hipStream_t stream) {
   constexpr int kRows = R * (kRowThreads / 64);
   int blocks = 0;
   for (int i = 0; i < g.n; ++i) {
@@ -257,7 +271,7 @@ template <MxType T, int R> hipError_t launch_rows(Group &g, hipStream_t stream) 
     blocks += (g.item[i].rows + kRows - 1) / kRows;
   }
   g.first[g.n] = blocks;
-  hipLaunchKernelGGL((mx_rows_kernel<T, R>), dim3((unsigned)blocks), dim3(kRowThreads), 0, stream, g);
+  hipLaunchKernelGGL((mx_rows_kernel<T, R, B>), dim3((unsigned)blocks), dim3(kRowThreads), 0, stream, g, batch);
   return hipGetLastError();
 }
 
@@ -265,15 +279,15 @@ template <MxType T, int R> hipError_t launch_rows(Group &g, hipStream_t stream) 
 // at once (four of them a CU) and x one segment, else two, which keep more bytes
 // under way (one, two rows: 4096 x 4096 4.0, 4.1 us, 8192 x 8192 8.2, 9.2; 11008 x
 // 4096 7.4, 6.5, three of 4096 x 4096 at once 8.3, 7.3, 8192 x 28672 24.6, 23.1).
-template <MxType T> hipError_t rows_as(Group &g, hipStream_t stream) {
+template <MxType T, int B> hipError_t rows_as(Group &g, int batch, hipStream_t stream) {
   int64_t rows = 0;
   int cols = 0;
   for (int i = 0; i < g.n; ++i) {
     rows += g.item[i].rows;
     cols = std::max(cols, g.item[i].cols);
   }
-  return rows <= 1024 * (kRowThreads / 64) && cols <= kSegment ? launch_rows<T, 1>(g, stream)
-                                                               : launch_rows<T, 2>(g, stream);
+  return rows <= 1024 * (kRowThreads / 64) && cols <= kSegment ? launch_rows<T, 1, B>(g, batch, stream)
+                                                               : launch_rows<T, 2, B>(g, batch, stream);
 }
 
 Group::Item item_of(const MxDesc &W, const void *x, void *y) {
@@ -283,24 +297,30 @@ Group::Item item_of(const MxDesc &W, const void *x, void *y) {
 
 constexpr int kSkinnyWaves = 8;
 
-// From two rows on, where the tile kernel is the faster: the skinny one takes
+// From three rows on, where the tile kernel is the faster: the skinny one takes
 // 1.1 ns and 0.1 ns a row of activations for 16 rows of W and a group of K,
 // spread over the chip, or, with few rows, 1.8 us and 0.2 us a row for each turn
 // of its wavefronts (fitted to 1024 x 8192 .. 28672 x 8192 from 2 to 16 rows:
 // 4096 x 4096 at 8 rows 6.3 us against 9.6, 28672 x 8192 59 against 35).
-bool tiles_pay(const MxDesc &W, int64_t batch) {
+// Whole-row wavefronts serve two rows of activations better than either (4096 x
+// 4096 3.9 us against 4.5, 11008 x 4096 7.9 against 10.8, 28672 x 8192 33 against
+// 34, 8192 x 28672 30 against 41), three about as well, four and more worse.
+// `split`: K may be split over workgroups.
+bool tiles_pay(const MxDesc &W, int64_t batch, bool split) {
   if (batch > 16) return true;
-  if (batch == 1) return false;
+  if (batch <= 2) return false;
   const double groups = (double)((W.cols / 32 + 15) / 16), tiles = (double)((W.rows + 15) / 16);
   const double turns = (double)(int64_t)((groups + kSkinnyWaves - 1) / kSkinnyWaves);
   const double us = std::max(2.5 + tiles * groups * (1.1e-3 + 0.1e-3 * (double)batch),
                              2.5 + turns * (1.8 + 0.2 * (double)batch));
-  return mx_gemm_tile_us(W, batch) < us;
+  return mx_gemm_tile_us(W, batch, split) < us;
 }
 
 // Up to 16 rows of activations, without the tile kernel.
 template <MxType T> hipError_t few_as(Group &g, int batch, hipStream_t stream) {
-  return batch == 1 ? rows_as<T>(g, stream) : launch_skinny<T, kSkinnyWaves>(g, batch, stream);
+  if (batch == 1) return rows_as<T, 1>(g, batch, stream);
+  if (batch == 2) return rows_as<T, 2>(g, batch, stream);
+  return launch_skinny<T, kSkinnyWaves>(g, batch, stream);
 }
 
 hipError_t launch_few(Group &g, int batch, MxType type, hipStream_t stream) {
@@ -315,8 +335,8 @@ hipError_t launch_mx_gemv_batched(const MxDesc *W, const void *const *x, void *c
   Group g;
   g.n = 0;
   for (int i = 0; i < n; ++i) {
-    if (tiles_pay(W[i], batch)) {
-      const hipError_t e = launch_mx_gemm_tile(W[i], x[i], batch, y[i], type, nullptr, stream);
+    if (tiles_pay(W[i], batch, false)) {
+      const hipError_t e = launch_mx_gemm_tile(W[i], x[i], batch, y[i], type, false, nullptr, stream);
       if (e != hipSuccess) return e;
     } else {
       g.item[g.n++] = item_of(W[i], x[i], y[i]);
@@ -326,12 +346,12 @@ hipError_t launch_mx_gemv_batched(const MxDesc *W, const void *const *x, void *c
 }
 
 int64_t mx_gemm_ws_bytes(const MxDesc &W, int64_t batch) {
-  return tiles_pay(W, batch) ? mx_gemm_tile_ws_bytes(W, batch) : 0;
+  return tiles_pay(W, batch, true) ? mx_gemm_tile_ws_bytes(W, batch) : 0;
 }
 
 hipError_t launch_mx_gemm(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
                           void *ws, hipStream_t stream) {
-  if (tiles_pay(W, batch)) return launch_mx_gemm_tile(W, x, batch, y, type, ws, stream);
+  if (tiles_pay(W, batch, true)) return launch_mx_gemm_tile(W, x, batch, y, type, true, ws, stream);
   Group g;
   g.n = 1;
   g.item[0] = item_of(W, x, y);

@@ -290,8 +290,8 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
 constexpr TileShape kShapes[] = {
     {2, 2, 2, 1, 3.96, 2.17}, {1, 2, 1, 2, 2.83, 1.55}, {1, 1, 1, 2, 2.07, 0.73}};
 
-TilePlan plan_of(const MxDesc &W, int64_t batch) {
-  return plan_tiles(kShapes, W.rows, batch, (W.cols / 32 + 15) / 16, batch <= 8 ? 1 : 8);
+TilePlan plan_of(const MxDesc &W, int64_t batch, bool split) {
+  return plan_tiles(kShapes, W.rows, batch, (W.cols / 32 + 15) / 16, split ? 8 : 1);
 }
 
 template <MxType T, int RT, int NT, int TW, int KW>
@@ -313,15 +313,15 @@ template <MxType T> hipError_t tile_as(const TileShape &c, const TileArgs &A, hi
 
 }  // namespace
 
-double mx_gemm_tile_us(const MxDesc &W, int64_t batch) {
-  return std::max(plan_of(W, batch).us, mx_read_us(W));
+double mx_gemm_tile_us(const MxDesc &W, int64_t batch, bool split) {
+  return std::max(plan_of(W, batch, split).us, mx_read_us(W));
 }
 
-int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch) { return plan_of(W, batch).ws_bytes(); }
+int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch) { return plan_of(W, batch, true).ws_bytes(); }
 
 hipError_t launch_mx_gemm_tile(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
-                               void *ws, hipStream_t stream) {
-  const TilePlan p = plan_of(W, batch);
+                               bool split, void *ws, hipStream_t stream) {
+  const TilePlan p = plan_of(W, batch, split);
   const TileArgs A = tile_args(p, W, x, nullptr, batch, y, ws);
   return type == MxType::kF16 ? tile_as<MxType::kF16>(p.shape, A, stream)
                               : tile_as<MxType::kBF16>(p.shape, A, stream);

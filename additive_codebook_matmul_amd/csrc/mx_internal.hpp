@@ -42,12 +42,12 @@ int64_t mx_gemm_quant_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_gemm_quant(const MxDesc &W, const void *x, int64_t batch, bool ceil_rule, void *y,
                                 MxType type, void *ws, hipStream_t stream);
 // Their tile kernels (mx_gemm_tile.hip, mx_gemm_mx_tile.hip): modelled duration
-// in us, workspace, launch. Up to 8 rows of half activations K is not split
-// and no workspace needed.
-double mx_gemm_tile_us(const MxDesc &W, int64_t batch);
+// in us, workspace, launch. Without `split` K is not split over workgroups and
+// no workspace needed.
+double mx_gemm_tile_us(const MxDesc &W, int64_t batch, bool split);
 int64_t mx_gemm_tile_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_gemm_tile(const MxDesc &W, const void *x, int64_t batch, void *y, MxType type,
-                               void *ws, hipStream_t stream);
+                               bool split, void *ws, hipStream_t stream);
 double mx_gemm_mx_tile_us(const MxDesc &W, int64_t batch);
 int64_t mx_gemm_mx_tile_ws_bytes(const MxDesc &W, int64_t batch);
 hipError_t launch_mx_gemm_mx_tile(const MxDesc &W, const MxDesc &x, void *y, MxType type, void *ws,

@@ -95,7 +95,7 @@ AQLM_API int aqlm_mx_dequant(const aqlm_mx_matrix *m, int32_t type, void *W, voi
  * num_layers entries (at most 4096); x[i] is [batch][cols_i] and y[i]
  * [batch][rows_i], both of `type` (F16 or BF16). x[i] may be shared. Up to 16
  * layers go into one launch, but large ones that a tile kernel serves better
- * (from two rows on) into one each. Results are bit-identical to calls with one
+ * (from three rows on) into one each. Results are bit-identical to calls with one
  * layer.
  */
 AQLM_API int aqlm_mx_gemv_batched(const aqlm_mx_matrix *W, const void *const *x, void *const *y,
@@ -103,8 +103,9 @@ AQLM_API int aqlm_mx_gemv_batched(const aqlm_mx_matrix *W, const void *const *x,
 
 /*
  * aqlm_mx_gemm: y [batch][rows] = x [batch][cols] . W^T for any batch
- * (0: no-op), x and y of `type` (F16 or BF16). Up to 8 rows it runs
- * aqlm_mx_gemv_batched's kernels and gives its bits. Weights are expanded in
+ * (0: no-op), x and y of `type` (F16 or BF16). Up to 2 rows it gives
+ * aqlm_mx_gemv_batched's bits; from 3 on it may split K over workgroups, which
+ * that entry point, without a workspace, does not. Weights are expanded in
  * registers on their way to the matrix instructions and never written.
  *   workspace  at least aqlm_mx_gemm_workspace_size bytes (NULL where that is
  *              0): float32 partial sums where K is split over workgroups;
