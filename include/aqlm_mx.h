@@ -133,8 +133,9 @@ AQLM_API int aqlm_mx_gemm_mx(const aqlm_mx_matrix *W, const aqlm_mx_matrix *x, v
  * aqlm_mx_gemm_quant: y [batch][rows] = Q(x) . W^T with x [batch][cols] of
  * `type` (F16 or BF16) quantised by aqlm_mx_quantize's `rule` on the way, y of
  * the same type: aqlm_mx_quantize and aqlm_mx_gemm_mx in one call, with
- * their bits. batch == 0 is a no-op. Workspace as above, the activations' codes
- * and scales among it (never 0 bytes for a batch of 1 or more).
+ * their bits but at 5 and 6 rows, where the sums may be added in another order.
+ * batch == 0 is a no-op. Workspace as above, the activations' codes and scales
+ * among it where they are written.
  */
 AQLM_API int aqlm_mx_gemm_quant_workspace_size(const aqlm_mx_matrix *W, int64_t batch,
                                                int64_t *bytes);

@@ -251,6 +251,57 @@ def test_large_products_and_gradients_exact(batch, out, n_in):
         ok_dx()
 
 
+# A few rows of activations, with rows of W longer than the part of x that a
+# workgroup holds, ends inside every unit, and W on both sides of the choice of
+# kernel.
+FEW = [(1, 50, 65600), (1, 50, 16416), (1, 8200, 96), (2, 70, 8224), (2, 33, 20000), (2, 9001, 64),
+       (3, 20, 20512), (4, 35, 16448), (5, 18, 12320), (6, 21, 10272), (5, 8193, 160),
+       (6, 9000, 288), (7, 40, 12320), (8, 33, 16416)]
+
+
+@pytest.mark.parametrize("batch,out,n_in", FEW)
+def test_few_rows_exact(batch, out, n_in):
+    packed, scales, w = whole_weights(out, n_in, batch + out)
+    xp, xs, xm = whole_weights(batch, n_in, 7 * batch + n_in, 127, 128)
+    x = whole(batch, n_in, n_in + batch)
+    assert (np.abs(xm) @ np.abs(w).T).max() * 16 < 1 << 24
+    layer = MxLayer(dev(packed), dev(scales))
+    want_y, want_mx = x @ w.T, xm @ w.T
+    for dtype in HALVES:
+        xd = rounded(x, dtype).to(DEV)
+        for call, want in ((lambda y: layer.gemm(xd, out=y), want_y),
+                           (lambda y: mx_gemv_batched([layer], [xd], [y]), want_y),
+                           (lambda y: layer.gemm_mx(dev(xp), dev(xs), dtype, out=y), want_mx),
+                           (lambda y: layer.forward_mx(xd, "floor", out=y), want_y),
+                           (lambda y: layer.forward_mx(xd, "ceil", out=y), want_y)):
+            y, ok = guarded((batch, out), dtype)
+            call(y)
+            same(y, rounded(want, dtype))
+            ok()
+
+
+@pytest.mark.parametrize("rule", ["floor", "ceil"])
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("batch", [1, 2, 3, 4, 5, 6])
+def test_quantised_on_the_way_like_by_itself(batch, dtype, rule):
+    """Activations of every size, blocks of zeros, infinities and NaN: what the product quantises
+    on the way is what mx_quantize gives (a block of 32 times one-hot rows of W, exactly)."""
+    n_in = 32 * 70
+    x = _values(batch, n_in, dtype, batch)
+    if batch > 3:
+        x[2, 2000], x[3, 100] = float("nan"), float("-inf")
+    w = np.zeros((n_in, n_in), dtype=np.uint8)
+    w[np.arange(n_in), np.arange(n_in)] = 2                    # 1.0
+    layer = MxLayer(dev(MO.pack(w)), torch.full((n_in, n_in // 32), 127, dtype=torch.uint8, device=DEV))
+    got = layer.forward_mx(x.to(DEV), rule)
+    q = mx_dequant(*mx_quantize(x.to(DEV), rule), torch.float32).cpu().double()
+    bad = q.isnan().view(batch, -1, 32).any(2)                 # NaN blocks reach every row of W
+    rows = ~bad.any(1)
+    want = q.float().to(dtype)
+    assert torch.equal(got.cpu()[rows] + 0.0, want[rows] + 0.0)
+    assert bool(got.cpu()[~rows].isnan().all())
+
+
 @pytest.mark.parametrize("dtype", HALVES)
 def test_arrays_past_32_bit_offsets(dtype):
     """Codes, activations and results above 4 GiB: the far end's results are those of the far end

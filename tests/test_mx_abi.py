@@ -118,7 +118,7 @@ def test_gemm_quant_refusals():
     assert f(M(), FAKE, 1, 0, MISALIGNED, 0, FAKE, big, None) == ALIGN
     assert f(M(), None, 0, 0, None, 0, None, 0, None) == 0
     n, own = ctypes.c_int64(-1), ctypes.c_int64(-1)
-    for rows, cols, batch in ((1, 32, 1), (4096, 11008, 77), (300, 1 << 15, 300)):
+    for rows, cols, batch in ((64, 32, 7), (4096, 11008, 77), (300, 1 << 15, 300)):
         assert size(M(rows, cols), batch, ctypes.byref(n)) == 0
         assert mx._lib().aqlm_mx_gemm_mx_workspace_size(M(rows, cols), batch, ctypes.byref(own)) == 0
         assert n.value >= batch * cols * 17 // 32 + own.value
