@@ -29,13 +29,20 @@ struct Group {
 // chunk c multiplies codes 8 s .. 8 s + 7 of every block, so its activation
 // operand is the 16 bytes of inputs 8 s of the same block of the lane's token.
 // (The sum over K does not care which inputs meet in one instruction, so no
-// code changes lanes.) The wavefronts' float32 sums meet in LDS in a fixed
-// order. What bounds it are requests, a 128-byte line each: scales byte by byte
-// cost as many as the codes (4096 x 4096 at 2 rows 5.1 us, 11008 x 4096 at 8
-// 14.9; this 4.5 and 14.4).
-template <MxType T, int NW>
+// code changes lanes.) Activations pass through LDS, which belongs to the
+// wavefront alone: in whole lines to it, spread over the banks from it, a group
+// of 512 inputs of up to 8 rows (H = 1) or half of it of up to 16 (H = 2) at a
+// time. The wavefronts' float32 sums meet in LDS in a fixed order.
+// What bounds it are requests, a 128-byte line each: scales byte by byte cost as
+// many as the codes, activations read by each lane for itself more (4 rows: 4096 x
+// 4096 5.7 us, 11008 x 4096 12.0), and codes loaded past the L1, which has the
+// line's second half ready, double (5.1 and 8.9; this 4.5 and 7.8).
+template <MxType T, int NW, int H>
 __global__ __launch_bounds__(NW * 64) void mx_skinny_kernel(const Group g, const int batch) {
-  __shared__ __attribute__((aligned(16))) float4_t red[NW * 64];
+  constexpr int kLoads = 8;                     // of x into LDS, at most
+  constexpr int kChunkBits = H == 1 ? 6 : 5;    // of 64 / H chunks of 16 bytes of a token
+  extern __shared__ __attribute__((aligned(16))) uint8_t xs[];  // [NW][loads][1 KiB]
+  const uint32_t mine = (threadIdx.x >> 6) * (uint32_t)((batch + H - 1) / H) * 1024u;  // the wavefront's
   int li = 0;
   while (li + 1 < g.n && (int)blockIdx.x >= g.first[li + 1]) ++li;
   const Group::Item &L = g.item[li];
@@ -56,48 +63,77 @@ __global__ __launch_bounds__(NW * 64) void mx_skinny_kernel(const Group g, const
   const Rsrc xrs = make_rsrc(L.x, (uint32_t)batch * cols * 2u);
   const uint32_t srow = (uint32_t)min(r16, tile_rows - 1) * nb + base;
 
+  // Activations of blocks from..from + 16 / H - 1 into the wavefront's LDS: a load
+  // takes 1 KiB, a token (two with H = 2), in whole lines. Chunk j of token t lies
+  // at place j ^ t, which spreads the 16 tokens of a read over the banks: the lane
+  // that fills a place reads the chunk that belongs there.
+  const int lt = lane >> kChunkBits, lp = lane & ((1 << kChunkBits) - 1);
+  auto fill = [&](int from) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if (i * H >= batch) break;
+      const int t = i * H + lt, j = lp ^ (t & 15), blk = from + (j >> 2);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          xrs, (__attribute__((address_space(3))) void *)(xs + (__builtin_amdgcn_readfirstlane(mine) + i * 1024)), 16,
+          blk < nb && t < batch ? (uint32_t)t * cols * 2u + (uint32_t)from * 64u + 16u * j : kMxOOB, 0, 0, 0);
+    }
+  };
+  // (tokens past the last read another's: their results are not stored)
+  const int tok = min(r16, batch - 1);
+  auto x_of = [&](int c, int s) __attribute__((always_inline)) {  // c: chunk of 128 inputs in LDS
+    const int j = (4 * c + q) * 4 + s;
+    return *reinterpret_cast<const uint4 *>(xs + (mine + tok * (1024 / H) + ((j ^ (tok & 15)) << 4)));
+  };
+
   float4_t acc = {0.f, 0.f, 0.f, 0.f};
   for (int gr = wave; 16 * gr < nb; gr += NW) {
-    uint4 w[4], x[4][4];
+    uint4 w[4];
+    fill(16 * gr);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int blk = 16 * gr + 4 * c + q;
-      w[c] = buf_load16_nt(crs, blk < nb ? (uint32_t)r16 * half + (uint32_t)blk * 16u : kMxOOB);
+      w[c] = buf_load16(crs, blk < nb ? (uint32_t)r16 * half + (uint32_t)blk * 16u : kMxOOB);
     }
     const uint4 sc = mx_scales16(srs, srow, 16 * gr, nb);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int blk = 16 * gr + 4 * c + q;
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        x[c][s] = buf_load16(xrs, blk < nb ? (uint32_t)r16 * cols * 2u + (uint32_t)blk * 64u + 16u * s : kMxOOB);
-    }
     const uint32_t sb[4] = {(sc.x >> (8 * q)) & 0xFFu, (sc.y >> (8 * q)) & 0xFFu, (sc.z >> (8 * q)) & 0xFFu,
                             (sc.w >> (8 * q)) & 0xFFu};
     bool fits = true;
     if constexpr (T == MxType::kF16)
       fits = __all(mx_fits_f16(sb[0]) && mx_fits_f16(sb[1]) && mx_fits_f16(sb[2]) && mx_fits_f16(sb[3]));
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    auto products = [&](int c) __attribute__((always_inline)) {
       const uint32_t ww[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
       const float sv = mx_scale(sb[c]);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
+        const uint4 x = x_of(c % (4 / H), s);
         if (fits) {
-          acc = mx_mfma16<T>(mx_decode8<T>(ww[s], sv), x[c][s], acc);
+          acc = mx_mfma16<T>(mx_decode8<T>(ww[s], sv), x, acc);
         } else {
           // scales that float16 weights cannot take: the same product in
           // bfloat16, which holds every weight, with x split exactly in two
           uint4 hi, lo;
-          split_f16(x[c][s], hi, lo);
+          split_f16(x, hi, lo);
           const uint4 a = mx_decode8<MxType::kBF16>(ww[s], sv);
           acc = mx_mfma16<MxType::kBF16>(a, hi, acc);
           acc = mx_mfma16<MxType::kBF16>(a, lo, acc);
         }
       }
+    };
+    products(0);
+    products(1);
+    if constexpr (H == 2) {
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+      fill(16 * gr + 8);
+      asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
     }
+    products(2);
+    products(3);
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // (before x is overwritten)
   }
 
+  __syncthreads();
+  float4_t *const red = reinterpret_cast<float4_t *>(xs);  // (1 KiB a wavefront)
   red[threadIdx.x] = acc;
   __syncthreads();
   // lane (t, q) holds rows 4 q .. 4 q + 3 of token t
@@ -109,14 +145,15 @@ __global__ __launch_bounds__(NW * 64) void mx_skinny_kernel(const Group g, const
   }
 }
 
-template <MxType T, int NW> hipError_t launch_skinny(Group &g, int batch, hipStream_t stream) {
+template <MxType T, int NW, int H> hipError_t launch_skinny(Group &g, int batch, hipStream_t stream) {
   int blocks = 0;
   for (int i = 0; i < g.n; ++i) {
     g.first[i] = blocks;
     blocks += (g.item[i].rows + 15) / 16;
   }
   g.first[g.n] = blocks;
-  hipLaunchKernelGGL((mx_skinny_kernel<T, NW>), dim3((unsigned)blocks), dim3(NW * 64), 0, stream, g, batch);
+  hipLaunchKernelGGL((mx_skinny_kernel<T, NW, H>), dim3((unsigned)blocks), dim3(NW * 64),
+                     NW * 1024 * ((batch + H - 1) / H), stream, g, batch);
   return hipGetLastError();
 }
 
@@ -298,10 +335,10 @@ Group::Item item_of(const MxDesc &W, const void *x, void *y) {
 constexpr int kSkinnyWaves = 8;
 
 // From three rows on, where the tile kernel is the faster: the skinny one takes
-// 1.1 ns and 0.1 ns a row of activations for 16 rows of W and a group of K,
-// spread over the chip, or, with few rows, 1.8 us and 0.2 us a row for each turn
-// of its wavefronts (fitted to 1024 x 8192 .. 28672 x 8192 from 2 to 16 rows:
-// 4096 x 4096 at 8 rows 6.3 us against 9.6, 28672 x 8192 59 against 35).
+// 0.84 ns and 0.046 ns a row of activations for 16 rows of W and a group of K,
+// spread over the chip, or, with few rows of W, 1.15 us and 0.07 us a row for each
+// turn of its wavefronts (fitted to 1024 x 8192 .. 28672 x 8192 from 3 to 16 rows:
+// 4096 x 4096 at 8 rows 4.7 us against 9.6, 28672 x 8192 38 against 34).
 // Whole-row wavefronts serve two rows of activations better than either (4096 x
 // 4096 3.9 us against 4.5, 11008 x 4096 7.9 against 10.8, 28672 x 8192 33 against
 // 34, 8192 x 28672 30 against 41), three about as well, four and more worse.
@@ -311,8 +348,8 @@ bool tiles_pay(const MxDesc &W, int64_t batch, bool split) {
   if (batch <= 2) return false;
   const double groups = (double)((W.cols / 32 + 15) / 16), tiles = (double)((W.rows + 15) / 16);
   const double turns = (double)(int64_t)((groups + kSkinnyWaves - 1) / kSkinnyWaves);
-  const double us = std::max(2.5 + tiles * groups * (1.1e-3 + 0.1e-3 * (double)batch),
-                             2.5 + turns * (1.8 + 0.2 * (double)batch));
+  const double us = 2.7 + std::max(tiles * groups * (0.84e-3 + 0.046e-3 * (double)batch),
+                                   turns * (1.15 + 0.07 * (double)batch));
   return mx_gemm_tile_us(W, batch, split) < us;
 }
 
@@ -320,7 +357,8 @@ bool tiles_pay(const MxDesc &W, int64_t batch, bool split) {
 template <MxType T> hipError_t few_as(Group &g, int batch, hipStream_t stream) {
   if (batch == 1) return rows_as<T, 1>(g, batch, stream);
   if (batch == 2) return rows_as<T, 2>(g, batch, stream);
-  return launch_skinny<T, kSkinnyWaves>(g, batch, stream);
+  if (batch <= 8) return launch_skinny<T, kSkinnyWaves, 1>(g, batch, stream);
+  return launch_skinny<T, kSkinnyWaves, 2>(g, batch, stream);
 }
 
 hipError_t launch_few(Group &g, int batch, MxType type, hipStream_t stream) {

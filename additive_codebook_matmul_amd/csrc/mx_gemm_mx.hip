@@ -53,7 +53,7 @@ __global__ __launch_bounds__(NW * 64) void mx_mx_skinny_kernel(
     for (int c = 0; c < 4; ++c) {
       const int blk = 16 * gr + 4 * c + q;
       const uint32_t at = blk < nb ? (uint32_t)r16 * half + (uint32_t)blk * 16u : kMxOOB;
-      w[c] = buf_load16_nt(crs, at);
+      w[c] = buf_load16(crs, at);
       x[c] = buf_load16(xrs, at);
     }
     const uint4 sw = mx_scales16(srs, srow, 16 * gr, nb), sx = mx_scales16(xss, xrow, 16 * gr, nb);
@@ -82,7 +82,7 @@ hipError_t launch_skinny(const MxDesc &W, const MxDesc &x, void *y, hipStream_t 
   return hipGetLastError();
 }
 
-// Up to eight rows of activations (batch of B): whole rows of W by a wavefront,
+// Up to five rows of activations (B): whole rows of W by a wavefront,
 // R at a time, as for half activations (mx_rows_kernel; 28672 x 8192 at one row
 // 23.2 us, 5.4 TB/s): lane (m, q) = (lane % 16, lane / 16) gives its own block of W's
 // row and the same block of x, so that the result's diagonal (m, m) holds the sums
@@ -222,41 +222,40 @@ hipError_t rows_as(const MxDesc &W, const void *x, const uint8_t *xsc, int batch
   else if (batch == 2) launch_rows<T, 2, Q>(W, x, xsc, batch, y, stream);
   else if (batch == 3) launch_rows<T, 3, Q>(W, x, xsc, batch, y, stream);
   else if (batch == 4) launch_rows<T, 4, Q>(W, x, xsc, batch, y, stream);
-  else if (batch == 5) launch_rows<T, 5, Q>(W, x, xsc, batch, y, stream);
-  else launch_rows<T, 6, Q>(W, x, xsc, batch, y, stream);
+  else launch_rows<T, 5, Q>(W, x, xsc, batch, y, stream);
   return hipGetLastError();
 }
 
-// Where whole-row wavefronts are the faster: up to four rows of activations (one
-// row, against the better of the other two: 4096 x 4096 2.7 us, 3.6; 28672 x 8192
-// 23.2, 27.0; four rows 4.4, 4.4 and 25.9, 27.1), with five and six, whose sums
-// leave room for two workgroups a CU, while those hold all of W (five rows: 8192 x
-// 28672 24.0, 29.3; 11008 x 4096 8.7, 8.0).
+// Where whole-row wavefronts are the faster: one or two rows of activations
+// (against the better of the other two kernels, 4096 x 4096 2.7 us, 3.6, 28672 x
+// 8192 23.3, 27.0), up to four where W has many rows, up to five where they are
+// long (four rows: 11008 x 4096 6.8, 7.4, 4096 x 4096 4.4, 3.7; five: 8192 x 28672
+// 24.5, 29.4, 11008 x 4096 8.2, 7.7).
 bool rows_pay(const MxDesc &W, int64_t batch) {
-  return batch <= 4 || (batch <= 6 && W.rows <= 512 * kWaveRows * (kRowThreads / 64));
+  return batch <= (W.cols > 16384 ? 5 : W.rows > 4096 ? 4 : 2);
 }
 
 // Whether they also quantise x, every workgroup again, rather than a launch of its
-// own, which takes 2 us: up to about 480 million steps of K in all rows and
-// tokens (one row: 4096 x 4096 2.9, 4.5 us; five rows of 11008 x 4096 9.9, 10.3;
-// three of 28672 x 8192 27.3, 26.6, five of them 34.4, 29.8).
+// own, which takes 2 us: up to five rows and about 480 million steps of K in all
+// rows and tokens (one row: 4096 x 4096 2.9, 4.5 us; five rows of 4096 x 4096 5.4,
+// 5.8; three of 28672 x 8192 27.3, 26.6, five of them 34.4, 29.8).
 bool quant_pays(const MxDesc &W, int64_t batch) {
-  return batch <= 6 && W.rows * W.cols * batch <= (int64_t)480 << 20;
+  return batch <= 5 && W.rows * W.cols * batch <= (int64_t)480 << 20;
 }
 
 constexpr int kSkinnyWaves = 8;
 
-// Of the others, where the tile kernel is the faster: the skinny one takes 0.9 ns and 0.02 ns a
-// row of activations for 16 rows of W and a group of K, spread over the chip,
-// or, with few rows, 1.1 us and 0.07 us a row for each turn of its wavefronts
-// (fitted to 1024 x 8192 .. 28672 x 8192 at 1, 5 and 16 rows: 4096 x 4096 at 5
-// 4.3 us against 6.6, 28672 x 8192 32.2 against 27.4).
+// Of the others, where the tile kernel is the faster: the skinny one takes 0.82 ns
+// and 0.022 ns a row of activations for 16 rows of W and a group of K, spread over
+// the chip, or, with few rows of W, 1 us and 0.05 us a row for each turn of its
+// wavefronts (fitted to 1024 x 8192 .. 28672 x 8192 from 2 to 16 rows: 4096 x 4096
+// at 5 3.8 us against 6.6, 28672 x 8192 at 16 36.5 against 27.8).
 bool tiles_pay(const MxDesc &W, int64_t batch) {
   if (batch > 16) return true;
   const double groups = (double)((W.cols / 32 + 15) / 16), tiles = (double)((W.rows + 15) / 16);
   const double turns = (double)(int64_t)((groups + kSkinnyWaves - 1) / kSkinnyWaves);
-  const double us = std::max(2.5 + tiles * groups * (0.9e-3 + 0.02e-3 * (double)batch),
-                             2.5 + turns * (1.1 + 0.07 * (double)batch));
+  const double us = 2.7 + std::max(tiles * groups * (0.82e-3 + 0.022e-3 * (double)batch),
+                                   turns * (1.0 + 0.05 * (double)batch));
   return mx_gemm_mx_tile_us(W, batch) < us;
 }
 

@@ -133,7 +133,7 @@ AQLM_API int aqlm_mx_gemm_mx(const aqlm_mx_matrix *W, const aqlm_mx_matrix *x, v
  * aqlm_mx_gemm_quant: y [batch][rows] = Q(x) . W^T with x [batch][cols] of
  * `type` (F16 or BF16) quantised by aqlm_mx_quantize's `rule` on the way, y of
  * the same type: aqlm_mx_quantize and aqlm_mx_gemm_mx in one call, with
- * their bits but at 5 and 6 rows, where the sums may be added in another order.
+ * their bits but at 3 to 5 rows, where the sums may be added in another order.
  * batch == 0 is a no-op. Workspace as above, the activations' codes and scales
  * among it where they are written.
  */

@@ -213,7 +213,7 @@ def test_grad_input_exact(batch, out, n_in, dtype):
 
 @pytest.mark.parametrize("rule", ["floor", "ceil"])
 @pytest.mark.parametrize("dtype", HALVES)
-@pytest.mark.parametrize("batch,out,n_in", [(1, 40, 32), (3, 129, 2080), (9, 65, 4128), (77, 301, 1376), (300, 520, 1024)])
+@pytest.mark.parametrize("batch,out,n_in", [(1, 40, 32), (2, 129, 2080), (9, 65, 4128), (77, 301, 1376), (300, 520, 1024)])
 def test_forward_mx_gives_the_bits_of_its_parts(batch, out, n_in, dtype, rule):
     layer, _ = _layer(out, n_in, 2)
     x = rounded(np.random.default_rng(batch).standard_normal((batch, n_in)) * 3, dtype).to(DEV)
