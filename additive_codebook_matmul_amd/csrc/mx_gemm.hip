@@ -38,7 +38,7 @@ struct Group {
 // 4096 5.7 us, 11008 x 4096 12.0), and codes loaded past the L1, which has the
 // line's second half ready, double (5.1 and 8.9; this 4.5 and 7.8).
 template <MxType T, int NW, int H>
-__global__ __launch_bounds__(NW * 64) void mx_skinny_kernel(const Group g, const int batch) {
+__global__ __launch_bounds__(NW * 64, H == 1 ? 6 : 5) void mx_skinny_kernel(const Group g, const int batch) {
   constexpr int kLoads = 8;                     // of x into LDS, at most
   constexpr int kChunkBits = H == 1 ? 6 : 5;    // of 64 / H chunks of 16 bytes of a token
   extern __shared__ __attribute__((aligned(16))) uint8_t xs[];  // [NW][loads][1 KiB]
@@ -105,30 +105,37 @@ __global__ __launch_bounds__(NW * 64) void mx_skinny_kernel(const Group g, const
       const uint32_t ww[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
       const float sv = mx_scale(sb[c]);
 #pragma unroll
+      for (int s = 0; s < 4; ++s) acc = mx_mfma16<T>(mx_decode8<T>(ww[s], sv), x_of(c % (4 / H), s), acc);
+    };
+    // scales that float16 weights cannot take: the same product in bfloat16,
+    // which holds every weight, with x split exactly in two
+    auto wide_products = [&](int c) __attribute__((always_inline)) {
+      const uint32_t ww[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+      const float sv = mx_scale(sb[c]);
+#pragma unroll 1
       for (int s = 0; s < 4; ++s) {
-        const uint4 x = x_of(c % (4 / H), s);
-        if (fits) {
-          acc = mx_mfma16<T>(mx_decode8<T>(ww[s], sv), x, acc);
-        } else {
-          // scales that float16 weights cannot take: the same product in
-          // bfloat16, which holds every weight, with x split exactly in two
-          uint4 hi, lo;
-          split_f16(x, hi, lo);
-          const uint4 a = mx_decode8<MxType::kBF16>(ww[s], sv);
-          acc = mx_mfma16<MxType::kBF16>(a, hi, acc);
-          acc = mx_mfma16<MxType::kBF16>(a, lo, acc);
-        }
+        uint4 hi, lo;
+        split_f16(x_of(c % (4 / H), s), hi, lo);
+        const uint4 a = mx_decode8<MxType::kBF16>(s == 0 ? ww[0] : s == 1 ? ww[1] : s == 2 ? ww[2] : ww[3], sv);
+        acc = mx_mfma16<MxType::kBF16>(a, hi, acc);
+        acc = mx_mfma16<MxType::kBF16>(a, lo, acc);
       }
     };
-    products(0);
-    products(1);
-    if constexpr (H == 2) {
-      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
-      fill(16 * gr + 8);
-      asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+#pragma unroll
+    for (int part = 0; part < H; ++part) {
+      if (part > 0) {
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        fill(16 * gr + 8);
+        asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+      }
+      if (fits) {
+#pragma unroll
+        for (int c = 0; c < 4 / H; ++c) products(part * (4 / H) + c);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4 / H; ++c) wide_products(part * (4 / H) + c);
+      }
     }
-    products(2);
-    products(3);
     asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // (before x is overwritten)
   }
 
