@@ -14,6 +14,7 @@ fallback: a missing library or a failing call raises.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -49,8 +50,7 @@ def _lib() -> ctypes.CDLL:
         M = ctypes.POINTER(MxMatrixStruct)
         lib.aqlm_mx_quantize.argtypes = [P, I32, I64, I64, I32, P, P, P]
         lib.aqlm_mx_dequant.argtypes = [M, I32, P, P]
-        lib.aqlm_mx_gemv_batched.argtypes = [M, ctypes.POINTER(P), ctypes.POINTER(P), I32, I64, I32,
-                                             P]
+        lib.aqlm_mx_gemv_batched.argtypes = [P, P, P, I32, I64, I32, P]
         for name in ("gemm", "gemm_mx", "gemm_quant", "grad_input"):
             getattr(lib, f"aqlm_mx_{name}_workspace_size").argtypes = [M, I64, ctypes.POINTER(I64)]
         lib.aqlm_mx_gemm.argtypes = [M, P, I64, P, I32, P, I64, P]
@@ -159,6 +159,7 @@ class MxLayer:
         self.device = codes.device
         self._struct = MxMatrixStruct(rows, cols, codes.data_ptr(), scales.data_ptr())
         self._ref = ctypes.byref(self._struct)
+        self._raw = bytes(self._struct)
         self._ws_bytes = {}  # (operator, batch) -> bytes: a rule of sizes alone
 
     @classmethod
@@ -288,8 +289,7 @@ def mx_gemv_batched(layers, xs, outs=None):
         ys = list(torch.empty((n, batch, sizes[0]), dtype=dtype, device=device).unbind(0))
     else:
         ys = [torch.empty((batch, k), dtype=dtype, device=device) for k in sizes]
-    structs = (MxMatrixStruct * n)(*[L._struct for L in layers])
-    xp = (ctypes.c_void_p * n)(*[x.data_ptr() for x in xs])
-    yp = (ctypes.c_void_p * n)(*[y.data_ptr() for y in ys])
-    _call(device, _lib().aqlm_mx_gemv_batched, structs, xp, yp, n, batch, MX_TYPES[dtype])
+    _call(device, _lib().aqlm_mx_gemv_batched, b"".join([L._raw for L in layers]),
+          struct.pack(f"{n}P", *[x.data_ptr() for x in xs]),
+          struct.pack(f"{n}P", *[y.data_ptr() for y in ys]), n, batch, MX_TYPES[dtype])
     return ys
