@@ -31,6 +31,7 @@ MX_SYMBOLS = ("aqlm_mx_quantize", "aqlm_mx_dequant", "aqlm_mx_gemv_batched",
               "aqlm_mx_grad_input_workspace_size", "aqlm_mx_grad_input")
 
 _HALVES = (torch.float16, torch.bfloat16)
+_BYTES = (torch.uint8,)
 
 
 class MxMatrixStruct(ctypes.Structure):
@@ -86,20 +87,19 @@ def _check_dense(t: torch.Tensor, what: str, dtypes, shape=None) -> None:
     if t.dtype not in dtypes or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
         names = ", ".join(str(d).replace("torch.", "") for d in dtypes)
         raise ValueError(f"{what} must be a contiguous 2-D tensor on the GPU, of type {names}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
 
 
 def _check_packed(codes: torch.Tensor, scales: torch.Tensor) -> Tuple[int, int]:
-    _check_dense(codes, "codes", (torch.uint8,))
-    _check_dense(scales, "scales", (torch.uint8,))
+    _check_dense(codes, "codes", _BYTES)
+    _check_dense(scales, "scales", _BYTES)
     rows, half = codes.shape
-    cols = 2 * half
-    if cols < MX_BLOCK or cols % MX_BLOCK or tuple(scales.shape) != (rows, cols // MX_BLOCK):
+    if half < MX_BLOCK // 2 or half % (MX_BLOCK // 2) or scales.shape != (rows, half // (MX_BLOCK // 2)):
         raise ValueError("codes are [rows, cols/2] and scales [rows, cols/32], cols a multiple of 32")
     if codes.device != scales.device:
         raise ValueError("codes and scales must be on one device")
-    return rows, cols
+    return rows, 2 * half
 
 
 def _output(out: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
