@@ -14,7 +14,7 @@ namespace {
 constexpr int kCThreads = 256;
 constexpr int kCUnroll = 4;  // octets per thread, a block's threads apart
 
-template <MxType T, bool CEIL>
+template <MxType T, bool CEIL, bool NT>
 __global__ __launch_bounds__(kCThreads) void mx_quantize_kernel(const void *__restrict__ x,
                                                                 uint32_t *__restrict__ codes,
                                                                 uint8_t *__restrict__ scales,
@@ -28,7 +28,7 @@ __global__ __launch_bounds__(kCThreads) void mx_quantize_kernel(const void *__re
 #pragma unroll
     for (int u = 0; u < kCUnroll; ++u) {
       const int64_t i = base + u * kCThreads;
-      if (i < octets) o[u] = load_octet<T>(x, i);
+      if (i < octets) o[u] = load_octet<T, NT>(x, i);
       else o[u] = {};
     }
 #pragma unroll
@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kCThreads) void mx_quantize_kernel(const void *__re
   }
 }
 
-template <MxType T>
+template <MxType T, bool NT>
 __global__ __launch_bounds__(kCThreads) void mx_dequant_kernel(const uint32_t *__restrict__ codes,
                                                                const uint8_t *__restrict__ scales,
                                                                u32x4_t *__restrict__ W,
@@ -76,7 +76,8 @@ __global__ __launch_bounds__(kCThreads) void mx_dequant_kernel(const uint32_t *_
         W[2 * i + 1] = u32x4_t{v[2].x, v[2].y, v[3].x, v[3].y};
       } else {
         const uint4 r = mx_decode8<T>(c[u], s);
-        W[i] = u32x4_t{r.x, r.y, r.z, r.w};
+        if constexpr (NT) __builtin_nontemporal_store(u32x4_t{r.x, r.y, r.z, r.w}, W + i);
+        else W[i] = u32x4_t{r.x, r.y, r.z, r.w};
       }
     }
   }
@@ -89,16 +90,46 @@ unsigned convert_grid(int64_t octets) {
   return (unsigned)std::min<int64_t>((octets + per - 1) / per, int64_t(1) << 22);
 }
 
-template <MxType T>
-void quantize_as(const void *x, int64_t octets, bool ceil_rule, uint8_t *codes, uint8_t *scales,
-                 hipStream_t stream) {
+// From these sizes of a half matrix on it is read, or written, without a place in
+// the caches. A matrix to quantise is read once: 90 MB 22.1 us, without caching
+// 19.2 (48.4 and 42.8 together with the kernel that writes it), 470 MB 103.4 and
+// 99.9, but 45 MB that lie in the cache 9.9 and 10.5. What is expanded may be read
+// next, so that only what the last-level cache (256 MB) cannot hold passes it: 470
+// MB 101.3 and 97.1, and 254 and 250 together with a kernel that reads it; 90 MB
+// 24.2 and 17.5, but 47 and 54. (470 MB quantised and expanded in turn: 223 and
+// 174.) float32, whose eight values are two accesses, only loses: 940 MB expanded
+// 246 and 374.
+constexpr int64_t kNtLoad = (int64_t)64 << 20, kNtStore = (int64_t)256 << 20;
+
+template <MxType T, bool CEIL>
+void quantize_as(const void *x, int64_t octets, uint8_t *codes, uint8_t *scales, hipStream_t stream) {
+  const dim3 grid(convert_grid(octets)), block(kCThreads);
   uint32_t *cw = reinterpret_cast<uint32_t *>(codes);
-  if (ceil_rule)
-    hipLaunchKernelGGL((mx_quantize_kernel<T, true>), dim3(convert_grid(octets)), dim3(kCThreads), 0,
-                       stream, x, cw, scales, octets);
-  else
-    hipLaunchKernelGGL((mx_quantize_kernel<T, false>), dim3(convert_grid(octets)), dim3(kCThreads),
-                       0, stream, x, cw, scales, octets);
+  if constexpr (T != MxType::kF32)
+    if (octets * 16 >= kNtLoad) {
+      hipLaunchKernelGGL((mx_quantize_kernel<T, CEIL, true>), grid, block, 0, stream, x, cw, scales, octets);
+      return;
+    }
+  hipLaunchKernelGGL((mx_quantize_kernel<T, CEIL, false>), grid, block, 0, stream, x, cw, scales, octets);
+}
+
+template <MxType T>
+void quantize_by(const void *x, int64_t octets, bool ceil_rule, uint8_t *codes, uint8_t *scales, hipStream_t stream) {
+  if (ceil_rule) quantize_as<T, true>(x, octets, codes, scales, stream);
+  else quantize_as<T, false>(x, octets, codes, scales, stream);
+}
+
+template <MxType T> void dequant_as(const MxDesc &m, void *W, hipStream_t stream) {
+  const int64_t octets = m.rows * m.cols / 8;
+  const dim3 grid(convert_grid(octets)), block(kCThreads);
+  const uint32_t *codes = reinterpret_cast<const uint32_t *>(m.codes);
+  u32x4_t *out = static_cast<u32x4_t *>(W);
+  if constexpr (T != MxType::kF32)
+    if (octets * 16 >= kNtStore) {
+      hipLaunchKernelGGL((mx_dequant_kernel<T, true>), grid, block, 0, stream, codes, m.scales, out, octets);
+      return;
+    }
+  hipLaunchKernelGGL((mx_dequant_kernel<T, false>), grid, block, 0, stream, codes, m.scales, out, octets);
 }
 
 }  // namespace
@@ -108,31 +139,18 @@ hipError_t launch_mx_quantize(const void *x, MxType type, int64_t rows, int64_t 
                               hipStream_t stream) {
   const int64_t octets = rows * cols / 8;
   switch (type) {
-    case MxType::kF16: quantize_as<MxType::kF16>(x, octets, ceil_rule, codes, scales, stream); break;
-    case MxType::kBF16: quantize_as<MxType::kBF16>(x, octets, ceil_rule, codes, scales, stream); break;
-    case MxType::kF32: quantize_as<MxType::kF32>(x, octets, ceil_rule, codes, scales, stream); break;
+    case MxType::kF16: quantize_by<MxType::kF16>(x, octets, ceil_rule, codes, scales, stream); break;
+    case MxType::kBF16: quantize_by<MxType::kBF16>(x, octets, ceil_rule, codes, scales, stream); break;
+    case MxType::kF32: quantize_by<MxType::kF32>(x, octets, ceil_rule, codes, scales, stream); break;
   }
   return hipGetLastError();
 }
 
 hipError_t launch_mx_dequant(const MxDesc &m, MxType type, void *W, hipStream_t stream) {
-  const int64_t octets = m.rows * m.cols / 8;
-  const dim3 grid(convert_grid(octets)), block(kCThreads);
-  const uint32_t *codes = reinterpret_cast<const uint32_t *>(m.codes);
-  u32x4_t *out = static_cast<u32x4_t *>(W);
   switch (type) {
-    case MxType::kF16:
-      hipLaunchKernelGGL(mx_dequant_kernel<MxType::kF16>, grid, block, 0, stream, codes, m.scales,
-                         out, octets);
-      break;
-    case MxType::kBF16:
-      hipLaunchKernelGGL(mx_dequant_kernel<MxType::kBF16>, grid, block, 0, stream, codes, m.scales,
-                         out, octets);
-      break;
-    case MxType::kF32:
-      hipLaunchKernelGGL(mx_dequant_kernel<MxType::kF32>, grid, block, 0, stream, codes, m.scales,
-                         out, octets);
-      break;
+    case MxType::kF16: dequant_as<MxType::kF16>(m, W, stream); break;
+    case MxType::kBF16: dequant_as<MxType::kBF16>(m, W, stream); break;
+    case MxType::kF32: dequant_as<MxType::kF32>(m, W, stream); break;
   }
   return hipGetLastError();
 }

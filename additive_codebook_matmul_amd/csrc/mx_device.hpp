@@ -50,12 +50,13 @@ template <MxType T> struct Octet {
   uint32_t w[T == MxType::kF32 ? 8 : 4];
 };
 
-template <MxType T> __device__ __forceinline__ Octet<T> load_octet(const void *x, int64_t i) {
+// NT: without a place in the caches.
+template <MxType T, bool NT> __device__ __forceinline__ Octet<T> load_octet(const void *x, int64_t i) {
   Octet<T> o;
   const u32x4_t *p = static_cast<const u32x4_t *>(x) + i * (T == MxType::kF32 ? 2 : 1);
 #pragma unroll
   for (int k = 0; k < (T == MxType::kF32 ? 2 : 1); ++k) {
-    const u32x4_t v = p[k];
+    const u32x4_t v = NT ? __builtin_nontemporal_load(p + k) : p[k];
 #pragma unroll
     for (int e = 0; e < 4; ++e) o.w[4 * k + e] = v[e];
   }

@@ -302,6 +302,25 @@ def test_quantised_on_the_way_like_by_itself(batch, dtype, rule):
     assert bool(got.cpu()[~rows].isnan().all())
 
 
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rows", [4095, 8193, 32769])
+def test_large_matrices_convert_like_their_parts(rows, dtype):
+    """Matrices read and written past the caches (from 64 and 256 MiB on): every row's bits are
+    those of the row's own small matrix."""
+    cols = 4128
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(rows)
+    x = torch.randn((rows, cols), generator=gen, device=DEV).to(dtype)
+    for rule in ("floor", "ceil"):
+        codes, scales = mx_quantize(x, rule)
+        w = mx_dequant(codes, scales, dtype)
+        for at in range(0, rows, 1000):
+            part = mx_quantize(x[at:at + 1000].contiguous(), rule)
+            assert torch.equal(codes[at:at + 1000], part[0])
+            assert torch.equal(scales[at:at + 1000], part[1])
+            assert torch.equal(w[at:at + 1000], mx_dequant(*part, dtype))
+
+
 @pytest.mark.parametrize("dtype", HALVES)
 def test_arrays_past_32_bit_offsets(dtype):
     """Codes, activations and results above 4 GiB: the far end's results are those of the far end
