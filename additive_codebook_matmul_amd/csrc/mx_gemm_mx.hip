@@ -1,4 +1,4 @@
-// Product of two microscaled matrices for up to 16 rows of activations: y = x .
+// Product of two microscaled matrices for up to 32 rows of activations: y = x .
 // W^T on the block-scaled matrix instructions, which take E2M1 codes and E8M0
 // scales as they are. (Larger tiles, and more rows: mx_gemm_mx_tile.hip.)
 //
@@ -7,8 +7,8 @@
 // 128-input chunk and that block's scale byte, for A (rows of W) and B (rows
 // of x) alike, so both sides are loaded straight from their row-major arrays.
 // The wavefronts of a workgroup share K in groups of 512 inputs, four chunks
-// with 16 scale bytes of a row, and add their float32 sums through LDS in a
-// fixed order.
+// with 16 scale bytes of a row, for NT tiles of 16 rows of x, and add their
+// float32 sums through LDS in a fixed order.
 #include <algorithm>
 
 #include "mx_device.hpp"
@@ -23,12 +23,12 @@ __device__ __forceinline__ float4_t mfma_mx16(const uint4 &a, uint32_t sa, const
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-template <MxType T, int NW>
+template <MxType T, int NW, int NT>
 __global__ __launch_bounds__(NW * 64) void mx_mx_skinny_kernel(
     const uint8_t *__restrict__ wc, const uint8_t *__restrict__ wsc,
     const uint8_t *__restrict__ xc, const uint8_t *__restrict__ xsc, uint16_t *__restrict__ y,
     const int rows, const int cols, const int batch) {
-  __shared__ __attribute__((aligned(16))) float4_t red[NW * 64];
+  __shared__ __attribute__((aligned(16))) float4_t red[NT][NW * 64];
   const int row0 = (int)blockIdx.x * 16;
   const int nb = cols >> 5;
   const int lane = threadIdx.x & 63;
@@ -44,39 +44,53 @@ __global__ __launch_bounds__(NW * 64) void mx_mx_skinny_kernel(
   const Rsrc xrs = make_rsrc(xc, (uint32_t)batch * half);
   const Rsrc xss = make_rsrc(xsc, (uint32_t)batch * nb);
   const uint32_t srow = (uint32_t)min(r16, tile_rows - 1) * nb + base;
-  const uint32_t xrow = (uint32_t)min(r16, batch - 1) * nb;
 
-  float4_t acc = {0.f, 0.f, 0.f, 0.f};
+  float4_t acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = float4_t{0.f, 0.f, 0.f, 0.f};
   for (int gr = wave; 16 * gr < nb; gr += NW) {
-    uint4 w[4], x[4];
+    uint4 w[4], x[NT][4], sx[NT];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int blk = 16 * gr + 4 * c + q;
-      const uint32_t at = blk < nb ? (uint32_t)r16 * half + (uint32_t)blk * 16u : kMxOOB;
-      w[c] = buf_load16(crs, at);
-      x[c] = buf_load16(xrs, at);
+      w[c] = buf_load16(crs, blk < nb ? (uint32_t)r16 * half + (uint32_t)blk * 16u : kMxOOB);
     }
-    const uint4 sw = mx_scales16(srs, srow, 16 * gr, nb), sx = mx_scales16(xss, xrow, 16 * gr, nb);
-    const uint32_t swv[4] = {sw.x, sw.y, sw.z, sw.w}, sxv[4] = {sx.x, sx.y, sx.z, sx.w};
+    const uint4 sw = mx_scales16(srs, srow, 16 * gr, nb);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      acc = mfma_mx16(w[c], swv[c] >> (8 * q), x[c], sxv[c] >> (8 * q), acc);
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int blk = 16 * gr + 4 * c + q;
+        x[j][c] = buf_load16(xrs, blk < nb ? (uint32_t)(16 * j + r16) * half + (uint32_t)blk * 16u : kMxOOB);
+      }
+      sx[j] = mx_scales16(xss, (uint32_t)min(16 * j + r16, batch - 1) * nb, 16 * gr, nb);
+    }
+    const uint32_t swv[4] = {sw.x, sw.y, sw.z, sw.w};
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint32_t sxv[4] = {sx[j].x, sx[j].y, sx[j].z, sx[j].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        acc[j] = mfma_mx16(w[c], swv[c] >> (8 * q), x[j][c], sxv[c] >> (8 * q), acc[j]);
+    }
   }
 
-  red[threadIdx.x] = acc;
-  __syncthreads();
-  // lane (t, q) holds rows 4 q .. 4 q + 3 of token t
-  if (threadIdx.x < 64) {
-    float4_t v = red[lane];
 #pragma unroll
-    for (int u = 1; u < NW; ++u) v += red[u * 64 + lane];
-    if (r16 < batch) store4<T>(y + (int64_t)r16 * rows, row0 + 4 * q, rows, v, (rows & 3) == 0);
+  for (int j = 0; j < NT; ++j) red[j][threadIdx.x] = acc[j];
+  __syncthreads();
+  // lane (t, q) holds rows 4 q .. 4 q + 3 of token t; wavefront j adds up tile j
+  if (threadIdx.x < 64 * NT) {
+    float4_t v = red[wave][lane];
+#pragma unroll
+    for (int u = 1; u < NW; ++u) v += red[wave][u * 64 + lane];
+    const int tok = 16 * wave + r16;
+    if (tok < batch) store4<T>(y + (int64_t)tok * rows, row0 + 4 * q, rows, v, (rows & 3) == 0);
   }
 }
 
-template <MxType T, int NW>
+template <MxType T, int NW, int NT>
 hipError_t launch_skinny(const MxDesc &W, const MxDesc &x, void *y, hipStream_t stream) {
-  hipLaunchKernelGGL((mx_mx_skinny_kernel<T, NW>), dim3((unsigned)((W.rows + 15) / 16)), dim3(NW * 64), 0,
+  hipLaunchKernelGGL((mx_mx_skinny_kernel<T, NW, NT>), dim3((unsigned)((W.rows + 15) / 16)), dim3(NW * 64), 0,
                      stream, W.codes, W.scales, x.codes, x.scales, static_cast<uint16_t *>(y), (int)W.rows,
                      (int)W.cols, (int)x.rows);
   return hipGetLastError();
@@ -249,9 +263,10 @@ constexpr int kSkinnyWaves = 8;
 // and 0.022 ns a row of activations for 16 rows of W and a group of K, spread over
 // the chip, or, with few rows of W, 1 us and 0.05 us a row for each turn of its
 // wavefronts (fitted to 1024 x 8192 .. 28672 x 8192 from 2 to 16 rows: 4096 x 4096
-// at 5 3.8 us against 6.6, 28672 x 8192 at 16 36.5 against 27.8).
+// at 5 3.8 us against 6.6, at 32 5.8 against 7.2, 28672 x 8192 at 16 36.5 against
+// 27.8).
 bool tiles_pay(const MxDesc &W, int64_t batch) {
-  if (batch > 16) return true;
+  if (batch > 32) return true;
   const double groups = (double)((W.cols / 32 + 15) / 16), tiles = (double)((W.rows + 15) / 16);
   const double turns = (double)(int64_t)((groups + kSkinnyWaves - 1) / kSkinnyWaves);
   const double us = 2.7 + std::max(tiles * groups * (0.82e-3 + 0.022e-3 * (double)batch),
@@ -298,8 +313,11 @@ hipError_t launch_mx_gemm_mx(const MxDesc &W, const MxDesc &x, void *y, MxType t
     return type == MxType::kF16 ? rows_as<MxType::kF16, kGiven>(W, x.codes, x.scales, (int)x.rows, y, stream)
                                 : rows_as<MxType::kBF16, kGiven>(W, x.codes, x.scales, (int)x.rows, y, stream);
   if (tiles_pay(W, x.rows)) return launch_mx_gemm_mx_tile(W, x, y, type, ws, stream);
-  return type == MxType::kF16 ? launch_skinny<MxType::kF16, kSkinnyWaves>(W, x, y, stream)
-                              : launch_skinny<MxType::kBF16, kSkinnyWaves>(W, x, y, stream);
+  if (x.rows > 16)
+    return type == MxType::kF16 ? launch_skinny<MxType::kF16, kSkinnyWaves, 2>(W, x, y, stream)
+                                : launch_skinny<MxType::kBF16, kSkinnyWaves, 2>(W, x, y, stream);
+  return type == MxType::kF16 ? launch_skinny<MxType::kF16, kSkinnyWaves, 1>(W, x, y, stream)
+                              : launch_skinny<MxType::kBF16, kSkinnyWaves, 1>(W, x, y, stream);
 }
 
 }  // namespace aqlm
