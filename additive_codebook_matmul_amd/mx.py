@@ -64,8 +64,11 @@ def _lib() -> ctypes.CDLL:
     return _ready
 
 
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# torch's own quick forms of torch.cuda.current_device and current_stream, where
+# the installed torch has them
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(device: torch.device, fn, *args) -> None:
