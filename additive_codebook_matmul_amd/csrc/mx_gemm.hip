@@ -1,6 +1,6 @@
 // Product of half activations with microscaled weights: y = x . W^T, for the
 // batches of token generation. One or two rows of activations: mx_rows_kernel; up
-// to sixteen: mx_skinny_kernel; where its tiles are faster, and above: the tile
+// to 64: mx_skinny_kernel; where its tiles are faster, and above: the tile
 // kernels of mx_gemm_tile.hip.
 #include <algorithm>
 
@@ -21,7 +21,7 @@ struct Group {
   int n;
 };
 
-// Up to 16 rows of activations against tiles of 16 rows of W, K shared by the
+// Tiles of 16 rows of activations (up to four) and 16 rows of W, K shared by the
 // NW wavefronts of a workgroup in groups of 512 inputs (16 blocks, 256 bytes of
 // a row): lane (r, q) = (lane % 16, lane / 16) loads the 16 bytes that hold block
 // 4 c + q of the group for c = 0 .. 3, and the group's 16 scale bytes of row r,
@@ -31,17 +31,18 @@ struct Group {
 // (The sum over K does not care which inputs meet in one instruction, so no
 // code changes lanes.) Activations pass through LDS, which belongs to the
 // wavefront alone: in whole lines to it, spread over the banks from it, a group
-// of 512 inputs of up to 8 rows (H = 1) or half of it of up to 16 (H = 2) at a
-// time. The wavefronts' float32 sums meet in LDS in a fixed order.
+// of 512 inputs where there are up to 8 rows (H = 1), else half of it of 16 (H =
+// 2), at a time. The wavefronts' float32 sums meet in LDS in a fixed order.
 // What bounds it are requests, a 128-byte line each: scales byte by byte cost as
 // many as the codes, activations read by each lane for itself more (4 rows: 4096 x
 // 4096 5.7 us, 11008 x 4096 12.0), and codes loaded past the L1, which has the
 // line's second half ready, double (5.1 and 8.9; this 4.5 and 7.8).
 template <MxType T, int NW, int H>
-__global__ __launch_bounds__(NW * 64, H == 1 ? 6 : 5) void mx_skinny_kernel(const Group g, const int batch) {
+__global__ __launch_bounds__(NW * 64, H == 1 ? 6 : 5) void mx_skinny_kernel(const Group g, const int all_tokens) {
   constexpr int kLoads = 8;                     // of x into LDS, at most
   constexpr int kChunkBits = H == 1 ? 6 : 5;    // of 64 / H chunks of 16 bytes of a token
   extern __shared__ __attribute__((aligned(16))) uint8_t xs[];  // [NW][loads][1 KiB]
+  const int tok0 = 16 * (int)blockIdx.y, batch = min(16, all_tokens - tok0);
   const uint32_t mine = (threadIdx.x >> 6) * (uint32_t)((batch + H - 1) / H) * 1024u;  // the wavefront's
   int li = 0;
   while (li + 1 < g.n && (int)blockIdx.x >= g.first[li + 1]) ++li;
@@ -60,7 +61,7 @@ __global__ __launch_bounds__(NW * 64, H == 1 ? 6 : 5) void mx_skinny_kernel(cons
   const int base = (int)(((int64_t)row0 * nb) & 3);
   const Rsrc crs = make_rsrc(L.codes + (int64_t)row0 * half, (uint32_t)tile_rows * half);
   const Rsrc srs = make_rsrc(L.scales + (int64_t)row0 * nb - base, (uint32_t)tile_rows * nb + base);
-  const Rsrc xrs = make_rsrc(L.x, (uint32_t)batch * cols * 2u);
+  const Rsrc xrs = make_rsrc(L.x + (int64_t)tok0 * cols, (uint32_t)batch * cols * 2u);
   const uint32_t srow = (uint32_t)min(r16, tile_rows - 1) * nb + base;
 
   // Activations of blocks from..from + 16 / H - 1 into the wavefront's LDS: a load
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(NW * 64, H == 1 ? 6 : 5) void mx_skinny_kernel(cons
     float4_t v = red[lane];
 #pragma unroll
     for (int u = 1; u < NW; ++u) v += red[u * 64 + lane];
-    if (r16 < batch) store4<T>(L.y + (int64_t)r16 * rows, row0 + 4 * q, rows, v, (rows & 3) == 0);
+    if (r16 < batch) store4<T>(L.y + (int64_t)(tok0 + r16) * rows, row0 + 4 * q, rows, v, (rows & 3) == 0);
   }
 }
 
@@ -159,8 +160,8 @@ template <MxType T, int NW, int H> hipError_t launch_skinny(Group &g, int batch,
     blocks += (g.item[i].rows + 15) / 16;
   }
   g.first[g.n] = blocks;
-  hipLaunchKernelGGL((mx_skinny_kernel<T, NW, H>), dim3((unsigned)blocks), dim3(NW * 64),
-                     NW * 1024 * ((batch + H - 1) / H), stream, g, batch);
+  hipLaunchKernelGGL((mx_skinny_kernel<T, NW, H>), dim3((unsigned)blocks, (unsigned)(batch + 15) / 16), dim3(NW * 64),
+                     NW * 1024 * ((std::min(batch, 16) + H - 1) / H), stream, g, batch);
   return hipGetLastError();
 }
 
@@ -344,23 +345,25 @@ constexpr int kSkinnyWaves = 8;
 // From three rows on, where the tile kernel is the faster: the skinny one takes
 // 0.84 ns and 0.046 ns a row of activations for 16 rows of W and a group of K,
 // spread over the chip, or, with few rows of W, 1.15 us and 0.07 us a row for each
-// turn of its wavefronts (fitted to 1024 x 8192 .. 28672 x 8192 from 3 to 16 rows:
-// 4096 x 4096 at 8 rows 4.7 us against 9.6, 28672 x 8192 38 against 34).
+// turn of its wavefronts (fitted to 1024 x 8192 .. 28672 x 8192 from 3 to 64 rows:
+// 4096 x 4096 at 8 rows 4.7 us against 9.6, at 32 8.1 against 9.2, 1024 x 8192 at 64
+// 8.1 against 10.2, 28672 x 8192 at 8 38 against 34).
 // Whole-row wavefronts serve two rows of activations better than either (4096 x
 // 4096 3.9 us against 4.5, 11008 x 4096 7.9 against 10.8, 28672 x 8192 33 against
 // 34, 8192 x 28672 30 against 41), three about as well, four and more worse.
 // `split`: K may be split over workgroups.
 bool tiles_pay(const MxDesc &W, int64_t batch, bool split) {
-  if (batch > 16) return true;
+  if (batch > 64) return true;
   if (batch <= 2) return false;
   const double groups = (double)((W.cols / 32 + 15) / 16), tiles = (double)((W.rows + 15) / 16);
   const double turns = (double)(int64_t)((groups + kSkinnyWaves - 1) / kSkinnyWaves);
-  const double us = 2.7 + std::max(tiles * groups * (0.84e-3 + 0.046e-3 * (double)batch),
-                                   turns * (1.15 + 0.07 * (double)batch));
+  const double more = (double)((batch - 1) / 16);  // times that W is read again, from the caches
+  const double us = 2.7 + std::max(tiles * groups * (0.84e-3 * (1 + 0.5 * more) + 0.046e-3 * (double)batch),
+                                   turns * (1.15 + 0.07 * (double)std::min<int64_t>(batch, 16)));
   return mx_gemm_tile_us(W, batch, split) < us;
 }
 
-// Up to 16 rows of activations, without the tile kernel.
+// Without the tile kernel.
 template <MxType T> hipError_t few_as(Group &g, int batch, hipStream_t stream) {
   if (batch == 1) return rows_as<T, 1>(g, batch, stream);
   if (batch == 2) return rows_as<T, 2>(g, batch, stream);
