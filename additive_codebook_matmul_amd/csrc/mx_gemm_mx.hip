@@ -1,4 +1,4 @@
-// Product of two microscaled matrices for up to 32 rows of activations: y = x .
+// Product of two microscaled matrices for few rows of activations: y = x .
 // W^T on the block-scaled matrix instructions, which take E2M1 codes and E8M0
 // scales as they are. (Larger tiles, and more rows: mx_gemm_mx_tile.hip.)
 //
@@ -27,7 +27,8 @@ template <MxType T, int NW, int NT>
 __global__ __launch_bounds__(NW * 64) void mx_mx_skinny_kernel(
     const uint8_t *__restrict__ wc, const uint8_t *__restrict__ wsc,
     const uint8_t *__restrict__ xc, const uint8_t *__restrict__ xsc, uint16_t *__restrict__ y,
-    const int rows, const int cols, const int batch) {
+    const int rows, const int cols, const int all_tokens) {
+  const int tok0 = 16 * NT * (int)blockIdx.y, batch = min(16 * NT, all_tokens - tok0);
   __shared__ __attribute__((aligned(16))) float4_t red[NT][NW * 64];
   const int row0 = (int)blockIdx.x * 16;
   const int nb = cols >> 5;
@@ -41,8 +42,9 @@ __global__ __launch_bounds__(NW * 64) void mx_mx_skinny_kernel(
   const int base = (int)(((int64_t)row0 * nb) & 3);
   const Rsrc crs = make_rsrc(wc + (int64_t)row0 * half, (uint32_t)tile_rows * half);
   const Rsrc srs = make_rsrc(wsc + (int64_t)row0 * nb - base, (uint32_t)tile_rows * nb + base);
-  const Rsrc xrs = make_rsrc(xc, (uint32_t)batch * half);
-  const Rsrc xss = make_rsrc(xsc, (uint32_t)batch * nb);
+  const int xbase = (int)(((int64_t)tok0 * nb) & 3);
+  const Rsrc xrs = make_rsrc(xc + (int64_t)tok0 * half, (uint32_t)batch * half);
+  const Rsrc xss = make_rsrc(xsc + (int64_t)tok0 * nb - xbase, (uint32_t)batch * nb + xbase);
   const uint32_t srow = (uint32_t)min(r16, tile_rows - 1) * nb + base;
 
   float4_t acc[NT];
@@ -63,7 +65,7 @@ __global__ __launch_bounds__(NW * 64) void mx_mx_skinny_kernel(
         const int blk = 16 * gr + 4 * c + q;
         x[j][c] = buf_load16(xrs, blk < nb ? (uint32_t)(16 * j + r16) * half + (uint32_t)blk * 16u : kMxOOB);
       }
-      sx[j] = mx_scales16(xss, (uint32_t)min(16 * j + r16, batch - 1) * nb, 16 * gr, nb);
+      sx[j] = mx_scales16(xss, (uint32_t)min(16 * j + r16, batch - 1) * nb + xbase, 16 * gr, nb);
     }
     const uint32_t swv[4] = {sw.x, sw.y, sw.z, sw.w};
 #pragma unroll
@@ -84,15 +86,15 @@ __global__ __launch_bounds__(NW * 64) void mx_mx_skinny_kernel(
 #pragma unroll
     for (int u = 1; u < NW; ++u) v += red[wave][u * 64 + lane];
     const int tok = 16 * wave + r16;
-    if (tok < batch) store4<T>(y + (int64_t)tok * rows, row0 + 4 * q, rows, v, (rows & 3) == 0);
+    if (tok < batch) store4<T>(y + (int64_t)(tok0 + tok) * rows, row0 + 4 * q, rows, v, (rows & 3) == 0);
   }
 }
 
 template <MxType T, int NW, int NT>
 hipError_t launch_skinny(const MxDesc &W, const MxDesc &x, void *y, hipStream_t stream) {
-  hipLaunchKernelGGL((mx_mx_skinny_kernel<T, NW, NT>), dim3((unsigned)((W.rows + 15) / 16)), dim3(NW * 64), 0,
-                     stream, W.codes, W.scales, x.codes, x.scales, static_cast<uint16_t *>(y), (int)W.rows,
-                     (int)W.cols, (int)x.rows);
+  const dim3 grid((unsigned)((W.rows + 15) / 16), (unsigned)((x.rows + 16 * NT - 1) / (16 * NT)));
+  hipLaunchKernelGGL((mx_mx_skinny_kernel<T, NW, NT>), grid, dim3(NW * 64), 0, stream, W.codes, W.scales,
+                     x.codes, x.scales, static_cast<uint16_t *>(y), (int)W.rows, (int)W.cols, (int)x.rows);
   return hipGetLastError();
 }
 
@@ -262,15 +264,17 @@ constexpr int kSkinnyWaves = 8;
 // Of the others, where the tile kernel is the faster: the skinny one takes 0.82 ns
 // and 0.022 ns a row of activations for 16 rows of W and a group of K, spread over
 // the chip, or, with few rows of W, 1 us and 0.05 us a row for each turn of its
-// wavefronts (fitted to 1024 x 8192 .. 28672 x 8192 from 2 to 16 rows: 4096 x 4096
-// at 5 3.8 us against 6.6, at 32 5.8 against 7.2, 28672 x 8192 at 16 36.5 against
-// 27.8).
+// wavefronts (fitted to 1024 x 8192 .. 28672 x 8192 from 2 to 128 rows: 4096 x 4096
+// at 5 3.8 us against 6.6, at 32 5.8 against 7.2, 1024 x 4096 at 64 5.5 against 6.7,
+// 28672 x 8192 at 16 36.5 against 27.8).
 bool tiles_pay(const MxDesc &W, int64_t batch) {
-  if (batch > 32) return true;
+  if (batch > 128) return true;
   const double groups = (double)((W.cols / 32 + 15) / 16), tiles = (double)((W.rows + 15) / 16);
   const double turns = (double)(int64_t)((groups + kSkinnyWaves - 1) / kSkinnyWaves);
-  const double us = 2.7 + std::max(tiles * groups * (0.82e-3 + 0.022e-3 * (double)batch),
-                                   turns * (1.0 + 0.05 * (double)batch));
+  const double more = (double)((batch - 1) / 32);  // times that W is read again, from the caches
+  const double us = 2.7 + 0.5 * more +
+                    std::max(tiles * groups * (0.82e-3 * (1 + 0.5 * more) + 0.022e-3 * (double)batch),
+                             turns * (1.0 + 0.05 * (double)std::min<int64_t>(batch, 32)));
   return mx_gemm_mx_tile_us(W, batch) < us;
 }
 
