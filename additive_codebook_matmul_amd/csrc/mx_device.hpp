@@ -142,8 +142,10 @@ __device__ __forceinline__ u16x2_t mx_above_f16(const uint4 &s) {
 }
 
 // Eight float16 activations as the exact sum hi + lo of two bfloat16 vectors
-// (11 significant bits: hi takes the nearest 8, what is left has 3 or fewer
-// and a magnitude bfloat16 holds). Infinities and NaN stay in hi alone.
+// (11 significant bits: hi takes the first 8, what is left has 3 or fewer and a
+// magnitude bfloat16 holds). hi is cut off, not rounded, so that lo has its sign and
+// a product with hi overflows only where the whole does, to the same infinity.
+// Infinities and NaN stay in hi alone.
 __device__ __forceinline__ void split_f16(const uint4 &x, uint4 &hi, uint4 &lo) {
   const uint32_t in[4] = {x.x, x.y, x.z, x.w};
   uint32_t h[4], l[4];
@@ -153,18 +155,31 @@ __device__ __forceinline__ void split_f16(const uint4 &x, uint4 &hi, uint4 &lo) 
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float v = h2f(e ? in[i] >> 16 : in[i] & 0xFFFFu);
-      const __bf16 a = static_cast<__bf16>(v);
-      const float rest = v - static_cast<float>(a);
+      hw[e] = __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u;
       const bool finite = __builtin_fabsf(v) < __builtin_inff();
-      const __bf16 b = static_cast<__bf16>(finite ? rest : 0.0f);
-      hw[e] = __builtin_bit_cast(uint16_t, a);
-      lw[e] = __builtin_bit_cast(uint16_t, b);
+      lw[e] = __builtin_bit_cast(uint32_t, finite ? v - __builtin_bit_cast(float, hw[e]) : 0.0f);
     }
-    h[i] = hw[0] | (hw[1] << 16);
-    l[i] = lw[0] | (lw[1] << 16);
+    h[i] = (hw[0] >> 16) | hw[1];
+    l[i] = (lw[0] >> 16) | (lw[1] & 0xFFFF0000u);
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Eight bfloat16 weights for the product with lo: an infinity (scale bytes 253 and
+// 254) becomes the largest number, since lo is zero for most values and infinity
+// times zero would be NaN. The product with hi, whose sign lo has, gives the
+// infinity, or the NaN where x is zero. (NaN becomes a number too: hi's product has it.)
+__device__ __forceinline__ uint4 finite_bf16(const uint4 &w) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const u16x2_t top = {0x7F7F, 0x7F7F};
+    const u16x2_t m = __builtin_elementwise_min(__builtin_bit_cast(u16x2_t, in[i] & 0x7FFF7FFFu), top);
+    r[i] = (in[i] & 0x80008000u) | __builtin_bit_cast(uint32_t, m);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // Scale bytes of 16 consecutive blocks of a row, from block `blk` on: `at` is

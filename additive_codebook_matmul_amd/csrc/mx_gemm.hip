@@ -119,7 +119,7 @@ __global__ __launch_bounds__(NW * 64, H == 1 ? 6 : 5) void mx_skinny_kernel(cons
         split_f16(x_of(c % (4 / H), s), hi, lo);
         const uint4 a = mx_decode8<MxType::kBF16>(s == 0 ? ww[0] : s == 1 ? ww[1] : s == 2 ? ww[2] : ww[3], sv);
         acc = mx_mfma16<MxType::kBF16>(a, hi, acc);
-        acc = mx_mfma16<MxType::kBF16>(a, lo, acc);
+        acc = mx_mfma16<MxType::kBF16>(finite_bf16(a), lo, acc);
       }
     };
 #pragma unroll
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(const Group g, con
             } else {
               const uint4 a = mx_decode8<MxType::kBF16>(w, mx_scale(sv[r]));
               acc[r][b] = mx_mfma16<MxType::kBF16>(a, hi, acc[r][b]);
-              acc[r][b] = mx_mfma16<MxType::kBF16>(a, lo, acc[r][b]);
+              acc[r][b] = mx_mfma16<MxType::kBF16>(finite_bf16(a), lo, acc[r][b]);
             }
           }
         }

@@ -178,7 +178,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_tile_kernel(const
             const uint32_t ww[4] = {w[U & 1][i].x, w[U & 1][i].y, w[U & 1][i].z, w[U & 1][i].w};
             const uint4 av = mx_decode8<MxType::kBF16>(ww[s], sv[i]);
             acc[i][j] = mx_mfma32<MxType::kBF16>(av, hi, acc[i][j]);
-            acc[i][j] = mx_mfma32<MxType::kBF16>(av, lo, acc[i][j]);
+            acc[i][j] = mx_mfma32<MxType::kBF16>(finite_bf16(av), lo, acc[i][j]);
           }
         }
     }

@@ -198,7 +198,7 @@ __global__ __launch_bounds__(64 * kRowWaves * TW * KW) void mx_grad_tile_kernel(
             uint4 hi, lo;
             split_f16(b[s & 1][j], hi, lo);
             acc[i][j] = mx_mfma32<MxType::kBF16>(wv[s & 1][i], hi, acc[i][j]);
-            acc[i][j] = mx_mfma32<MxType::kBF16>(wv[s & 1][i], lo, acc[i][j]);
+            acc[i][j] = mx_mfma32<MxType::kBF16>(finite_bf16(wv[s & 1][i]), lo, acc[i][j]);
           } else {
             acc[i][j] = mx_mfma32<T>(wv[s & 1][i], b[s & 1][j], acc[i][j]);
           }
