@@ -21,9 +21,11 @@
  * Products accumulate in float32 in a fixed order and round once, to nearest
  * even, to the type of the result. A weight enters a product as the value
  * above, exactly, whatever its scale (with float16 activations too, whose
- * type cannot hold every such value); only magnitudes from 2^128 on (scale
- * bytes 253 and 254, which aqlm_mx_quantize writes by its CEIL rule alone, for
- * blocks that reach above 6 * 2^125) become infinities.
+ * type cannot hold every such value). In the products with half activations
+ * and in the gradient magnitudes from 2^128 on are infinities (scale bytes 253
+ * and 254; aqlm_mx_quantize writes 253 by its CEIL rule alone, for blocks that
+ * reach above 6 * 2^125, and 254 never); where both sides are microscaled they
+ * keep their value, and only a sum can overflow.
  * NaN and infinities propagate as in a dense product, also from activations.
  *
  * Pointers, streams and errors as in aqlm.h: every pointer is a device pointer
