@@ -24,7 +24,7 @@ STATUS_NAMES = {0: "AQLM_OK", 1: "AQLM_ERR_NULL", 2: "AQLM_ERR_SHAPE", 3: "AQLM_
 EXPORTED_SYMBOLS = ("aqlm_dequant", "aqlm_gemv", "aqlm_gemv_batched", "aqlm_gemv_workspace_size",
                     "aqlm_gemv_ws", "aqlm_gemm", "aqlm_gemm_workspace_size", "aqlm_gemm_ws",
                     "aqlm_gemm_noalloc", "aqlm_status_string", "aqlm_abi_version")
-ABI_VERSION = 5
+ABI_VERSION = 6
 # bytes of the library's static scratch array (AQLM_STATIC_SCRATCH_BYTES)
 STATIC_SCRATCH_BYTES = 64 << 20
 AQLM_CODES_PACKED = 1
@@ -69,6 +69,11 @@ def load_library() -> ctypes.CDLL:
             f"HIP library not found at {LIB_PATH}; build it with "
             "`python -m additive_codebook_matmul_amd.build` (hipcc, gfx950)")
     lib = ctypes.CDLL(LIB_PATH)
+    # before any other symbol, which an older build may lack
+    lib.aqlm_abi_version.argtypes = []
+    lib.aqlm_abi_version.restype = ctypes.c_int
+    if lib.aqlm_abi_version() != ABI_VERSION:
+        raise RuntimeError("libaqlm_mi355x.so ABI version mismatch; rebuild the library")
     lp = ctypes.POINTER(AqlmLayerStruct)
     lib.aqlm_dequant.argtypes = [lp, ctypes.c_void_p, ctypes.c_void_p]
     lib.aqlm_dequant.restype = ctypes.c_int
@@ -94,10 +99,6 @@ def load_library() -> ctypes.CDLL:
     lib.aqlm_gemv_ws.restype = ctypes.c_int
     lib.aqlm_status_string.argtypes = [ctypes.c_int]
     lib.aqlm_status_string.restype = ctypes.c_char_p
-    lib.aqlm_abi_version.argtypes = []
-    lib.aqlm_abi_version.restype = ctypes.c_int
-    if lib.aqlm_abi_version() != ABI_VERSION:
-        raise RuntimeError("libaqlm_mi355x.so ABI version mismatch; rebuild the library")
     _lib = lib
     return lib
 
