@@ -10,6 +10,10 @@ fallback: a missing library or a failing call raises.
     y = layer.forward(x)                        # x: [batch, in] float16 or bfloat16
     y = layer.forward_mx(x)                     # activations microscaled too
     dx = layer.grad_input(dy)                   # gradient through the frozen weights
+
+Under autograd an x that requires a gradient gets it: forward, forward_mx, gemm,
+gemv and mx_gemv_batched are recorded with grad_input as their backward
+(forward_mx: straight through the quantisation). The weights are constants.
 """
 from __future__ import annotations
 
@@ -18,6 +22,7 @@ import struct
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._lib import _check, load_library
 
@@ -147,6 +152,37 @@ def mx_dequant(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = t
     return W
 
 
+class _Recorded(torch.autograd.Function):
+    """Products of layers with one x each, and for backward each layer's grad_input."""
+
+    @staticmethod
+    def forward(ctx, products, layers, *xs):
+        ctx.layers = layers
+        ctx.set_materialize_grads(False)
+        return tuple(products(xs))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *dys):
+        grads = []
+        for layer, dy, wanted in zip(ctx.layers, dys, ctx.needs_input_grad[2:]):
+            if dy is None or not wanted:
+                grads.append(None)
+                continue
+            dy = dy.contiguous()
+            if dy.data_ptr() % 16:  # a part of a larger gradient
+                dy = dy.clone()
+            grads.append(layer.grad_input(dy))
+        return (None, None, *grads)
+
+
+def _record(products, layers, xs, outs):
+    """products(xs), called again inside of the recording, as results of autograd's."""
+    if outs is not None:
+        raise ValueError("out takes no part in autograd: x must not require a gradient")
+    return _Recorded.apply(products, layers, *xs)
+
+
 class MxLayer:
     """A linear layer [out, in] whose weights are a microscaled matrix.
 
@@ -208,6 +244,8 @@ class MxLayer:
         """y = x . W^T for any number of activation rows; a workspace, where the
         call needs one, comes from torch's allocator on the current stream."""
         self._check_half(x, "x", self.in_features)
+        if x.requires_grad and torch.is_grad_enabled():
+            return _record(lambda xs: [self.gemm(xs[0])], (self,), (x,), out)[0]
         batch = x.shape[0]
         y = _output(out, (batch, self.out_features), x.dtype, self.device)
         ws, ptr, need = self._workspace(batch, "gemm")
@@ -243,6 +281,8 @@ class MxLayer:
         self._check_half(x, "x", self.in_features)
         if rule not in MX_RULES:
             raise ValueError(f"rule must be one of {sorted(MX_RULES)}")
+        if x.requires_grad and torch.is_grad_enabled():
+            return _record(lambda xs: [self.forward_mx(xs[0], rule)], (self,), (x,), out)[0]
         batch = x.shape[0]
         y = _output(out, (batch, self.out_features), x.dtype, self.device)
         ws, ptr, need = self._workspace(batch, "gemm_quant")
@@ -252,7 +292,7 @@ class MxLayer:
 
     def grad_input(self, dy: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """dx = dy . W: the gradient of forward(x) with respect to x, and the
-        straight-through one of forward_mx(x)."""
+        straight-through one of forward_mx(x). Not recorded by autograd itself."""
         self._check_half(dy, "dy", self.out_features)
         batch = dy.shape[0]
         dx = _output(out, (batch, self.in_features), dy.dtype, self.device)
@@ -277,14 +317,19 @@ def mx_gemv_batched(layers, xs, outs=None):
     device = layers[0].device
     layers[0]._check_half(xs[0], "x", layers[0].in_features)
     batch, dtype = xs[0].shape[0], xs[0].dtype
-    seen, seen_cols = xs[0], layers[0].in_features
+    seen, seen_cols, record = xs[0], layers[0].in_features, xs[0].requires_grad
     for L, x in zip(layers, xs):
         if x is seen and L.in_features == seen_cols and L.device == device:
             continue  # the x of the layer before, as with query, key and value
         L._check_half(x, "x", L.in_features)
         if x.shape[0] != batch or x.dtype != dtype or L.device != device:
             raise ValueError("all layers share the batch size, the type and the device")
-        seen, seen_cols = x, L.in_features
+        seen, seen_cols, record = x, L.in_features, record or x.requires_grad
+    if record and torch.is_grad_enabled():
+        def products(given):  # (not parts of one allocation, which could not be changed in place)
+            return mx_gemv_batched(layers, given, [
+                torch.empty((batch, L.out_features), dtype=dtype, device=device) for L in layers])
+        return list(_record(products, tuple(layers), xs, outs))
     sizes = [L.out_features for L in layers]
     if outs is not None:
         ys = [_output(o, (batch, k), dtype, device) for o, k in zip(outs, sizes)]
