@@ -58,11 +58,10 @@ __global__ __launch_bounds__(NW * 64, H == 1 ? 6 : 5) void mx_skinny_kernel(cons
   // resources that end with the tile's last row: rows past it read zero (their
   // scales are those of the last one, and not stored results theirs)
   const int tile_rows = __builtin_amdgcn_readfirstlane(min(16, rows - row0));
-  const int base = (int)(((int64_t)row0 * nb) & 3);
   const Rsrc crs = make_rsrc(L.codes + (int64_t)row0 * half, (uint32_t)tile_rows * half);
-  const Rsrc srs = make_rsrc(L.scales + (int64_t)row0 * nb - base, (uint32_t)tile_rows * nb + base);
+  const Rsrc srs = make_rsrc(L.scales + (int64_t)row0 * nb, (uint32_t)tile_rows * nb);
   const Rsrc xrs = make_rsrc(L.x + (int64_t)tok0 * cols, (uint32_t)batch * cols * 2u);
-  const uint32_t srow = (uint32_t)min(r16, tile_rows - 1) * nb + base;
+  const uint32_t srow = (uint32_t)min(r16, tile_rows - 1) * nb;
 
   // Activations of blocks from..from + 16 / H - 1 into the wavefront's LDS: a load
   // takes 1 KiB, a token (two with H = 2), in whole lines. Chunk j of token t lies

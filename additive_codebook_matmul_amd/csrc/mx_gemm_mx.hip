@@ -39,13 +39,11 @@ __global__ __launch_bounds__(NW * 64) void mx_mx_skinny_kernel(
   // scales are those of the last one)
   const int tile_rows = __builtin_amdgcn_readfirstlane(min(16, rows - row0));
   const uint32_t half = (uint32_t)cols >> 1;
-  const int base = (int)(((int64_t)row0 * nb) & 3);
   const Rsrc crs = make_rsrc(wc + (int64_t)row0 * half, (uint32_t)tile_rows * half);
-  const Rsrc srs = make_rsrc(wsc + (int64_t)row0 * nb - base, (uint32_t)tile_rows * nb + base);
-  const int xbase = (int)(((int64_t)tok0 * nb) & 3);
+  const Rsrc srs = make_rsrc(wsc + (int64_t)row0 * nb, (uint32_t)tile_rows * nb);
   const Rsrc xrs = make_rsrc(xc + (int64_t)tok0 * half, (uint32_t)batch * half);
-  const Rsrc xss = make_rsrc(xsc + (int64_t)tok0 * nb - xbase, (uint32_t)batch * nb + xbase);
-  const uint32_t srow = (uint32_t)min(r16, tile_rows - 1) * nb + base;
+  const Rsrc xss = make_rsrc(xsc + (int64_t)tok0 * nb, (uint32_t)batch * nb);
+  const uint32_t srow = (uint32_t)min(r16, tile_rows - 1) * nb;
 
   float4_t acc[NT];
 #pragma unroll
@@ -65,7 +63,7 @@ __global__ __launch_bounds__(NW * 64) void mx_mx_skinny_kernel(
         const int blk = 16 * gr + 4 * c + q;
         x[j][c] = buf_load16(xrs, blk < nb ? (uint32_t)(16 * j + r16) * half + (uint32_t)blk * 16u : kMxOOB);
       }
-      sx[j] = mx_scales16(xss, (uint32_t)min(16 * j + r16, batch - 1) * nb + xbase, 16 * gr, nb);
+      sx[j] = mx_scales16(xss, (uint32_t)min(16 * j + r16, batch - 1) * nb, 16 * gr, nb);
     }
     const uint32_t swv[4] = {sw.x, sw.y, sw.z, sw.w};
 #pragma unroll

@@ -57,17 +57,17 @@ template <int ROWS, int THREADS, int GROUPS> struct ScaleStage {
   static constexpr int kAll = ROWS * GROUPS, kChunks = (kAll + THREADS - 1) / THREADS;
   static constexpr int kBytes = kAll * 16;
   Rsrc rs;
-  int nb, base, rows, blk;  // blocks of a row; first byte within its word; rows there are
+  int nb, rows, blk;  // blocks of a row; rows there are
   uint4 v[kChunks];
   uint32_t extra[kChunks];
 
+  // (row0, a tile's first, is a multiple of 32: its scales begin with a whole word)
   __device__ __forceinline__ ScaleStage(const uint8_t *scales, int64_t row0, int rows_, int nb_)
       : nb(nb_), rows(rows_), blk(0) {
-    base = (int)((row0 * nb) & 3);
-    rs = make_rsrc(scales + row0 * nb - base, (uint32_t)rows * nb + base);
+    rs = make_rsrc(scales + row0 * nb, (uint32_t)rows * nb);
   }
   __device__ __forceinline__ uint32_t at(int id) const {  // of chunk id's first byte
-    return (uint32_t)min(id / GROUPS, rows - 1) * nb + base + (uint32_t)(blk + 16 * (id % GROUPS));
+    return (uint32_t)min(id / GROUPS, rows - 1) * nb + (uint32_t)(blk + 16 * (id % GROUPS));
   }
   static __device__ __forceinline__ uint32_t place(int r, int g) {
     return (uint32_t)r * (16 * GROUPS) + (uint32_t)((g ^ ((r * GROUPS >> 4) & (GROUPS - 1))) << 4);
@@ -96,7 +96,7 @@ template <int ROWS, int THREADS, int GROUPS> struct ScaleStage {
         uint32_t d[5] = {w[0], w[1], w[2], w[3], extra[i]};
         // A word that ends past the array reads zero; its bytes that exist are
         // read one by one (the last row's end alone).
-        const uint32_t end = (uint32_t)rows * nb + base, word = end & ~3u, to = from & ~3u;
+        const uint32_t end = (uint32_t)rows * nb, word = end & ~3u, to = from & ~3u;
         if (word != end && left > 0 && to + 20 > word) {
           uint32_t tail = buf_load_u8(rs, word);
           if ((end & 3u) > 1) tail |= buf_load_u8(rs, word + 1) << 8;
