@@ -24,7 +24,7 @@ STATUS_NAMES = {0: "AQLM_OK", 1: "AQLM_ERR_NULL", 2: "AQLM_ERR_SHAPE", 3: "AQLM_
 EXPORTED_SYMBOLS = ("aqlm_dequant", "aqlm_gemv", "aqlm_gemv_batched", "aqlm_gemv_workspace_size",
                     "aqlm_gemv_ws", "aqlm_gemm", "aqlm_gemm_workspace_size", "aqlm_gemm_ws",
                     "aqlm_gemm_noalloc", "aqlm_status_string", "aqlm_abi_version")
-ABI_VERSION = 6
+ABI_VERSION = 7
 # bytes of the library's static scratch array (AQLM_STATIC_SCRATCH_BYTES)
 STATIC_SCRATCH_BYTES = 64 << 20
 AQLM_CODES_PACKED = 1

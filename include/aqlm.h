@@ -69,7 +69,7 @@
 extern "C" {
 #endif
 
-#define AQLM_ABI_VERSION 6
+#define AQLM_ABI_VERSION 7
 
 /* aqlm_layer.flags: codes are bit-packed (see the format above). */
 #define AQLM_CODES_PACKED 1

@@ -8,3 +8,4 @@ from .aqlm_oracle import (  # noqa: F401
 )
 from . import encoder_oracle  # noqa: F401
 from . import mx_oracle  # noqa: F401
+from . import i8_oracle  # noqa: F401
