@@ -10,64 +10,151 @@
 namespace aqlm {
 namespace {
 
+// A row by WAVES wavefronts, ROUNDS octets a thread in registers; 256 / (64 WAVES)
+// rows a workgroup (one from four wavefronts on).
+template <MxType T, int WAVES, int ROUNDS, bool NT>
+__global__ __launch_bounds__(WAVES < 4 ? 256 : WAVES * 64) void i8_quantize_rows_kernel(
+    const void *__restrict__ x, uint2 *__restrict__ codes, float *__restrict__ scales, int octets, int64_t rows) {
+  constexpr int kThreads = WAVES * 64, kPer = WAVES < 4 ? 4 / WAVES : 1;
+  __shared__ uint32_t tops[WAVES > 1 ? WAVES : 1];
+  static_assert(WAVES == 1 || WAVES >= 4, "tops are one row's");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tid = WAVES == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+  for (int64_t row = (int64_t)blockIdx.x * kPer + (WAVES == 1 ? wave : 0); row < rows; row += (int64_t)gridDim.x * kPer) {
+    const int64_t base = row * octets;
+    Octet<T> o[ROUNDS];
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < ROUNDS; ++u) {
+      const int i = tid + u * kThreads;
+      if (i < octets) o[u] = load_octet<T, NT>(x, base + i);
+      else o[u] = {};
+    }
+#pragma unroll
+    for (int u = 0; u < ROUNDS; ++u) m = max(m, octet_max<T>(o[u]));
+    m = wave_max(m);
+    if constexpr (WAVES > 1) {
+      __syncthreads();  // the row before is done with `tops`
+      if ((threadIdx.x & 63) == 0) tops[wave] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) m = max(m, tops[w]);
+    }
+    const RowScale r = row_scale(max_bits<T>(m));
+    if (tid == 0) scales[row] = r.scale;
+#pragma unroll
+    for (int u = 0; u < ROUNDS; ++u) {
+      const int i = tid + u * kThreads;
+      if (i < octets) codes[base + i] = encode_octet<T>(o[u], r);
+    }
+  }
+}
+
+// Rows longer than that: read twice.
 template <MxType T>
-__global__ __launch_bounds__(256) void i8_quantize_kernel(const void *__restrict__ x, uint2 *__restrict__ codes,
-                                                          float *__restrict__ scales, int octets, int64_t rows) {
-  __shared__ uint32_t tops[4];
+__global__ __launch_bounds__(1024) void i8_quantize_long_kernel(const void *__restrict__ x, uint2 *__restrict__ codes,
+                                                                float *__restrict__ scales, int octets, int64_t rows) {
+  __shared__ uint32_t tops[16];
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const int64_t base = row * octets;
     uint32_t m = 0;
-    for (int i = threadIdx.x; i < octets; i += 256) m = max(m, octet_max<T>(load_octet<T, false>(x, base + i)));
+    for (int i = threadIdx.x; i < octets; i += 1024) m = max(m, octet_max<T>(load_octet<T, false>(x, base + i)));
     m = wave_max(m);
     if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = m;
     __syncthreads();
-    m = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+#pragma unroll
+    for (int w = 0; w < 16; ++w) m = max(m, tops[w]);
     const RowScale r = row_scale(max_bits<T>(m));
     if (threadIdx.x == 0) scales[row] = r.scale;
-    for (int i = threadIdx.x; i < octets; i += 256)
+    for (int i = threadIdx.x; i < octets; i += 1024)
       codes[base + i] = encode_octet<T>(load_octet<T, false>(x, base + i), r);
     __syncthreads();
   }
 }
 
-// In pieces of 16 bytes of W, eight halves or four floats, a thread each.
-template <MxType T>
+// In pieces of 16 bytes of W, eight halves or four floats, a thread each, a row's
+// pieces over grid.x: a store of a wavefront is 1 KiB in one run.
+template <MxType T, bool NT>
 __global__ __launch_bounds__(256) void i8_dequant_kernel(const int8_t *__restrict__ codes,
                                                          const float *__restrict__ scales, u32x4_t *__restrict__ W,
                                                          int row_pieces, int64_t rows) {
-  constexpr int kPer = T == MxType::kF32 ? 4 : 8;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+  constexpr int kPer = T == MxType::kF32 ? 4 : 8, kUnroll = 4;
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
     const float s = scales[row];
     const int64_t base = row * row_pieces;
-    for (int i = threadIdx.x; i < row_pieces; i += 256) {
-      const uint32_t *p = reinterpret_cast<const uint32_t *>(codes + (base + i) * kPer);
-      float v[kPer];
+    for (int i0 = (int)blockIdx.x * (256 * kUnroll) + threadIdx.x; i0 < row_pieces; i0 += (int)gridDim.x * (256 * kUnroll)) {
+      uint32_t c[kUnroll][kPer / 4];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) v[e] = (float)(int8_t)(p[e >> 2] >> (8 * (e & 3))) * s;
-      u32x4_t r;
-      if constexpr (T == MxType::kF32) {
+      for (int k = 0; k < kUnroll; ++k) {
+        const int i = i0 + 256 * k;
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(codes + (base + i) * kPer);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = __builtin_bit_cast(uint32_t, v[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = f2t<T>(materialize(v[2 * e])) | (f2t<T>(materialize(v[2 * e + 1])) << 16);
+        for (int e = 0; e < kPer / 4; ++e) c[k][e] = i < row_pieces ? p[e] : 0u;
       }
-      W[base + i] = r;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int i = i0 + 256 * k;
+        if (i >= row_pieces) break;
+        float v[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v[e] = (float)(int8_t)(c[k][e >> 2] >> (8 * (e & 3))) * s;
+        u32x4_t r;
+        if constexpr (T == MxType::kF32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[e] = __builtin_bit_cast(uint32_t, v[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[e] = f2t<T>(materialize(v[2 * e])) | (f2t<T>(materialize(v[2 * e + 1])) << 16);
+        }
+        if constexpr (NT) __builtin_nontemporal_store(r, W + base + i);
+        else W[base + i] = r;
+      }
     }
   }
 }
 
 unsigned row_grid(int64_t rows) { return (unsigned)std::min<int64_t>(rows, int64_t(1) << 20); }
 
+// From these sizes on a half matrix is read, or a matrix written, without a place in
+// the caches (as the MXFP4 conversions).
+constexpr int64_t kNtLoad = (int64_t)64 << 20, kNtStore = (int64_t)256 << 20;
+
+template <MxType T, int WAVES, int ROUNDS>
+void quantize_rows(const void *x, int64_t rows, int64_t cols, int8_t *codes, float *scales, hipStream_t stream) {
+  constexpr int kPer = WAVES < 4 ? 4 / WAVES : 1;
+  const dim3 grid(row_grid((rows + kPer - 1) / kPer)), block(WAVES < 4 ? 256 : WAVES * 64);
+  uint2 *const c = reinterpret_cast<uint2 *>(codes);
+  const int octets = (int)(cols / 8);
+  if (T != MxType::kF32 && rows * cols * 2 >= kNtLoad)
+    hipLaunchKernelGGL((i8_quantize_rows_kernel<T, WAVES, ROUNDS, true>), grid, block, 0, stream, x, c, scales, octets, rows);
+  else
+    hipLaunchKernelGGL((i8_quantize_rows_kernel<T, WAVES, ROUNDS, false>), grid, block, 0, stream, x, c, scales, octets, rows);
+}
+
+// Wavefronts and octets a thread by the row's length.
 template <MxType T>
 void quantize_as(const void *x, int64_t rows, int64_t cols, int8_t *codes, float *scales, hipStream_t stream) {
-  hipLaunchKernelGGL((i8_quantize_kernel<T>), dim3(row_grid(rows)), dim3(256), 0, stream, x,
-                     reinterpret_cast<uint2 *>(codes), scales, (int)(cols / 8), rows);
+  const int64_t octets = cols / 8;
+  if (octets <= 64) quantize_rows<T, 1, 1>(x, rows, cols, codes, scales, stream);
+  else if (octets <= 128) quantize_rows<T, 1, 2>(x, rows, cols, codes, scales, stream);
+  else if (octets <= 256) quantize_rows<T, 4, 1>(x, rows, cols, codes, scales, stream);
+  else if (octets <= 512) quantize_rows<T, 4, 2>(x, rows, cols, codes, scales, stream);
+  else if (octets <= 1024) quantize_rows<T, 4, 4>(x, rows, cols, codes, scales, stream);
+  else if (octets <= 2048) quantize_rows<T, 8, 4>(x, rows, cols, codes, scales, stream);
+  else if (octets <= 4096) quantize_rows<T, 16, 4>(x, rows, cols, codes, scales, stream);
+  else
+    hipLaunchKernelGGL((i8_quantize_long_kernel<T>), dim3(row_grid(rows)), dim3(1024), 0, stream, x,
+                       reinterpret_cast<uint2 *>(codes), scales, (int)octets, rows);
 }
 
 template <MxType T> void dequant_as(const I8Desc &m, void *W, hipStream_t stream) {
-  hipLaunchKernelGGL((i8_dequant_kernel<T>), dim3(row_grid(m.rows)), dim3(256), 0, stream, m.codes, m.scales,
-                     static_cast<u32x4_t *>(W), (int)(m.cols / (T == MxType::kF32 ? 4 : 8)), m.rows);
+  const int64_t pieces = m.cols / (T == MxType::kF32 ? 4 : 8);
+  const dim3 grid((unsigned)std::min<int64_t>((pieces + 1023) / 1024, 1024), (unsigned)std::min<int64_t>(m.rows, 65535));
+  u32x4_t *const out = static_cast<u32x4_t *>(W);
+  if (m.rows * pieces * 16 >= kNtStore)
+    hipLaunchKernelGGL((i8_dequant_kernel<T, true>), grid, dim3(256), 0, stream, m.codes, m.scales, out, (int)pieces, m.rows);
+  else
+    hipLaunchKernelGGL((i8_dequant_kernel<T, false>), grid, dim3(256), 0, stream, m.codes, m.scales, out, (int)pieces, m.rows);
 }
 
 }  // namespace
