@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "i8_device.hpp"
+#include "mx_tile.hpp"
 
 namespace aqlm {
 namespace {
@@ -26,136 +27,582 @@ struct I8GradRowsArgs {
   I8Act act;
 };
 
-// D of row `i` of the matrix (both matrices), before its power of two.
-template <MxType T, bool GATED>
-__device__ __forceinline__ void grad_terms(const I8GradRowsArgs &A, int64_t at, int i, float (&v)[GATED ? 2 : 1]) {
-  const uint16_t h = static_cast<const uint16_t *>(A.dy)[at + i];
-  const float dy = T == MxType::kF16 ? h2f(h) : __builtin_bit_cast(float, (uint32_t)h << 16);
+// The terms of one row of the matrix (both matrices), before their power of two.
+template <bool GATED>
+__device__ __forceinline__ void grad_terms(const I8GradRowsArgs &A, float dy, float g, float u, float wg, float wu,
+                                           float (&v)[GATED ? 2 : 1]) {
   if constexpr (GATED) {
     float a, slope;
-    act_and_slope(A.act, A.g[at + i], a, slope);
-    v[0] = dy * A.u[at + i] * slope * A.ws[0][i];
-    v[1] = dy * a * A.ws[1][i];
+    act_and_slope(A.act, g, a, slope);
+    v[0] = dy * u * slope * wg;
+    v[1] = dy * a * wu;
   } else {
-    v[0] = dy * A.ws[0][i];
+    v[0] = dy * wg;
   }
 }
 
-template <MxType T, bool GATED>
-__global__ __launch_bounds__(256) void i8_grad_rows_kernel(const I8GradRowsArgs A, int64_t batch) {
-  constexpr int M = GATED ? 2 : 1;
-  __shared__ uint32_t tops[4];
+template <MxType T> __device__ __forceinline__ float half_value(uint32_t h) {
+  return T == MxType::kF16 ? h2f(h) : __builtin_bit_cast(float, h << 16);
+}
+
+// Bits of the largest finite magnitude.
+__device__ __forceinline__ uint32_t finite_max(uint32_t top, float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+  return b < 0x7F800000u ? max(top, b) : top;
+}
+
+// Maximum over a workgroup of WAVES wavefronts; the power of two that takes it to
+// [2^14, 2^15).
+template <int WAVES> __device__ __forceinline__ int power_of(uint32_t top, uint32_t *tops) {
+  top = wave_max(top);
+  __syncthreads();  // the token before is done with `tops`
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) top = max(top, tops[w]);
+  return top == 0 ? 0 : 15 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, top));
+}
+
+// A token a workgroup, 8 rows of the matrix a thread and round, the terms in
+// registers between their maximum and their rounding: everything is read and written
+// once, 16 bytes at a time. (rows a multiple of 8)
+template <MxType T, bool GATED, int WAVES, int ROUNDS>
+__global__ __launch_bounds__(WAVES * 64) void i8_grad_rows_kernel(const I8GradRowsArgs A, int64_t batch) {
+  constexpr int M = GATED ? 2 : 1, kThreads = WAVES * 64;
+  __shared__ uint32_t tops[WAVES];
   for (int64_t tok = blockIdx.x; tok < batch; tok += gridDim.x) {
     const int64_t at = tok * A.rows;
-    uint32_t top = 0;  // of the finite ones
-    for (int i = threadIdx.x; i < A.rows; i += 256) {
-      float v[M];
-      grad_terms<T, GATED>(A, at, i, v);
+    float v[ROUNDS][M][8];
+    uint32_t top = 0;
 #pragma unroll
-      for (int m = 0; m < M; ++m) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, v[m]) & 0x7FFFFFFFu;
-        if (b < 0x7F800000u) top = max(top, b);
+    for (int r = 0; r < ROUNDS; ++r) {
+      const int i = 8 * ((int)threadIdx.x + r * kThreads);
+      if (i < A.rows) {
+        const uint4 h = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(A.dy) + at + i);
+        const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+        float c[M][8], gu[2][8] = {};
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float4_t *>(&c[m][4 * k]) = *reinterpret_cast<const float4_t *>(A.ws[m] + i + 4 * k);
+        if constexpr (GATED) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            *reinterpret_cast<float4_t *>(&gu[0][4 * k]) = *reinterpret_cast<const float4_t *>(A.g + at + i + 4 * k);
+            *reinterpret_cast<float4_t *>(&gu[1][4 * k]) = *reinterpret_cast<const float4_t *>(A.u + at + i + 4 * k);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float t[M];
+          grad_terms<GATED>(A, half_value<T>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu), gu[0][e], gu[1][e], c[0][e],
+                            c[M - 1][e], t);
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            v[r][m][e] = t[m];
+            top = finite_max(top, t[m]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[r][m][e] = 0.f;
       }
     }
-    top = wave_max(top);
-    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-    // largest = f 2^e, 1/2 <= f < 1: taken to [2^14, 2^15)
-    int e = 0;
-    if (top != 0) {
-      const float f = __builtin_bit_cast(float, top);
-      e = 15 - (__builtin_amdgcn_frexp_expf(f));
-    }
-    if (threadIdx.x == 0) A.power[tok] = -e;
-    for (int i = threadIdx.x; i < A.part; i += 256) {
-      float v[M] = {};
-      if (i < A.rows) grad_terms<T, GATED>(A, at, i, v);
+    const int e2 = power_of<WAVES>(top, tops);
+    if (threadIdx.x == 0) A.power[tok] = -e2;
 #pragma unroll
-      for (int m = 0; m < M; ++m)
-        A.d[tok * A.ld + m * A.part + i] = (uint16_t)f2h(__builtin_amdgcn_ldexpf(v[m], e));
+    for (int r = 0; r < ROUNDS; ++r) {
+      const int i = 8 * ((int)threadIdx.x + r * kThreads);
+      if (i < A.part) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = f2h(__builtin_amdgcn_ldexpf(v[r][m][e], e2));
+          *reinterpret_cast<uint4 *>(A.d + tok * A.ld + m * A.part + i) =
+              make_uint4(o[0] | (o[1] << 16), o[2] | (o[3] << 16), o[4] | (o[5] << 16), o[6] | (o[7] << 16));
+        }
+      }
     }
-    __syncthreads();
   }
 }
 
+// Ragged rows, whose tokens begin anywhere, and more rows than registers hold: one row
+// of the matrix a thread, computed twice.
+template <MxType T, bool GATED>
+__global__ __launch_bounds__(1024) void i8_grad_any_rows_kernel(const I8GradRowsArgs A, int64_t batch) {
+  constexpr int M = GATED ? 2 : 1;
+  __shared__ uint32_t tops[16];
+  for (int64_t tok = blockIdx.x; tok < batch; tok += gridDim.x) {
+    const int64_t at = tok * A.rows;
+    auto terms = [&](int i, float(&v)[M]) __attribute__((always_inline)) {
+      const float dy = half_value<T>(static_cast<const uint16_t *>(A.dy)[at + i]);
+      grad_terms<GATED>(A, dy, GATED ? A.g[at + i] : 0.f, GATED ? A.u[at + i] : 0.f, A.ws[0][i], A.ws[M - 1][i], v);
+    };
+    uint32_t top = 0;
+    for (int i = threadIdx.x; i < A.rows; i += 1024) {
+      float v[M];
+      terms(i, v);
+#pragma unroll
+      for (int m = 0; m < M; ++m) top = finite_max(top, v[m]);
+    }
+    const int e2 = power_of<16>(top, tops);
+    if (threadIdx.x == 0) A.power[tok] = -e2;
+    for (int i = threadIdx.x; i < A.part; i += 1024) {
+      float v[M] = {};
+      if (i < A.rows) terms(i, v);
+#pragma unroll
+      for (int m = 0; m < M; ++m) A.d[tok * A.ld + m * A.part + i] = (uint16_t)f2h(__builtin_amdgcn_ldexpf(v[m], e2));
+    }
+  }
+}
+
+template <MxType T, bool GATED> void launch_terms(const I8GradRowsArgs &R, int64_t batch, hipStream_t stream) {
+  const dim3 grid((unsigned)std::min<int64_t>(batch, 1 << 20));
+  if (R.rows % 8 != 0 || R.part > 32768)
+    hipLaunchKernelGGL((i8_grad_any_rows_kernel<T, GATED>), grid, dim3(1024), 0, stream, R, batch);
+  else if (R.part <= 2048)
+    hipLaunchKernelGGL((i8_grad_rows_kernel<T, GATED, 4, 1>), grid, dim3(256), 0, stream, R, batch);
+  else if (R.part <= 4096)
+    hipLaunchKernelGGL((i8_grad_rows_kernel<T, GATED, 4, 2>), grid, dim3(256), 0, stream, R, batch);
+  else if (R.part <= 8192)
+    hipLaunchKernelGGL((i8_grad_rows_kernel<T, GATED, 8, 2>), grid, dim3(512), 0, stream, R, batch);
+  else if (R.part <= 16384)
+    hipLaunchKernelGGL((i8_grad_rows_kernel<T, GATED, 16, 2>), grid, dim3(1024), 0, stream, R, batch);
+  else
+    hipLaunchKernelGGL((i8_grad_rows_kernel<T, GATED, 16, 4>), grid, dim3(1024), 0, stream, R, batch);
+}
+
+// The product D . C: one workgroup per [columns of C] x [tokens] tile. The sum runs
+// over the rows of C, along which codes are not contiguous, while a matrix
+// instruction wants eight consecutive terms of the sum in a lane.
+//   * A K step is 64 rows of one matrix. Codes and D go from memory straight to LDS,
+//     one or two steps ahead. 16-byte chunk c of row r of the codes lies at chunk
+//     c ^ turn(r), so that the 32 lanes that read 8 rows x 32 columns at once touch
+//     all banks; D's 128-byte rows are permuted as in the other tile kernels.
+//   * ds_read_b64_tr_b8 transposes on the way out of LDS: 16 lanes give the places of
+//     8 rows x 16 columns and each receives eight rows of one column, which is one
+//     side of v_mfma_f32_32x32x16_f16 but for the type.
+//   * A code becomes float16 in registers: its bits with the sign bit turned, below
+//     the exponent of 1024, are 1152 more than it, exactly. Ten instructions for
+//     the eight terms of a lane, between the products of the chunk before.
 struct I8GradArgs {
   const int8_t *w[2];
   const uint16_t *d;  // [batch][ld]
   const int *power;
   uint16_t *dx;       // [batch][cols]
-  int rows, part, ld, cols, batch, matrices;
+  float4_t *part;     // [splits][tiles][RT * NT * 4][64 RW TW], or null
+  int rows, part_rows, ld, cols, batch, matrices;
+  int col_tiles, tok_tiles, splits, steps_per_split;
 };
 
-// One workgroup: 64 columns of W by 64 tokens, 32 rows of W a step.
-template <MxType T>
-__global__ __launch_bounds__(256) void i8_grad_kernel(const I8GradArgs A) {
-  __shared__ __attribute__((aligned(16))) uint16_t wt[64][40], xt[64][40];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col0 = (int)blockIdx.x * 64, tok0 = (int)blockIdx.y * 64;
-  const int toks = __builtin_amdgcn_readfirstlane(min(64, A.batch - tok0));
-  const Rsrc xrs = make_rsrc(A.d + (int64_t)tok0 * A.ld, (uint32_t)toks * (uint32_t)A.ld * 2u);
-  float16_t acc;
+// RW x TW wavefronts of RT x NT 32 x 32 tiles, KW such sets that share K.
+template <int RT_, int NT_, int RW_, int TW_, int KW_, int STAGES_> struct Shape {
+  static constexpr int RT = RT_, NT = NT_, RW = RW_, TW = TW_, KW = KW_, STAGES = STAGES_;
+  static constexpr int kWaves = RW * TW, kThreads = 64 * kWaves;  // of one share of K
+  static constexpr int kCols = 32 * RT * RW, kToks = 32 * NT * TW;
+  static constexpr int kWBytes = 64 * kCols, kStage = kWBytes + kToks * 128;
+  static constexpr int kSums = kCols * kToks * 4;
+};
+
+// Where chunk c of row r of the codes lies: c ^ turn.
+template <int COLS> __device__ __forceinline__ int turn_of(int r) {
+  static_assert(COLS == 256 || COLS == 128, "16 or 8 chunks a row");
+  return COLS == 256 ? 2 * (r & 7) : 2 * ((r >> 1) & 3);
+}
+
+// Eight codes as float16.
+__device__ __forceinline__ uint4 codes_to_f16(const uint2 &c) {
+  const uint32_t in[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
+  const half2_t off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+  uint32_t r[4];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-  for (int m = 0; m < A.matrices; ++m)
-    for (int o0 = 0; o0 < A.part; o0 += 32) {
-      const int rows = __builtin_amdgcn_readfirstlane(max(0, min(32, A.rows - o0)));
-      const Rsrc wrs = make_rsrc(A.w[m] + (rows > 0 ? (int64_t)o0 * A.cols : 0), (uint32_t)rows * (uint32_t)A.cols);
-      const int o = tid >> 3, c = 8 * (tid & 7);
-      const uint2 b = buf_load8(wrs, col0 + c < A.cols ? (uint32_t)o * A.cols + col0 + c : kMxOOB);
-      const uint4 d = buf_load16(xrs, (uint32_t)(tid >> 2) * A.ld * 2u + (uint32_t)(m * A.part + o0) * 2u + 16u * (tid & 3));
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = __builtin_amdgcn_perm(0x64646464u, in[i >> 1], i & 1 ? 0x04030402u : 0x04010400u);
+    r[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, v) + off);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <MxType T, class S>
+__global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8GradArgs A) {
+  constexpr int RT = S::RT, NT = S::NT, TW = S::TW, KW = S::KW, kWaves = S::kWaves, kCols = S::kCols;
+  constexpr int kStage = S::kStage, kWBytes = S::kWBytes;
+  constexpr int kArray = KW * kStage > (KW > 1 ? S::kSums : 0) ? KW * kStage : S::kSums;
+  constexpr int kStore = RT * 2048;  // of LDS a wavefront, for its results
+  static_assert(kArray >= kWaves * kStore, "room for the results");
+  // one array per stage: the compiler then knows which loads into LDS a read
+  // of LDS can depend on
+  __shared__ __attribute__((aligned(16))) uint8_t s0[kArray], s1[kArray], s2[S::STAGES > 2 ? kArray : 16];
+  const int lane = threadIdx.x & 63;
+  const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = KW == 1 ? 0 : wave_all / kWaves, wave = KW == 1 ? wave_all : wave_all % kWaves;
+  const int rw = wave / TW, tw = wave % TW;
+  const int l32 = lane & 31, h = lane >> 5;
+  const int tiles = A.col_tiles * A.tok_tiles;
+  const int job = xcd_job((int)blockIdx.x, tiles * A.splits);
+  const int split = __builtin_amdgcn_readfirstlane(job / tiles);
+  const TilePlace at = tile_place(job - split * tiles, A.col_tiles, A.tok_tiles);
+  const int col0 = at.row_tile * kCols, tok0 = at.tok_tile * S::kToks;
+  const uint32_t cols = (uint32_t)A.cols;
+
+  // The steps of this split, and of those the wavefront's: each of the KW shares
+  // takes as many as the largest (past its end with zeros), so that all meet at
+  // every barrier. Steps go through the first matrix, then the second.
+  const int per = A.part_rows >> 6;  // steps of a matrix
+  const int t0 = split * A.steps_per_split, t1 = min(per * A.matrices, t0 + A.steps_per_split);
+  const int share = (t1 - t0 + KW - 1) / KW;
+  const int g0 = t0 + kw * share, g1 = min(t1, g0 + share), gend = g0 + share;
+
+  const int tile_toks = __builtin_amdgcn_readfirstlane(min(S::kToks, A.batch - tok0));
+  const Rsrc xrs = make_rsrc(A.d + (int64_t)tok0 * A.ld, (uint32_t)tile_toks * (uint32_t)A.ld * 2u);
+
+  float16_t acc[RT][NT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  const int wcol0 = col0 + rw * 32 * RT, wtok0 = tok0 + tw * 32 * NT;
+  int power[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) power[j] = A.power[min(wtok0 + 32 * j + l32, A.batch - 1)];
+
+  // Step t into a stage: loads of a wavefront fill 1 KiB in lane order, 1024 /
+  // kCols rows of codes or eight tokens.
+  constexpr int kWLoads = 64 * kCols / 1024 / kWaves, kXLoads = S::kToks / 8 / kWaves;
+  constexpr int kLoadRows = 1024 / kCols, kRowLanes = kCols / 16;
+  static_assert(64 * kCols % (1024 * kWaves) == 0 && S::kToks % (8 * kWaves) == 0, "loads");
+  static_assert(kWLoads <= 8 && kXLoads <= 8, "places of a lane's loads");
+  uint32_t woff[8], xoff[8];
+#pragma unroll
+  for (int i = 0; i < kWLoads; ++i) {
+    const int r = (wave + i * kWaves) * kLoadRows + lane / kRowLanes;
+    const int c = (lane % kRowLanes) ^ turn_of<kCols>(r);
+    woff[i] = col0 + 16 * c < A.cols ? (uint32_t)r * cols + (uint32_t)(col0 + 16 * c) : kMxOOB;
+  }
+#pragma unroll
+  for (int i = 0; i < kXLoads; ++i) {
+    const int r = 8 * (wave + i * kWaves) + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+    xoff[i] = (uint32_t)r * (uint32_t)A.ld * 2u + 16u * c;
+  }
+  typedef __attribute__((address_space(3))) void *LdsPtr;
+  auto fill = [&](int t, uint8_t *a) __attribute__((always_inline)) {
+    // a resource of the step's rows: past the last they read zero
+    const bool second = t >= per;
+    const int o = 64 * (second ? t - per : t);
+    const int rows = __builtin_amdgcn_readfirstlane(t < g1 ? max(0, min(64, A.rows - o)) : 0);
+    const int8_t *const base = second ? A.w[1] : A.w[0];
+    const Rsrc wrs = make_rsrc(base + (rows > 0 ? (int64_t)o * cols : 0), (uint32_t)rows * cols);
+    const uint32_t k = t < g1 ? (uint32_t)t * 128u : kMxOOB;
+#pragma unroll
+    for (int i = 0; i < kWLoads; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wrs, (LdsPtr)(a + (kw * kStage + (wave + i * kWaves) * 1024)), 16,
+                                               woff[i], 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs,
+                                               (LdsPtr)(a + (kw * kStage + kWBytes + (wave + i * kWaves) * 1024)), 16,
+                                               xoff[i] + k, 0, 0, 0);
+  };
+
+  // places of the lane's operands: 16 further rows of codes, 32 further columns or
+  // tokens are at the same permutation but for the columns' chunk
+  const int e16 = lane & 15, er = 8 * h + (e16 >> 1);  // row (of 16), and the lane's half chunk
+  uint32_t wbase[4], xbase[4];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int c = (rw * 32 * RT + 32 * i) / 16 + ((lane >> 4) & 1);
+    wbase[i] = kw * kStage + er * kCols + ((c ^ turn_of<kCols>(er)) << 4) + 8 * (e16 & 1);
+  }
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int t = tw * 32 * NT + l32;
+    xbase[s] = kw * kStage + kWBytes + t * 128 + (((2 * s + h) ^ ((t >> 1) & 7)) << 4);
+  }
+  static_assert(RT <= 4, "places of the operands");
+  uint2 raw[2][RT];
+  uint4 w[2][RT], b[2][NT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) w[1][i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) b[1][j] = make_uint4(0, 0, 0, 0);
+  auto read_w = [&](const uint8_t *a, int s) __attribute__((always_inline)) {
+    typedef int int2_vt __attribute__((ext_vector_type(2)));
+    typedef __attribute__((address_space(3))) int2_vt *TrPtr;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      raw[s & 1][i] = __builtin_bit_cast(
+          uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((TrPtr)(a + (wbase[i] + (uint32_t)(16 * s * kCols)))));
+  };
+  auto read_x = [&](const uint8_t *a, int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) b[s & 1][j] = *reinterpret_cast<const uint4 *>(a + (xbase[s] + 4096u * j));
+  };
+  auto convert = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) w[s & 1][i] = codes_to_f16(raw[s & 1][i]);
+  };
+  auto products = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma32<MxType::kF16>(w[s & 1][i], b[s & 1][j], acc[i][j]);
+  };
+  // Step t from stage `a`. `far` is the stage that the step before read, filled for
+  // step t + STAGES - 1. Codes are read two chunks ahead and converted one ahead; the
+  // products of a step's last chunk come behind the barrier, while the first reads of
+  // the next step are under way. (The first step's are zeros.) Before the barrier the
+  // wavefront waits for its own reads and until at most STAGES - 2 steps' loads are
+  // under way: loads complete in order, so behind it step t + 1 lies in LDS.
+  auto step = [&](int t, const uint8_t *a, uint8_t *far) __attribute__((always_inline)) {
+    fill(t + S::STAGES - 1, far);
+    __builtin_amdgcn_sched_barrier(0);
+    read_w(a, 0);
+    read_w(a, 1);
+    products(3);
+    read_x(a, 0);
+    convert(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      read_x(a, s + 1);
+      if (s < 2) read_w(a, s + 2);
+      products(s);
+      convert(s + 1);
+      __builtin_amdgcn_sched_group_barrier(0x100, NT, 0);
+      if (s < 2) __builtin_amdgcn_sched_group_barrier(0x100, RT, 0);
+#pragma unroll
+      for (int k = 0; k < RT * NT; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, (10 + NT - 1) / NT, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // (keeps the products in their step: nothing else ties them to a place)
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j][0] = materialize(acc[i][j][0]);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"((S::STAGES - 2) * (kWLoads + kXLoads)) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  fill(g0, s0);
+  __builtin_amdgcn_sched_barrier(0);
+  if constexpr (S::STAGES > 2) {
+    fill(g0 + 1, s1);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  asm volatile("s_waitcnt vmcnt(%0)" : : "i"((S::STAGES - 2) * (kWLoads + kXLoads)) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" : : : "memory");
+  // (whole turns of the stages: with a way out after each step the compiler keeps
+  // the sums in two sets of registers and moves them)
+  int g = g0;
+  for (; g + S::STAGES <= gend; g += S::STAGES) {
+    step(g, s0, S::STAGES > 2 ? s2 : s1);
+    step(g + 1, s1, s0);
+    if constexpr (S::STAGES > 2) step(g + 2, s2, s1);
+  }
+  if (g < gend) step(g, s0, S::STAGES > 2 ? s2 : s1);
+  if constexpr (S::STAGES > 2)
+    if (g + 1 < gend) step(g + 1, s1, s0);
+  products(3);
+  // what is under way past the last step is in LDS before it is used again
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  __syncthreads();
+
+  if constexpr (KW > 1) {  // the shares' sums, in order
+    auto slot = [&](int i, int j, int q) __attribute__((always_inline)) {
+      return reinterpret_cast<float4_t *>(s0 + ((((i * NT + j) * 4 + q) * kWaves + wave) * 64 + lane) * 16);
+    };
+#pragma unroll 1
+    for (int k = 1; k < KW; ++k) {
+      if (k > 1) __syncthreads();
+      if (kw == k) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) *slot(i, j, q) = quarter(acc[i][j], q);
+      }
       __syncthreads();
+      if (kw == 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        wt[c + e][o] = (uint16_t)f2h((float)(int8_t)((e < 4 ? b.x : b.y) >> (8 * (e & 3))));
-      *reinterpret_cast<uint4 *>(&xt[tid >> 2][8 * (tid & 3)]) = d;
-      __syncthreads();
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int k = 16 * s + 8 * (lane >> 5);
-        const uint4 wv = *reinterpret_cast<const uint4 *>(&wt[32 * (wave & 1) + (lane & 31)][k]);
-        const uint4 xv = *reinterpret_cast<const uint4 *>(&xt[32 * (wave >> 1) + (lane & 31)][k]);
-        acc = mx_mfma32<MxType::kF16>(wv, xv, acc);
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float4_t v = *slot(i, j, q);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+            }
       }
     }
-  const int tok = tok0 + 32 * (wave >> 1) + (lane & 31);
-  if (tok >= A.batch) return;
+    if (kw != 0) return;
+  }
+
+  if (A.splits > 1) {
+    float4_t *p = A.part + (int64_t)job * (RT * NT * 4 * S::kThreads) + wave * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        if (wtok0 + 32 * j + l32 < A.batch) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) p[((i * NT + j) * 4 + q) * S::kThreads] = quarter(acc[i][j], q);
+        }
+    return;
+  }
+  // Register 4 q + e of a 32 x 32 tile is column 8 q + 4 h + e, token l32. The results
+  // pass through LDS, 32 tokens at a time, from where neighbouring lanes store a
+  // token's columns (a multiple of 16).
+  constexpr int kChunks = 4 * RT;  // of 16 bytes, eight columns, for a token
+  uint8_t *const mine = s1 + wave * kStore;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = f2t<T>(materialize(__builtin_amdgcn_ldexpf(acc[i][j][4 * q + e], power[j])));
+        const int c = (4 * i + q) ^ (l32 & (kChunks - 1));
+        *reinterpret_cast<uint2 *>(mine + (l32 * kChunks + c) * 16 + 8 * h) =
+            make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+      }
+#pragma unroll
+    for (int k = 0; k < kChunks / 2; ++k) {
+      const int id = 64 * k + lane, tt = id / kChunks, c = id % kChunks;
+      const uint4 r = *reinterpret_cast<const uint4 *>(mine + (tt * kChunks + (c ^ (tt & (kChunks - 1)))) * 16);
+      const int tok = wtok0 + 32 * j + tt, col = wcol0 + 8 * c;
+      if (tok < A.batch && col < A.cols) *reinterpret_cast<uint4 *>(A.dx + (int64_t)tok * A.cols + col) = r;
+    }
+  }
+}
+
+// Sums of the split parts, in order of the split, and the results.
+template <MxType T, class S>
+__global__ __launch_bounds__(S::kThreads) void i8_grad_sum_kernel(const I8GradArgs A) {
+  constexpr int RT = S::RT, NT = S::NT;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tiles = A.col_tiles * A.tok_tiles;
+  const int slot = (int)blockIdx.x % (RT * NT * 4), tile = (int)blockIdx.x / (RT * NT * 4);
+  const int q = slot & 3, j = (slot >> 2) % NT, i = (slot >> 2) / NT;
+  const TilePlace at = tile_place(tile, A.col_tiles, A.tok_tiles);
+  const int tok = at.tok_tile * S::kToks + (wave % S::TW) * 32 * NT + 32 * j + (lane & 31);
+  const int col = at.row_tile * S::kCols + (wave / S::TW) * 32 * RT + 32 * i + 8 * q + 4 * (lane >> 5);
+  if (tok >= A.batch || col >= A.cols) return;
+  const float4_t *p = A.part + ((int64_t)tile * (RT * NT * 4) + slot) * S::kThreads + tid;
+  const int64_t stride = (int64_t)tiles * (RT * NT * 4) * S::kThreads;
+  float4_t v = p[0];
+  for (int s = 1; s < A.splits; s += 4) {  // four loads under way
+    float4_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[k] = p[min(s + k, A.splits - 1) * stride];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s + k < A.splits) v += u[k];
+  }
   const int power = A.power[tok];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float4_t v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_ldexpf(acc[4 * q + e], power);
-    store4<T>(A.dx + (int64_t)tok * A.cols, col0 + 32 * (wave & 1) + 8 * q + 4 * (lane >> 5), A.cols, v, true);
+  for (int e = 0; e < 4; ++e) v[e] = materialize(__builtin_amdgcn_ldexpf(v[e], power));
+  store4<T>(A.dx + (int64_t)tok * A.cols, col, A.cols, v, true);
+}
+
+typedef Shape<2, 2, 4, 2, 1, 3> Large;   // 256 columns x 128 tokens
+typedef Shape<2, 2, 2, 1, 2, 3> Middle;  // 128 x 64
+typedef Shape<2, 1, 2, 1, 2, 3> Small;   // 128 x 32
+
+struct GradCost {
+  int cols, toks, kw, sums;  // sums: bytes of a workgroup's in the workspace
+  double a, b;
+};
+template <class S> constexpr GradCost cost_of(double a, double b) { return {S::kCols, S::kToks, S::KW, S::kSums, a, b}; }
+constexpr GradCost kCosts[] = {cost_of<Large>(0.3, 0.5), cost_of<Middle>(0.3, 0.3), cost_of<Small>(0.25, 0.25)};
+
+struct GradPlan {
+  int shape, splits, steps_per_split;
+  int64_t col_tiles, tok_tiles;
+  double us;
+  int64_t ws_bytes() const {
+    return splits == 1 ? 0 : col_tiles * tok_tiles * splits * (int64_t)kCosts[shape].sums;
   }
+};
+
+GradPlan plan_of(const I8Desc &W, bool gated, int64_t batch) {
+  GradPlan best{};
+  const int64_t steps = (W.rows + 63) / 64 * (gated ? 2 : 1);
+  for (int c = 0; c < 3; ++c) {
+    const GradCost &k = kCosts[c];
+    GradPlan p{};
+    p.shape = c;
+    p.col_tiles = (W.cols + k.cols - 1) / k.cols;
+    p.tok_tiles = (batch + k.toks - 1) / k.toks;
+    const int64_t tiles = p.col_tiles * p.tok_tiles;
+    for (int s = 1; s <= 8; ++s) {
+      p.steps_per_split = (int)((steps + s - 1) / s);
+      p.splits = (int)((steps + p.steps_per_split - 1) / p.steps_per_split);
+      if (p.splits != s || (s > 1 && tiles * s > 256)) break;
+      const double whole = (double)(tiles * s / 256), rest = (double)(tiles * s % 256) / 256.0;
+      const double one = whole * (k.a + k.b) + (rest > 0 ? k.a + k.b * rest : 0.0);
+      double us = 2.7 + (double)((p.steps_per_split + k.kw - 1) / k.kw) * one;
+      if (s > 1) us += 2.3 + (double)p.ws_bytes() * 2.0 / 4e6;
+      p.us = us;
+      if (best.splits == 0 || us < best.us) best = p;
+    }
+  }
+  return best;
+}
+
+template <MxType T, class S> hipError_t launch_shape(const I8GradArgs &A, hipStream_t stream) {
+  const unsigned tiles = (unsigned)(A.col_tiles * A.tok_tiles);
+  hipLaunchKernelGGL((i8_grad_kernel<T, S>), dim3(tiles * A.splits), dim3(S::kThreads * S::KW), 0, stream, A);
+  if (A.splits > 1)
+    hipLaunchKernelGGL((i8_grad_sum_kernel<T, S>), dim3(tiles * S::RT * S::NT * 4), dim3(S::kThreads), 0, stream, A);
+  return hipGetLastError();
 }
 
 // Rows of one matrix in D: whole steps.
 int64_t part_of(const I8Desc &W) { return (W.rows + 63) / 64 * 64; }
-// Workspace: the powers, then D, from multiples of 256 bytes on.
+// Workspace: the powers, D and the split sums, from multiples of 256 bytes on.
 int64_t terms_at(int64_t batch) { return (batch * 4 + 255) / 256 * 256; }
+int64_t sums_at(const I8Desc &W, bool gated, int64_t batch) {
+  return terms_at(batch) + (batch * part_of(W) * (gated ? 2 : 1) * 2 + 255) / 256 * 256;
+}
 
 template <MxType T> hipError_t grad_as(const I8Grad &p, void *ws, hipStream_t stream) {
   const int part = (int)part_of(p.W), ld = part * (p.gated() ? 2 : 1);
   int *const power = static_cast<int *>(ws);
   uint16_t *const d = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + terms_at(p.batch));
   const I8GradRowsArgs R = {p.dy, p.g, p.u, {p.W.scales, p.up.scales}, d, power, (int)p.W.rows, part, ld, p.act};
-  const dim3 grid((unsigned)std::min<int64_t>(p.batch, 1 << 20));
-  if (p.gated()) hipLaunchKernelGGL((i8_grad_rows_kernel<T, true>), grid, dim3(256), 0, stream, R, p.batch);
-  else hipLaunchKernelGGL((i8_grad_rows_kernel<T, false>), grid, dim3(256), 0, stream, R, p.batch);
-  const I8GradArgs A = {{p.W.codes, p.up.codes}, d, power, static_cast<uint16_t *>(p.dx), (int)p.W.rows, part, ld,
-                        (int)p.W.cols, (int)p.batch, p.gated() ? 2 : 1};
-  hipLaunchKernelGGL((i8_grad_kernel<T>), dim3((unsigned)((p.W.cols + 63) / 64), (unsigned)((p.batch + 63) / 64)),
-                     dim3(256), 0, stream, A);
-  return hipGetLastError();
+  if (p.gated()) launch_terms<T, true>(R, p.batch, stream);
+  else launch_terms<T, false>(R, p.batch, stream);
+  const GradPlan g = plan_of(p.W, p.gated(), p.batch);
+  float4_t *const sums = reinterpret_cast<float4_t *>(static_cast<uint8_t *>(ws) + sums_at(p.W, p.gated(), p.batch));
+  const I8GradArgs A = {{p.W.codes, p.up.codes}, d, power, static_cast<uint16_t *>(p.dx), sums, (int)p.W.rows, part, ld,
+                        (int)p.W.cols, (int)p.batch, p.gated() ? 2 : 1, (int)g.col_tiles, (int)g.tok_tiles, g.splits,
+                        g.steps_per_split};
+  if (g.shape == 0) return launch_shape<T, Large>(A, stream);
+  if (g.shape == 1) return launch_shape<T, Middle>(A, stream);
+  return launch_shape<T, Small>(A, stream);
 }
 
 }  // namespace
 
 int64_t i8_grad_ws_bytes(const I8Desc &W, bool gated, int64_t batch) {
-  return terms_at(batch) + batch * part_of(W) * (gated ? 2 : 1) * 2;
+  return sums_at(W, gated, batch) + plan_of(W, gated, batch).ws_bytes();
 }
 
 hipError_t launch_i8_grad(const I8Grad &p, void *ws, hipStream_t stream) {
