@@ -9,6 +9,12 @@ namespace aqlm {
 typedef int int4_vt __attribute__((ext_vector_type(4)));
 typedef int int16_vt __attribute__((ext_vector_type(16)));
 
+// Pins a value in a register at this place of the code.
+__device__ __forceinline__ int held(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // v_mfma_i32_16x16x64_i8 / 32x32x32_i8: lane (r, q) gives the 16 bytes q of row r
 // of each side (q = lane / 16 or lane / 32).
 __device__ __forceinline__ int4_vt i8_mfma16(const uint4 &a, const uint4 &b, int4_vt c) {

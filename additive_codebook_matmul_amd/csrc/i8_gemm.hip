@@ -6,49 +6,10 @@
 // just what v_mfma_i32_16x16x64_i8 takes. The integer sums meet in LDS.
 #include <algorithm>
 
-#include "i8_device.hpp"
+#include "i8_gemm.hpp"
 
 namespace aqlm {
 namespace {
-
-struct I8Args {
-  const int8_t *w[2];     // the layer, or gate and up
-  const float *ws[2];
-  const int8_t *x;        // [batch][cols]
-  const float *xs;
-  uint16_t *y;
-  float *g, *u;           // or null
-  int rows, cols, batch;
-  I8Act act;
-};
-
-// Results of four consecutive rows, from `row` on, of token `tok`.
-template <MxType T, bool GATED>
-__device__ __forceinline__ void i8_store4(const I8Args &A, int tok, int row, const int4_vt (&sums)[GATED ? 2 : 1]) {
-  const float token = A.xs[tok];
-  const int64_t at = (int64_t)tok * A.rows;
-  float v[GATED ? 2 : 1][4], out[4];
-#pragma unroll
-  for (int m = 0; m < (GATED ? 2 : 1); ++m)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[m][e] = i8_value(sums[m][e], A.ws[m][min(row + e, A.rows - 1)], token);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if constexpr (GATED) out[e] = materialize(act_value(A.act, v[0][e]) * v[1][e]);
-    else out[e] = v[0][e];
-  }
-  if constexpr (GATED) {
-    if (A.g) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (row + e < A.rows) {
-          A.g[at + row + e] = v[0][e];
-          A.u[at + row + e] = v[1][e];
-        }
-    }
-  }
-  store4<T>(A.y + at, row, A.rows, float4_t{out[0], out[1], out[2], out[3]}, (A.rows & 3) == 0);
-}
 
 template <MxType T, bool GATED, int NW, int NT>
 __global__ __launch_bounds__(NW * 64) void i8_skinny_kernel(const I8Args A) {
@@ -122,11 +83,15 @@ template <MxType T, bool GATED> hipError_t product_as(const I8Args &A, hipStream
 
 // Workspace of quantised activations: scales, then codes, from multiples of 256 bytes on.
 int64_t codes_at(int64_t batch) { return (batch * 4 + 255) / 256 * 256; }
+int64_t product_at(const I8Desc &W, int64_t batch) { return codes_at(batch) + (batch * W.cols + 255) / 256 * 256; }
+
+bool tiles_pay(const I8Desc &, bool, int64_t batch) { return batch > 32; }
 
 }  // namespace
 
-int64_t i8_product_ws_bytes(const I8Desc &W, bool, int64_t batch, bool quant) {
-  return quant ? codes_at(batch) + batch * W.cols : 0;
+int64_t i8_product_ws_bytes(const I8Desc &W, bool gated, int64_t batch, bool quant) {
+  return (quant ? product_at(W, batch) : 0) +
+         (tiles_pay(W, gated, batch) ? i8_tile_ws_bytes(W.rows, W.cols, gated, batch) : 0);
 }
 
 hipError_t launch_i8_product(const I8Product &p, void *ws, hipStream_t stream) {
@@ -139,7 +104,9 @@ hipError_t launch_i8_product(const I8Product &p, void *ws, hipStream_t stream) {
     if (e != hipSuccess) return e;
     A.x = codes;
     A.xs = scales;
+    ws = static_cast<uint8_t *>(ws) + product_at(p.W, p.batch);
   }
+  if (tiles_pay(p.W, p.gated(), p.batch)) return launch_i8_tile(A, p.type, p.gated(), ws, stream);
   if (p.type == MxType::kF16)
     return p.gated() ? product_as<MxType::kF16, true>(A, stream) : product_as<MxType::kF16, false>(A, stream);
   return p.gated() ? product_as<MxType::kBF16, true>(A, stream) : product_as<MxType::kBF16, false>(A, stream);
