@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ("api.hip", "dequant.hip", "gemv.hip", "gemv_mfma.hip", "gemv_slice.hip", "gemm.hip",
            "gemm_mid.hip", "gemm_tile.hip", "general.hip", "encode.hip", "mx_api.hip",
            "mx_convert.hip", "mx_gemm.hip", "mx_gemm_tile.hip", "mx_gemm_mx.hip", "mx_gemm_mx_tile.hip",
-           "mx_grad.hip", "i8_api.hip", "i8_convert.hip", "i8_gemm.hip", "i8_tile.hip", "i8_grad.hip")
+           "mx_grad.hip", "i8_api.hip", "i8_convert.hip", "i8_gemm.hip", "i8_rows.hip", "i8_tile.hip", "i8_grad.hip")
 ARCH = "gfx950"
 HOST_SOURCE = "host_gemv.cpp"
 HOST_LIB_PATH = os.path.join(PKG_DIR, "libaqlm_host.so")

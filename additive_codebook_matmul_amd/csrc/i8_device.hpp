@@ -70,13 +70,14 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t m) {
   return max(a, b);
 }
 
-// What a row is quantised with. Rows whose largest magnitude A is below 2^-100
-// are taken times 2^100 first (exact), since 127 / A would overflow.
+// What a row is quantised with. Rows whose largest magnitude A is below 2^-100 or
+// from 2^100 on are taken times 2^100 or 2^-100 first (exact for all that does not
+// round to 0), since 127 / A or 127 A would overflow.
 struct RowScale {
   float scale;  // A / 127: what a code stands for; NaN for a row that has no number for it
   float top;    // A, times `lift`
   float inv;    // 127 / top, 0 for rows whose codes are zeros
-  float lift;   // 1 or 2^100
+  float lift;   // 1, 2^100 or 2^-100
 };
 __device__ __forceinline__ RowScale row_scale(uint32_t bits) {
   RowScale r = {0.f, 0.f, 0.f, 1.f};
@@ -85,7 +86,7 @@ __device__ __forceinline__ RowScale row_scale(uint32_t bits) {
   } else if (bits != 0u) {
     const float a = __builtin_bit_cast(float, bits);
     r.scale = a / 127.f;
-    if (a < 0x1p-100f) r.lift = 0x1p100f;
+    r.lift = a < 0x1p-100f ? 0x1p100f : a >= 0x1p100f ? 0x1p-100f : 1.f;
     r.top = a * r.lift;
     r.inv = 127.f / r.top;
   }
@@ -95,12 +96,12 @@ __device__ __forceinline__ RowScale row_scale(uint32_t bits) {
 // The code of v, exactly round-to-even of 127 v / A. t = v inv is within 2^-16 of
 // that (two roundings of 2^-24 each, at most 127), so where it lies further
 // than 2^-14 from the middle of two whole numbers the nearer one is right. Near the
-// middle m + 1/2 the products 127 v and (m + 1/2) A decide, which 64 bits hold
-// exactly (31 and 32 significant bits).
-__device__ __forceinline__ int code_near_tie(float v, const RowScale &r) {
-  const double x = 127.0 * (double)(v * r.lift);
+// middle m + 1/2 the products 127 v and (m + 1/2) A decide, which float32 holds
+// exactly for halves (18 and 19 significant bits) and float64 for float32 (31 and 32).
+template <MxType T> __device__ __forceinline__ int code_near_tie(float v, const RowScale &r) {
+  typedef std::conditional_t<T == MxType::kF32, double, float> Wide;
   const float low = __builtin_rintf((v * r.lift) * r.inv - 0.5f);
-  const double middle = ((double)low + 0.5) * (double)r.top;
+  const Wide x = (Wide)127 * (Wide)(v * r.lift), middle = ((Wide)low + (Wide)0.5) * (Wide)r.top;
   const int n = (int)low;
   return x > middle ? n + 1 : x < middle ? n : n + (n & 1);
 }
@@ -120,7 +121,7 @@ template <MxType T> __device__ __forceinline__ uint2 encode_octet(const Octet<T>
   }
   if (worst > 0.5f - 0x1p-14f) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) b[e] = (uint32_t)code_near_tie(octet_value<T>(o, e), r);
+    for (int e = 0; e < 8; ++e) b[e] = (uint32_t)code_near_tie<T>(octet_value<T>(o, e), r);
   }
   auto four = [&](int k) {
     const uint32_t lo = __builtin_amdgcn_perm(b[k + 1], b[k], 0x0C0C0400u);

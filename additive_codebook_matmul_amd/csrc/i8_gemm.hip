@@ -5,6 +5,7 @@
 // loads the 16 bytes at 64 c + 16 q of row r of W and of x for the four chunks c,
 // just what v_mfma_i32_16x16x64_i8 takes. The integer sums meet in LDS.
 #include <algorithm>
+#include <cmath>
 
 #include "i8_gemm.hpp"
 
@@ -23,9 +24,8 @@ __global__ __launch_bounds__(NW * 64) void i8_skinny_kernel(const I8Args A) {
   const uint32_t cols = (uint32_t)A.cols;
   // resources that end with the tile's last row: rows past it read zero
   const int tile_rows = __builtin_amdgcn_readfirstlane(min(16, A.rows - row0));
-  Rsrc wrs[M];
-#pragma unroll
-  for (int m = 0; m < M; ++m) wrs[m] = make_rsrc(A.w[m] + (int64_t)row0 * cols, (uint32_t)tile_rows * cols);
+  const Rsrc w0rs = make_rsrc(A.w[0] + (int64_t)row0 * cols, (uint32_t)tile_rows * cols);
+  const Rsrc w1rs = make_rsrc((GATED ? A.w[1] : A.w[0]) + (int64_t)row0 * cols, (uint32_t)tile_rows * cols);
   const Rsrc xrs = make_rsrc(A.x + (int64_t)tok0 * cols, (uint32_t)batch * cols);
 
   int4_vt acc[M][NT];
@@ -33,23 +33,38 @@ __global__ __launch_bounds__(NW * 64) void i8_skinny_kernel(const I8Args A) {
   for (int m = 0; m < M; ++m)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[m][j] = int4_vt{0, 0, 0, 0};
-  for (uint32_t k0 = 256u * wave; k0 < cols; k0 += 256u * NW) {
+  // a group of 256 inputs, loaded while the one before is multiplied
+  struct Group {
     uint4 w[M][4], x[NT][4];
+  };
+  auto load = [&](uint32_t k0, Group &g) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const uint32_t k = k0 + 64u * c + 16u * q;
       const uint32_t at = k < cols ? (uint32_t)r16 * cols + k : kMxOOB;
+      g.w[0][c] = buf_load16(w0rs, at);
+      if constexpr (GATED) g.w[M - 1][c] = buf_load16(w1rs, at);
 #pragma unroll
-      for (int m = 0; m < M; ++m) w[m][c] = buf_load16(wrs[m], at);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) x[j][c] = buf_load16(xrs, k < cols ? at + (uint32_t)(16 * j) * cols : kMxOOB);
+      for (int j = 0; j < NT; ++j) g.x[j][c] = buf_load16(xrs, k < cols ? at + (uint32_t)(16 * j) * cols : kMxOOB);
     }
+  };
+  auto products = [&](const Group &g) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[m][j] = i8_mfma16(w[m][c], x[j][c], acc[m][j]);
+        for (int j = 0; j < NT; ++j) acc[m][j] = i8_mfma16(g.w[m][c], g.x[j][c], acc[m][j]);
+  };
+  Group g0, g1;
+  uint32_t k = 256u * wave;
+  load(k, g0);
+  for (; k < cols; k += 512u * NW) {
+    load(k + 256u * NW, g1);
+    products(g0);
+    if (k + 256u * NW >= cols) break;
+    load(k + 512u * NW, g0);
+    products(g1);
   }
 #pragma unroll
   for (int m = 0; m < M; ++m)
@@ -70,14 +85,13 @@ __global__ __launch_bounds__(NW * 64) void i8_skinny_kernel(const I8Args A) {
   }
 }
 
-template <MxType T, bool GATED> hipError_t product_as(const I8Args &A, hipStream_t stream) {
-  constexpr int NW = 8;
+template <MxType T, bool GATED> hipError_t skinny_as(const I8Args &A, hipStream_t stream) {
   const unsigned tiles = (unsigned)((A.rows + 15) / 16);
   if (A.batch <= 16)
-    hipLaunchKernelGGL((i8_skinny_kernel<T, GATED, NW, 1>), dim3(tiles), dim3(NW * 64), 0, stream, A);
+    hipLaunchKernelGGL((i8_skinny_kernel<T, GATED, 8, 1>), dim3(tiles), dim3(512), 0, stream, A);
   else
-    hipLaunchKernelGGL((i8_skinny_kernel<T, GATED, NW, 4>), dim3(tiles, (unsigned)((A.batch + 63) / 64)),
-                       dim3(NW * 64), 0, stream, A);
+    hipLaunchKernelGGL((i8_skinny_kernel<T, GATED, 8, 2>), dim3(tiles, (unsigned)((A.batch + 31) / 32)), dim3(512), 0,
+                       stream, A);
   return hipGetLastError();
 }
 
@@ -85,18 +99,48 @@ template <MxType T, bool GATED> hipError_t product_as(const I8Args &A, hipStream
 int64_t codes_at(int64_t batch) { return (batch * 4 + 255) / 256 * 256; }
 int64_t product_at(const I8Desc &W, int64_t batch) { return codes_at(batch) + (batch * W.cols + 255) / 256 * 256; }
 
-bool tiles_pay(const I8Desc &, bool, int64_t batch) { return batch > 32; }
+// Where whole-row wavefronts are the faster: up to four tokens, and up to eight for a
+// gated block, which gives them twice the rows (with the tokens' quantisation, four
+// tokens of 4096 x 4096 8.3 us against 9.8 of the better of the others, of 28672 x 8192
+// gated 82 and 94; eight of 1376 x 4096 gated 10.6 and 12.4, but of 4096 x 4096 11.7
+// and 10.0, of 4096 x 11008 19.6 and 16.7).
+bool rows_pay(const I8Desc &, bool gated, int64_t batch) { return batch <= (gated ? 8 : 4); }
+
+// Whether they also quantise x, every workgroup again, rather than a launch of its
+// own: one or two tokens (one of 4096 x 4096 5.2 us against 8.7, of 11008 x 4096 gated
+// 16.5 and 19.3), and four where the rows are few (4096 x 4096 8.3 and 10.1, 1376 x
+// 4096 gated 7.8 and 8.9, but 11008 x 4096 gated 26 and 22).
+bool quant_pays(const I8Desc &W, bool gated, int64_t batch) {
+  return rows_pay(W, gated, batch) && i8_rows_quantize(W.cols, batch) &&
+         (batch <= 2 || W.rows * (gated ? 2 : 1) <= 8192);
+}
+
+// Of the others, where the tile kernels are the faster: the skinny one takes 0.95 us
+// and 0.054 us a token for each turn of its wavefronts, or, with many rows, 1.6 us and
+// 0.062 us a token for a turn of 256 workgroups (fitted as the tiles: 16 x 4096 x 4096
+// 7.2 us against 9.5, 16 x 11008 x 4096 15.8 and 13.3, 32 x 1024 x 8192 13.3 and 8.5).
+bool tiles_pay(const I8Desc &W, bool gated, int64_t batch) {
+  if (batch > 64) return true;
+  const double turns = (double)((W.cols + 2047) / 2048), tok_tiles = (double)((batch + 31) / 32);
+  const double tiles = (double)((W.rows + 15) / 16) * (gated ? 2 : 1) * tok_tiles;
+  const double b = (double)std::min<int64_t>(batch, 32);
+  const double alone = turns * (0.95 + 0.054 * b), full = tiles * turns / 256.0 * (1.6 + 0.062 * b);
+  const double us = 2.6 + std::cbrt(alone * alone * alone + full * full * full);
+  return i8_tile_us(W.rows, W.cols, gated, batch) < us;
+}
 
 }  // namespace
 
 int64_t i8_product_ws_bytes(const I8Desc &W, bool gated, int64_t batch, bool quant) {
+  if (quant && quant_pays(W, gated, batch)) return 0;
   return (quant ? product_at(W, batch) : 0) +
-         (tiles_pay(W, gated, batch) ? i8_tile_ws_bytes(W.rows, W.cols, gated, batch) : 0);
+         (!rows_pay(W, gated, batch) && tiles_pay(W, gated, batch) ? i8_tile_ws_bytes(W.rows, W.cols, gated, batch) : 0);
 }
 
 hipError_t launch_i8_product(const I8Product &p, void *ws, hipStream_t stream) {
   I8Args A = {{p.W.codes, p.up.codes}, {p.W.scales, p.up.scales}, p.xcodes, p.xscales,
               static_cast<uint16_t *>(p.y), p.g, p.u, (int)p.W.rows, (int)p.W.cols, (int)p.batch, p.act};
+  if (p.x && quant_pays(p.W, p.gated(), p.batch)) return launch_i8_rows(A, p.x, p.type, p.gated(), stream);
   if (p.x) {
     float *scales = static_cast<float *>(ws);
     int8_t *codes = static_cast<int8_t *>(ws) + codes_at(p.batch);
@@ -106,10 +150,11 @@ hipError_t launch_i8_product(const I8Product &p, void *ws, hipStream_t stream) {
     A.xs = scales;
     ws = static_cast<uint8_t *>(ws) + product_at(p.W, p.batch);
   }
+  if (rows_pay(p.W, p.gated(), p.batch)) return launch_i8_rows(A, nullptr, p.type, p.gated(), stream);
   if (tiles_pay(p.W, p.gated(), p.batch)) return launch_i8_tile(A, p.type, p.gated(), ws, stream);
   if (p.type == MxType::kF16)
-    return p.gated() ? product_as<MxType::kF16, true>(A, stream) : product_as<MxType::kF16, false>(A, stream);
-  return p.gated() ? product_as<MxType::kBF16, true>(A, stream) : product_as<MxType::kBF16, false>(A, stream);
+    return p.gated() ? skinny_as<MxType::kF16, true>(A, stream) : skinny_as<MxType::kF16, false>(A, stream);
+  return p.gated() ? skinny_as<MxType::kBF16, true>(A, stream) : skinny_as<MxType::kBF16, false>(A, stream);
 }
 
 }  // namespace aqlm

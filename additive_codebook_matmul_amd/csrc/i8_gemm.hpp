@@ -44,6 +44,12 @@ __device__ __forceinline__ void i8_store4(const I8Args &A, int tok, int row, con
   store4<T>(A.y + at, row, A.rows, float4_t{out[0], out[1], out[2], out[3]}, (A.rows & 3) == 0);
 }
 
+// Up to eight tokens by whole rows of W (i8_rows.hip); x: halves to be quantised on
+// the way, for sizes that i8_rows_quantize takes, or null where A.x and A.xs are given.
+constexpr int kI8RowTokens = 8;
+bool i8_rows_quantize(int64_t cols, int64_t batch);
+hipError_t launch_i8_rows(const I8Args &A, const void *x, MxType type, bool gated, hipStream_t stream);
+
 // The tile kernels (i8_tile.hip): modelled duration in us, workspace, launch.
 double i8_tile_us(int64_t rows, int64_t cols, bool gated, int64_t batch);
 int64_t i8_tile_ws_bytes(int64_t rows, int64_t cols, bool gated, int64_t batch);

@@ -12,6 +12,7 @@
 //   * GATED: of a wavefront's 32 RT rows the first half are the gate's, the second
 //     the same ones of up, so that both products of a result meet in a lane.
 #include <algorithm>
+#include <cmath>
 
 #include "i8_gemm.hpp"
 #include "mx_tile.hpp"
@@ -99,10 +100,11 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
 
   // Step t into a stage. One load of a wavefront fills 1 KiB, eight rows, in lane
   // order, so a chunk's place in its row is chosen by where the lane reads from
-  // (the same chunk jb in all of a lane's loads, whose rows are even multiples of
-  // eight apart). Wavefront w of the share makes loads w, w + kWaves, .. of each side.
+  // (chunk jb, or jb ^ 4 in every other one of a lane's loads where those are an odd
+  // number of eights apart). Wavefront w of the share makes loads w, w + kWaves, ..
+  // of each side.
   constexpr int kWLoads = S::kRows / 8 / kWaves, kXLoads = S::kToks / 8 / kWaves;
-  static_assert(S::kRows % (8 * kWaves) == 0 && S::kToks % (8 * kWaves) == 0 && kWaves % 2 == 0, "loads");
+  static_assert(S::kRows % (8 * kWaves) == 0 && S::kToks % (8 * kWaves) == 0, "loads");
   static_assert(kWLoads <= 8 && kXLoads <= 8, "places of a lane's loads");
   uint32_t woff[8], xoff[8];
   const int8_t *wfrom[8];
@@ -118,22 +120,23 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
       row = r8 / (32 * RT) * (16 * RT) + in % (16 * RT);
     }
     wfrom[i] = of + (int64_t)row0 * cols;
-    woff[i] = (uint32_t)(row + lr) * cols + 16u * jb;
+    woff[i] = (uint32_t)(row + lr) * cols + 16u * (jb ^ (4 * (i * kWaves & 1)));
   }
 #pragma unroll
-  for (int i = 0; i < kXLoads; ++i) xoff[i] = (uint32_t)(8 * (wave + i * kWaves) + lr) * cols + 16u * jb;
+  for (int i = 0; i < kXLoads; ++i) xoff[i] = (uint32_t)(8 * (wave + i * kWaves) + lr) * cols + 16u * (jb ^ (4 * (i * kWaves & 1)));
   typedef __attribute__((address_space(3))) void *LdsPtr;
   auto fill = [&](int t, uint8_t *a) __attribute__((always_inline)) {
-    const uint32_t k = ((t < g1) & (128 * t + 16 * jb < A.cols)) ? (uint32_t)t * 128u : kMxOOB;
+    const uint32_t k0 = ((t < g1) & (128 * t + 16 * jb < A.cols)) ? (uint32_t)t * 128u : kMxOOB;
+    const uint32_t k1 = ((t < g1) & (128 * t + 16 * (jb ^ 4) < A.cols)) ? (uint32_t)t * 128u : kMxOOB;
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wfrom[i], (uint32_t)tile_rows * cols), (LdsPtr)(a + (kw * kStage + (wave + i * kWaves) * 1024)), 16,
-                                               woff[i] + k, 0, 0, 0);
+                                               woff[i] + (i * kWaves & 1 ? k1 : k0), 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs,
                                                (LdsPtr)(a + (kw * kStage + kWBytes + (wave + i * kWaves) * 1024)), 16,
-                                               xoff[i] + k, 0, 0, 0);
+                                               xoff[i] + (i * kWaves & 1 ? k1 : k0), 0, 0, 0);
   };
 
   // (places of the lane's operands in a stage: 32 rows further on the
@@ -392,17 +395,31 @@ typedef Shape<4, 2, 2, 4, 1, 2> Large;    // 256 rows x 256 tokens
 typedef Shape<2, 3, 4, 2, 1, 2> Wide;     // 256 x 192
 typedef Shape<2, 2, 4, 2, 1, 3> Middle;   // 256 x 128
 typedef Shape<2, 2, 2, 1, 2, 3> Small;    // 128 x 64
-typedef Shape<2, 1, 2, 1, 2, 3> Least;    // 128 x 32
+typedef Shape<2, 1, 2, 1, 2, 3> Slim;     // 128 x 32
+typedef Shape<2, 1, 1, 1, 2, 3> Least;    // 64 x 32, two workgroups to a CU
 
+// Tile of a product and the workgroups K is split over: the choice with the
+// shortest modelled time. The grid runs in rounds of as many workgroups as the chip
+// holds (`slots`); a round takes f us, and a + b * (its share of the slots) us for
+// each step of a share of K. That, the reading of W at 5.3 TB/s and the products at
+// 2.04 POP/s, where the power limit holds the clock, are joined as a cube root of
+// cubes, 2.6 us pass around them, and a split launches a second kernel and writes and
+// reads its sums at 5.8 TB/s. Fitted to eight layers (1024 x 8192 to 22016 x 4096, 8192
+// x 28672) from 9 to 2048 tokens, each shape and split measured at each, within 7 %
+// at the median; the choice costs 2 % on average against the best one. (64 x 8192 x
+// 28672: the six take 116, 97, 57, 50, 59 and 62 us with their best splits; 2048 x 4096
+// x 11008 117, 96, 91, 163, 193 and 226.)
 struct I8ShapeCost {
   int rows, toks, kw, sums;  // sums: bytes of a workgroup's in the workspace
-  double a, b;
+  int slots;
+  double f, a, b;
 };
-template <class S> constexpr I8ShapeCost cost_of(double a, double b) {
-  return {S::kRows, S::kToks, S::KW, S::kSums, a, b};
+template <class S> constexpr I8ShapeCost cost_of(double f, double a, double b) {
+  return {S::kRows, S::kToks, S::KW, S::kSums, 256 * (160 * 1024 / (S::STAGES * S::KW * S::kStage)), f, a, b};
 }
-constexpr I8ShapeCost kCosts[] = {cost_of<Large>(0.3, 0.9), cost_of<Wide>(0.3, 0.7), cost_of<Middle>(0.3, 0.5), cost_of<Small>(0.3, 0.3),
-                                  cost_of<Least>(0.25, 0.25)};
+constexpr I8ShapeCost kCosts[] = {cost_of<Large>(1.37, 1.275, 0.0),    cost_of<Wide>(0.66, 1.112, 0.189),
+                                  cost_of<Middle>(2.11, 0.670, 0.235), cost_of<Small>(3.04, 0.782, 0.232),
+                                  cost_of<Slim>(2.02, 0.515, 0.179),   cost_of<Least>(2.03, 0.338, 0.380)};
 
 struct I8Plan {
   int shape, splits, steps_per_split;
@@ -416,7 +433,10 @@ struct I8Plan {
 I8Plan plan_of(int64_t rows, int64_t cols, bool gated, int64_t batch) {
   I8Plan best{};
   const int64_t steps = (cols + 127) / 128;
-  for (int c = 0; c < 5; ++c) {
+  const double all_rows = (double)rows * (gated ? 2 : 1);
+  const double read = all_rows * (double)cols / 5.3e6, power = 2.0 * all_rows * (double)cols * (double)batch / 2.04e9;
+  const double bounds = read * read * read + power * power * power;
+  for (int c = 0; c < (int)(sizeof(kCosts) / sizeof(kCosts[0])); ++c) {
     const I8ShapeCost &k = kCosts[c];
     I8Plan p{};
     p.shape = c;
@@ -427,13 +447,13 @@ I8Plan plan_of(int64_t rows, int64_t cols, bool gated, int64_t batch) {
     for (int s = 1; s <= 8; ++s) {
       p.steps_per_split = (int)((steps + s - 1) / s);
       p.splits = (int)((steps + p.steps_per_split - 1) / p.steps_per_split);
-      if (p.splits != s || (s > 1 && tiles * s > 256)) break;
-      const double whole = (double)(tiles * s / 256), rest = (double)(tiles * s % 256) / 256.0;
-      const double one = whole * (k.a + k.b) + (rest > 0 ? k.a + k.b * rest : 0.0);
-      double us = 2.7 + (double)((p.steps_per_split + k.kw - 1) / k.kw) * one;
-      if (s > 1) us += 2.3 + (double)p.ws_bytes() * 2.0 / 4e6;
-      p.us = us;
-      if (best.splits == 0 || us < best.us) best = p;
+      if (p.splits != s || (s > 1 && tiles * s > k.slots)) break;
+      const double whole = (double)(tiles * s / k.slots), rest = (double)(tiles * s % k.slots) / (double)k.slots;
+      const double turns = (double)((p.steps_per_split + k.kw - 1) / k.kw);
+      const double us = whole * (k.f + turns * (k.a + k.b)) + (rest > 0 ? k.f + turns * (k.a + k.b * rest) : 0.0);
+      p.us = 2.6 + std::cbrt(us * us * us + bounds);
+      if (s > 1) p.us += 1.4 + (double)p.ws_bytes() * 2.0 / 5.8e6;
+      if (best.splits == 0 || p.us < best.us) best = p;
     }
   }
   return best;
@@ -453,6 +473,7 @@ template <MxType T, bool GATED> hipError_t tile_as(int shape, const I8TileArgs &
   if (shape == 1) return launch_shape<T, GATED, Wide>(B, stream);
   if (shape == 2) return launch_shape<T, GATED, Middle>(B, stream);
   if (shape == 3) return launch_shape<T, GATED, Small>(B, stream);
+  if (shape == 4) return launch_shape<T, GATED, Slim>(B, stream);
   return launch_shape<T, GATED, Least>(B, stream);
 }
 
