@@ -136,15 +136,35 @@ template <MxType T> __device__ __forceinline__ uint2 encode_octet(const Octet<T>
 // result is not.
 __device__ __forceinline__ float i8_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
+// e^(t^2) erfc(t) for t >= 0, within 6 * 2^-24 of itself: y P(y) with y = 1 / (1 +
+// t / 2), P of degree 8 fitted to the quotient at 400 Chebyshev points of y by least
+// squares, weighted anew until the largest relative errors were alike (4.4e-8 before
+// float32). Keeps its precision far out, where 1 + erf has none, in a fifth of the
+// instructions of erfcf.
+__device__ __forceinline__ float scaled_erfc(float t) {
+  const float y = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, t, 1.f));
+  float p = -0.059386909f;
+  p = __builtin_fmaf(p, y, 0.286126167f);
+  p = __builtin_fmaf(p, y, -0.490410924f);
+  p = __builtin_fmaf(p, y, 0.28173852f);
+  p = __builtin_fmaf(p, y, -0.0291521549f);
+  p = __builtin_fmaf(p, y, 0.203754067f);
+  p = __builtin_fmaf(p, y, 0.242834732f);
+  p = __builtin_fmaf(p, y, 0.282412142f);
+  return __builtin_fmaf(p, y, 0.282084316f) * y;
+}
+
 __device__ __forceinline__ void act_and_slope(I8Act act, float g, float &a, float &slope) {
   if (act == I8Act::kSilu) {
     const float s = i8_sigmoid(g);
     a = g * s;
     slope = s * (1.f + g * (1.f - s));
-  } else if (act == I8Act::kGelu) {
-    const float phi = 0.5f * erfcf(g * -0.70710678f);
+  } else if (act == I8Act::kGelu) {  // Phi(g) = erfc(-g / sqrt 2) / 2
+    const float e = __expf(-0.5f * g * g);
+    const float tail = 0.5f * e * scaled_erfc(0.70710678f * __builtin_fabsf(g));
+    const float phi = g < 0.f ? tail : 1.f - tail;
     a = g * phi;
-    slope = phi + g * (0.39894228f * __expf(-0.5f * g * g));
+    slope = phi + g * (0.39894228f * e);
   } else {
     const float k = 1.59576912f, c = 0.044715f;  // 2 sqrt(2 / pi)
     const float s = i8_sigmoid(k * (g + c * g * g * g));

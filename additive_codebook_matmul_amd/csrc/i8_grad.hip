@@ -10,6 +10,7 @@
 // of the value is the only one before the last (bfloat16 gradients times float32
 // scales would lose 2^-9 in bfloat16).
 #include <algorithm>
+#include <cmath>
 
 #include "i8_device.hpp"
 #include "mx_tile.hpp"
@@ -206,6 +207,11 @@ template <int RT_, int NT_, int RW_, int TW_, int KW_, int STAGES_> struct Shape
   static constexpr int kCols = 32 * RT * RW, kToks = 32 * NT * TW;
   static constexpr int kWBytes = 64 * kCols, kStage = kWBytes + kToks * 128;
   static constexpr int kSums = kCols * kToks * 4;
+  // LDS bytes of a stage's array: the stage, the shares' sums in the first one, the
+  // results in the second (and third: half of the wavefronts each)
+  static constexpr int kStore = RT * 2048;  // a wavefront's results
+  static constexpr int kArray = std::max({KW * kStage, KW > 1 ? kSums : 0, kWaves * kStore / (STAGES > 2 ? 2 : 1)});
+  static constexpr int kSlots = 256 * (160 * 1024 / (STAGES * kArray));  // workgroups the chip holds
 };
 
 // Where chunk c of row r of the codes lies: c ^ turn.
@@ -231,9 +237,7 @@ template <MxType T, class S>
 __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8GradArgs A) {
   constexpr int RT = S::RT, NT = S::NT, TW = S::TW, KW = S::KW, kWaves = S::kWaves, kCols = S::kCols;
   constexpr int kStage = S::kStage, kWBytes = S::kWBytes;
-  constexpr int kArray = KW * kStage > (KW > 1 ? S::kSums : 0) ? KW * kStage : S::kSums;
-  constexpr int kStore = RT * 2048;  // of LDS a wavefront, for its results
-  static_assert(kArray >= kWaves * kStore, "room for the results");
+  constexpr int kArray = S::kArray;
   // one array per stage: the compiler then knows which loads into LDS a read
   // of LDS can depend on
   __shared__ __attribute__((aligned(16))) uint8_t s0[kArray], s1[kArray], s2[S::STAGES > 2 ? kArray : 16];
@@ -468,7 +472,8 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
   // pass through LDS, 32 tokens at a time, from where neighbouring lanes store a
   // token's columns (a multiple of 16).
   constexpr int kChunks = 4 * RT;  // of 16 bytes, eight columns, for a token
-  uint8_t *const mine = s1 + wave * kStore;
+  uint8_t *const mine = S::STAGES == 2 ? s1 + wave * S::kStore
+                                       : (wave & 1 ? s2 : s1) + (wave >> 1) * S::kStore;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -522,20 +527,32 @@ __global__ __launch_bounds__(S::kThreads) void i8_grad_sum_kernel(const I8GradAr
 }
 
 typedef Shape<2, 2, 4, 2, 1, 3> Large;   // 256 columns x 128 tokens
-typedef Shape<2, 2, 2, 1, 2, 3> Middle;  // 128 x 64
+typedef Shape<2, 1, 4, 2, 1, 3> Half;    // 256 x 64
+typedef Shape<2, 2, 2, 1, 2, 2> Middle;  // 128 x 64
 typedef Shape<2, 1, 2, 1, 2, 3> Small;   // 128 x 32
 
+// Tile of a product and the workgroups K is split over, chosen as for the int8
+// products (i8_tile.hip): reading at 5.3 TB/s, products at 1.2 PFLOP/s, sums of splits
+// at 4.2 TB/s. Fitted to eight layers from 1 to 2048 tokens, each shape and split
+// measured at each, within 4 % at the median; the choice costs 2 % on average against
+// the best one.
+// (Each shape with its best splits, Large to Small: 301 x 4096 x 11008 60, 49, 48 and 62
+// us, 2048 x 11008 x 4096 203, 241, 256, 331, 333 x 1376 x 4096 24, 20, 17, 17, 1 x
+// 28672 x 8192 60, 51, 57, 56.)
 struct GradCost {
   int cols, toks, kw, sums;  // sums: bytes of a workgroup's in the workspace
-  double a, b;
+  int slots;                 // workgroups the chip holds at a time
+  double f, a, b;
 };
-template <class S> constexpr GradCost cost_of(double a, double b) { return {S::kCols, S::kToks, S::KW, S::kSums, a, b}; }
-constexpr GradCost kCosts[] = {cost_of<Large>(0.3, 0.5), cost_of<Middle>(0.3, 0.3), cost_of<Small>(0.25, 0.25)};
+template <class S> constexpr GradCost cost_of(double f, double a, double b) {
+  return {S::kCols, S::kToks, S::KW, S::kSums, S::kSlots, f, a, b};
+}
+constexpr GradCost kCosts[] = {cost_of<Large>(1.94, 0.708, 0.0), cost_of<Half>(1.97, 0.517, 0.332),
+                               cost_of<Middle>(1.91, 0.839, 0.344), cost_of<Small>(1.98, 0.486, 0.424)};
 
 struct GradPlan {
   int shape, splits, steps_per_split;
   int64_t col_tiles, tok_tiles;
-  double us;
   int64_t ws_bytes() const {
     return splits == 1 ? 0 : col_tiles * tok_tiles * splits * (int64_t)kCosts[shape].sums;
   }
@@ -543,8 +560,12 @@ struct GradPlan {
 
 GradPlan plan_of(const I8Desc &W, bool gated, int64_t batch) {
   GradPlan best{};
+  double best_us = 0.0;
   const int64_t steps = (W.rows + 63) / 64 * (gated ? 2 : 1);
-  for (int c = 0; c < 3; ++c) {
+  const double codes = (double)W.rows * (gated ? 2 : 1) * (double)W.cols;
+  const double read = codes / 5.3e6, power = 2.0 * codes * (double)batch / 1.2e9;
+  const double bounds = read * read * read + power * power * power;
+  for (int c = 0; c < (int)(sizeof(kCosts) / sizeof(kCosts[0])); ++c) {
     const GradCost &k = kCosts[c];
     GradPlan p{};
     p.shape = c;
@@ -554,13 +575,16 @@ GradPlan plan_of(const I8Desc &W, bool gated, int64_t batch) {
     for (int s = 1; s <= 8; ++s) {
       p.steps_per_split = (int)((steps + s - 1) / s);
       p.splits = (int)((steps + p.steps_per_split - 1) / p.steps_per_split);
-      if (p.splits != s || (s > 1 && tiles * s > 256)) break;
-      const double whole = (double)(tiles * s / 256), rest = (double)(tiles * s % 256) / 256.0;
-      const double one = whole * (k.a + k.b) + (rest > 0 ? k.a + k.b * rest : 0.0);
-      double us = 2.7 + (double)((p.steps_per_split + k.kw - 1) / k.kw) * one;
-      if (s > 1) us += 2.3 + (double)p.ws_bytes() * 2.0 / 4e6;
-      p.us = us;
-      if (best.splits == 0 || us < best.us) best = p;
+      if (p.splits != s || (s > 1 && tiles * s > 512)) break;
+      const double whole = (double)(tiles * s / k.slots), rest = (double)(tiles * s % k.slots) / (double)k.slots;
+      const double turns = (double)((p.steps_per_split + k.kw - 1) / k.kw);
+      const double tile_us = whole * (k.f + turns * (k.a + k.b)) + (rest > 0 ? k.f + turns * (k.a + k.b * rest) : 0.0);
+      double us = std::cbrt(tile_us * tile_us * tile_us + bounds);
+      if (s > 1) us += 1.8 + (double)p.ws_bytes() * 2.0 / 4.2e6;
+      if (best.splits == 0 || us < best_us) {
+        best = p;
+        best_us = us;
+      }
     }
   }
   return best;
@@ -595,7 +619,8 @@ template <MxType T> hipError_t grad_as(const I8Grad &p, void *ws, hipStream_t st
                         (int)p.W.cols, (int)p.batch, p.gated() ? 2 : 1, (int)g.col_tiles, (int)g.tok_tiles, g.splits,
                         g.steps_per_split};
   if (g.shape == 0) return launch_shape<T, Large>(A, stream);
-  if (g.shape == 1) return launch_shape<T, Middle>(A, stream);
+  if (g.shape == 1) return launch_shape<T, Half>(A, stream);
+  if (g.shape == 2) return launch_shape<T, Middle>(A, stream);
   return launch_shape<T, Small>(A, stream);
 }
 

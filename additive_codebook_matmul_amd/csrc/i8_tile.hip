@@ -44,7 +44,9 @@ template <int RT_, int NT_, int RW_, int TW_, int KW_, int STAGES_> struct Shape
   static constexpr int kSums = kRows * kToks * 4;
 };
 
-template <MxType T, bool GATED, class S>
+// ONCE: the tile's rows are read by this workgroup alone (one tile of tokens), past
+// the caches.
+template <MxType T, bool GATED, class S, bool ONCE>
 __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8TileArgs B) {
   constexpr int RT = S::RT, NT = S::NT, TW = S::TW, KW = S::KW, kWaves = S::kWaves;
   constexpr int kStage = S::kStage, kWBytes = S::kWBytes;
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wfrom[i], (uint32_t)tile_rows * cols), (LdsPtr)(a + (kw * kStage + (wave + i * kWaves) * 1024)), 16,
-                                               woff[i] + (i * kWaves & 1 ? k1 : k0), 0, 0, 0);
+                                               woff[i] + (i * kWaves & 1 ? k1 : k0), 0, 0, ONCE ? 2 : 0);
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs,
@@ -208,8 +210,8 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
   asm volatile("s_waitcnt vmcnt(%0)" : : "i"((S::STAGES - 2) * (kWLoads + kXLoads)) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" : : : "memory");
-  // (whole turns of the stages: with a way out after each step the compiler may keep
-  // the sums in two sets of registers and move them)
+  // (whole turns of the stages: with a way out after each step the compiler keeps
+  // the sums in two sets of registers and moves them)
   int g = g0;
   for (; g + S::STAGES <= gend; g += S::STAGES) {
     step(g, s0, S::STAGES > 2 ? s2 : s1);
@@ -394,6 +396,7 @@ __global__ __launch_bounds__(S::kThreads) void i8_tile_sum_kernel(const I8TileAr
 typedef Shape<4, 2, 2, 4, 1, 2> Large;    // 256 rows x 256 tokens
 typedef Shape<2, 3, 4, 2, 1, 2> Wide;     // 256 x 192
 typedef Shape<2, 2, 4, 2, 1, 3> Middle;   // 256 x 128
+typedef Shape<2, 1, 4, 2, 1, 3> Half;     // 256 x 64
 typedef Shape<2, 2, 2, 1, 2, 3> Small;    // 128 x 64
 typedef Shape<2, 1, 2, 1, 2, 3> Slim;     // 128 x 32
 typedef Shape<2, 1, 1, 1, 2, 3> Least;    // 64 x 32, two workgroups to a CU
@@ -402,13 +405,14 @@ typedef Shape<2, 1, 1, 1, 2, 3> Least;    // 64 x 32, two workgroups to a CU
 // shortest modelled time. The grid runs in rounds of as many workgroups as the chip
 // holds (`slots`); a round takes f us, and a + b * (its share of the slots) us for
 // each step of a share of K. That, the reading of W at 5.3 TB/s and the products at
-// 2.04 POP/s, where the power limit holds the clock, are joined as a cube root of
-// cubes, 2.6 us pass around them, and a split launches a second kernel and writes and
-// reads its sums at 5.8 TB/s. Fitted to eight layers (1024 x 8192 to 22016 x 4096, 8192
-// x 28672) from 9 to 2048 tokens, each shape and split measured at each, within 7 %
-// at the median; the choice costs 2 % on average against the best one. (64 x 8192 x
-// 28672: the six take 116, 97, 57, 50, 59 and 62 us with their best splits; 2048 x 4096
-// x 11008 117, 96, 91, 163, 193 and 226.)
+// 2.2 POP/s, where the power limit holds the clock, are joined as a cube root of
+// cubes, 2.3 us pass around them, and a split launches a second kernel and writes and
+// reads its sums at 5.9 TB/s. Fitted to eight layers (1024 x 8192 to 22016 x 4096, 8192
+// x 28672) from 9 to 2048 tokens, each shape and split measured at each, within 6 %
+// at the median; the choice costs 2.5 % on average against the best one.
+// (Each shape with its best splits, Large to Least: 64 x 8192 x 28672 60, 58, 49, 46,
+// 47, 60 and 64 us, 301 x 11008 x 4096 43, 41, 31, 28, 40, 52, 51, 2048 x 4096 x 11008
+// 116, 123, 91, 133, 195, 251, 245, 16 x 4096 x 4096 14, 13, 11, 10.5, 12, 9.7, 8.9.)
 struct I8ShapeCost {
   int rows, toks, kw, sums;  // sums: bytes of a workgroup's in the workspace
   int slots;
@@ -417,9 +421,10 @@ struct I8ShapeCost {
 template <class S> constexpr I8ShapeCost cost_of(double f, double a, double b) {
   return {S::kRows, S::kToks, S::KW, S::kSums, 256 * (160 * 1024 / (S::STAGES * S::KW * S::kStage)), f, a, b};
 }
-constexpr I8ShapeCost kCosts[] = {cost_of<Large>(1.37, 1.275, 0.0),    cost_of<Wide>(0.66, 1.112, 0.189),
-                                  cost_of<Middle>(2.11, 0.670, 0.235), cost_of<Small>(3.04, 0.782, 0.232),
-                                  cost_of<Slim>(2.02, 0.515, 0.179),   cost_of<Least>(2.03, 0.338, 0.380)};
+constexpr I8ShapeCost kCosts[] = {cost_of<Large>(2.52, 1.276, 0.0),    cost_of<Wide>(2.0, 1.171, 0.0),
+                                  cost_of<Middle>(2.41, 0.708, 0.151), cost_of<Half>(2.14, 0.612, 0.09),
+                                  cost_of<Small>(3.2, 0.823, 0.171),   cost_of<Slim>(2.22, 0.583, 0.093),
+                                  cost_of<Least>(2.05, 0.349, 0.366)};
 
 struct I8Plan {
   int shape, splits, steps_per_split;
@@ -434,7 +439,7 @@ I8Plan plan_of(int64_t rows, int64_t cols, bool gated, int64_t batch) {
   I8Plan best{};
   const int64_t steps = (cols + 127) / 128;
   const double all_rows = (double)rows * (gated ? 2 : 1);
-  const double read = all_rows * (double)cols / 5.3e6, power = 2.0 * all_rows * (double)cols * (double)batch / 2.04e9;
+  const double read = all_rows * (double)cols / 5.3e6, power = 2.0 * all_rows * (double)cols * (double)batch / 2.2e9;
   const double bounds = read * read * read + power * power * power;
   for (int c = 0; c < (int)(sizeof(kCosts) / sizeof(kCosts[0])); ++c) {
     const I8ShapeCost &k = kCosts[c];
@@ -451,8 +456,8 @@ I8Plan plan_of(int64_t rows, int64_t cols, bool gated, int64_t batch) {
       const double whole = (double)(tiles * s / k.slots), rest = (double)(tiles * s % k.slots) / (double)k.slots;
       const double turns = (double)((p.steps_per_split + k.kw - 1) / k.kw);
       const double us = whole * (k.f + turns * (k.a + k.b)) + (rest > 0 ? k.f + turns * (k.a + k.b * rest) : 0.0);
-      p.us = 2.6 + std::cbrt(us * us * us + bounds);
-      if (s > 1) p.us += 1.4 + (double)p.ws_bytes() * 2.0 / 5.8e6;
+      p.us = 2.3 + std::cbrt(us * us * us + bounds);
+      if (s > 1) p.us += 1.7 + (double)p.ws_bytes() * 2.0 / 5.9e6;
       if (best.splits == 0 || p.us < best.us) best = p;
     }
   }
@@ -461,7 +466,10 @@ I8Plan plan_of(int64_t rows, int64_t cols, bool gated, int64_t batch) {
 
 template <MxType T, bool GATED, class S> hipError_t launch_shape(const I8TileArgs &B, hipStream_t stream) {
   const unsigned tiles = (unsigned)(B.row_tiles * B.tok_tiles);
-  hipLaunchKernelGGL((i8_tile_kernel<T, GATED, S>), dim3(tiles * B.splits), dim3(S::kThreads * S::KW), 0, stream, B);
+  const dim3 grid(tiles * B.splits), block(S::kThreads * S::KW);
+  // (19 tokens of 28672 x 8192 gated 97 us through the caches, 87 past them)
+  if (B.tok_tiles == 1) hipLaunchKernelGGL((i8_tile_kernel<T, GATED, S, true>), grid, block, 0, stream, B);
+  else hipLaunchKernelGGL((i8_tile_kernel<T, GATED, S, false>), grid, block, 0, stream, B);
   if (B.splits > 1)
     hipLaunchKernelGGL((i8_tile_sum_kernel<T, GATED, S>), dim3(tiles * (S::RT / (GATED ? 2 : 1)) * S::NT * 4),
                        dim3(S::kThreads), 0, stream, B);
@@ -472,8 +480,9 @@ template <MxType T, bool GATED> hipError_t tile_as(int shape, const I8TileArgs &
   if (shape == 0) return launch_shape<T, GATED, Large>(B, stream);
   if (shape == 1) return launch_shape<T, GATED, Wide>(B, stream);
   if (shape == 2) return launch_shape<T, GATED, Middle>(B, stream);
-  if (shape == 3) return launch_shape<T, GATED, Small>(B, stream);
-  if (shape == 4) return launch_shape<T, GATED, Slim>(B, stream);
+  if (shape == 3) return launch_shape<T, GATED, Half>(B, stream);
+  if (shape == 4) return launch_shape<T, GATED, Small>(B, stream);
+  if (shape == 5) return launch_shape<T, GATED, Slim>(B, stream);
   return launch_shape<T, GATED, Least>(B, stream);
 }
 
