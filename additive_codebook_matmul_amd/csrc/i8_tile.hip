@@ -127,9 +127,20 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
 #pragma unroll
   for (int i = 0; i < kXLoads; ++i) xoff[i] = (uint32_t)(8 * (wave + i * kWaves) + lr) * cols + 16u * (jb ^ (4 * (i * kWaves & 1)));
   typedef __attribute__((address_space(3))) void *LdsPtr;
-  auto fill = [&](int t, uint8_t *a) __attribute__((always_inline)) {
-    const uint32_t k0 = ((t < g1) & (128 * t + 16 * jb < A.cols)) ? (uint32_t)t * 128u : kMxOOB;
-    const uint32_t k1 = ((t < g1) & (128 * t + 16 * (jb ^ 4) < A.cols)) ? (uint32_t)t * 128u : kMxOOB;
+  // ONCE: each row of tiles begins elsewhere in its share of K (whole numbers: any
+  // order gives the same sum). Rows of W are often a power of two apart, and so may the
+  // two matrices be: workgroups at the same place of K then ask the same channels of
+  // memory (19 tokens of 28672 x 8192 gated 101 us, or 90 with other addresses, and
+  // 72 this way).
+  const int shift = ONCE && g1 > g0 ? __builtin_amdgcn_readfirstlane(at.row_tile % (g1 - g0)) : 0;
+  auto fill = [&](int step_t, uint8_t *a) __attribute__((always_inline)) {
+    int t = step_t;
+    if constexpr (ONCE) {
+      t += shift;
+      if (t >= g1) t -= g1 - g0;
+    }
+    const uint32_t k0 = ((step_t < g1) & (128 * t + 16 * jb < A.cols)) ? (uint32_t)t * 128u : kMxOOB;
+    const uint32_t k1 = ((step_t < g1) & (128 * t + 16 * (jb ^ 4) < A.cols)) ? (uint32_t)t * 128u : kMxOOB;
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(wfrom[i], (uint32_t)tile_rows * cols), (LdsPtr)(a + (kw * kStage + (wave + i * kWaves) * 1024)), 16,
