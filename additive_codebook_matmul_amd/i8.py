@@ -225,14 +225,15 @@ class I8Layer(_Workspaces):
 
 
 class _RecordedGated(torch.autograd.Function):
-    """A gated block, and for backward its grad_input from the saved products."""
+    """A gated block, and for backward its gradient from the saved products."""
 
     @staticmethod
     def forward(ctx, block, x):
-        h, g, u = block.forward_saving(x)
+        n, step = block._saved_floats(x.shape[0])
+        saved = torch.empty(n, dtype=torch.float32, device=block.device)  # g, then u
         ctx.block = block
-        ctx.save_for_backward(g, u)
-        return h
+        ctx.save_for_backward(saved)
+        return block._run(x, None, saved.data_ptr(), saved.data_ptr() + 4 * step)
 
     @staticmethod
     @once_differentiable
@@ -240,7 +241,10 @@ class _RecordedGated(torch.autograd.Function):
         dh = dh.contiguous()
         if dh.data_ptr() % 16:  # a part of a larger gradient
             dh = dh.clone()
-        return None, ctx.block.grad_input(dh, *ctx.saved_tensors)
+        (saved,) = ctx.saved_tensors
+        block = ctx.block
+        _, step = block._saved_floats(dh.shape[0])
+        return None, block._back(dh, saved.data_ptr(), saved.data_ptr() + 4 * step, None)
 
 
 class I8Gated(_Workspaces):
@@ -258,14 +262,26 @@ class I8Gated(_Workspaces):
         self.out_features, self.in_features, self.device = gate.out_features, gate.in_features, gate.device
         super().__init__(gate._ref, up._ref)
 
-    def _run(self, x: torch.Tensor, out: Optional[torch.Tensor], g, u) -> torch.Tensor:
+    def _saved_floats(self, batch: int) -> Tuple[int, int]:
+        """(floats of g and u in one allocation, where u begins: at a multiple of 16 bytes)."""
+        step = (batch * self.out_features + 3) // 4 * 4
+        return step + batch * self.out_features, step
+
+    def _run(self, x: torch.Tensor, out: Optional[torch.Tensor], g: Optional[int], u: Optional[int]) -> torch.Tensor:
         batch = x.shape[0]
         h = _output(out, (batch, self.out_features), x.dtype, self.device)
         ws, ptr, need = self._workspace(batch, "gated")
         _call(self.device, _lib().aqlm_i8_gated, self.gate._ref, self.up._ref, x.data_ptr(), batch, self._act,
-              h.data_ptr(), None if g is None else g.data_ptr(), None if u is None else u.data_ptr(),
-              I8_TYPES[x.dtype], ptr, need)
+              h.data_ptr(), g, u, I8_TYPES[x.dtype], ptr, need)
         return h
+
+    def _back(self, dh: torch.Tensor, g: int, u: int, out: Optional[torch.Tensor]) -> torch.Tensor:
+        batch = dh.shape[0]
+        dx = _output(out, (batch, self.in_features), dh.dtype, self.device)
+        ws, ptr, need = self._workspace(batch, "gated_grad")
+        _call(self.device, _lib().aqlm_i8_gated_grad, self.gate._ref, self.up._ref, g, u, dh.data_ptr(), batch,
+              self._act, dx.data_ptr(), I8_TYPES[dh.dtype], ptr, need)
+        return dx
 
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """h = act(Q(x) . gate^T) * (Q(x) . up^T), x [batch, in] float16 or bfloat16."""
@@ -282,20 +298,15 @@ class I8Gated(_Workspaces):
         self._check_half(x, "x", self.in_features)
         g = torch.empty((x.shape[0], self.out_features), dtype=torch.float32, device=self.device)
         u = torch.empty_like(g)
-        return self._run(x.detach(), None, g, u), g, u
+        return self._run(x, None, g.data_ptr(), u.data_ptr()), g, u
 
     def grad_input(self, dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor,
                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """dx = (dh u act'(g)) . gate + (dh act(g)) . up: the gradient of forward(x) with respect
         to x, straight through the quantisation, from forward_saving's g and u."""
         self._check_half(dh, "dh", self.out_features)
-        batch = dh.shape[0]
         for t, what in ((g, "g"), (u, "u")):
             _check_dense(t, what, _FLOAT, dh.shape)
             if t.device != self.device:
                 raise ValueError(f"{what} must be on the layer's device")
-        dx = _output(out, (batch, self.in_features), dh.dtype, self.device)
-        ws, ptr, need = self._workspace(batch, "gated_grad")
-        _call(self.device, _lib().aqlm_i8_gated_grad, self.gate._ref, self.up._ref, g.data_ptr(), u.data_ptr(),
-              dh.data_ptr(), batch, self._act, dx.data_ptr(), I8_TYPES[dh.dtype], ptr, need)
-        return dx
+        return self._back(dh, g.data_ptr(), u.data_ptr(), out)
