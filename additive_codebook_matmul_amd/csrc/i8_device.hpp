@@ -56,8 +56,8 @@ template <MxType T> __device__ __forceinline__ uint32_t max_bits(uint32_t m) {
   return m;
 }
 
-// Maximum over the 64 lanes of a wavefront, in every lane.
-__device__ __forceinline__ uint32_t wave_max(uint32_t m) {
+// Maximum over each 16 lanes, in every one of them.
+__device__ __forceinline__ uint32_t row16_max(uint32_t m) {
   auto step = [&](auto ctrl) __attribute__((always_inline)) {
     m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, decltype(ctrl)::value, 0xF, 0xF, false));
   };
@@ -65,8 +65,14 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t m) {
   step(std::integral_constant<int, kDppQuadXor2>{});
   step(std::integral_constant<int, kDppRowHalfMirror>{});
   step(std::integral_constant<int, kDppRowMirror>{});
-  const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)m, 0), (uint32_t)__builtin_amdgcn_readlane((int)m, 16));
-  const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)m, 32), (uint32_t)__builtin_amdgcn_readlane((int)m, 48));
+  return m;
+}
+
+// Maximum over the 64 lanes of a wavefront, in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  const int m = (int)row16_max(v);
+  const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane(m, 0), (uint32_t)__builtin_amdgcn_readlane(m, 16));
+  const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane(m, 32), (uint32_t)__builtin_amdgcn_readlane(m, 48));
   return max(a, b);
 }
 

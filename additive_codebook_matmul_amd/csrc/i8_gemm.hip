@@ -3,7 +3,9 @@
 // i8_skinny_kernel: a workgroup computes 16 rows of W (GATED: of both matrices)
 // for 16 NT tokens. Its wavefronts share K in groups of 256 inputs: lane (r, q)
 // loads the 16 bytes at 64 c + 16 q of row r of W and of x for the four chunks c,
-// just what v_mfma_i32_16x16x64_i8 takes. The integer sums meet in LDS.
+// just what v_mfma_i32_16x16x64_i8 takes. The integer sums meet in LDS. It serves short
+// layers, where a launch and two or three round trips to memory are all there is (16 x
+// 4096 x 4096 7.2 us, 2048 x 1024 3.6).
 #include <algorithm>
 #include <cmath>
 
@@ -100,11 +102,13 @@ int64_t codes_at(int64_t batch) { return (batch * 4 + 255) / 256 * 256; }
 int64_t product_at(const I8Desc &W, int64_t batch) { return codes_at(batch) + (batch * W.cols + 255) / 256 * 256; }
 
 // Where whole-row wavefronts are the faster: up to four tokens, and up to eight for a
-// gated block, which gives them twice the rows (with the tokens' quantisation, four
-// tokens of 4096 x 4096 8.3 us against 9.8 of the better of the others, of 28672 x 8192
-// gated 82 and 94; eight of 1376 x 4096 gated 10.6 and 12.4, but of 4096 x 4096 11.7
-// and 10.0, of 4096 x 11008 19.6 and 16.7).
-bool rows_pay(const I8Desc &, bool gated, int64_t batch) { return batch <= (gated ? 8 : 4); }
+// gated block, which gives them twice the rows, of at most 4096 (with the tokens'
+// quantisation, four tokens of 4096 x 4096 8.3 us against 9.8 of the better of the
+// others, of 28672 x 8192 gated 82 and 94; eight of 1376 x 4096 gated 10.6 and 12.1,
+// but of 4096 x 4096 11.7 and 10.0, of 11008 x 4096 gated 26.6 and 23.7).
+bool rows_pay(const I8Desc &W, bool gated, int64_t batch) {
+  return batch <= 4 || (gated && batch <= kI8RowTokens && W.rows <= 4096);
+}
 
 // Whether they also quantise x, every workgroup again, rather than a launch of its
 // own: one or two tokens (one of 4096 x 4096 5.2 us against 8.7, of 11008 x 4096 gated

