@@ -11,7 +11,8 @@
 // scales would lose 2^-9 in bfloat16).
 // What bounds the product of many tokens is the card's power, as for the int8 products:
 // 2048 x 11008 x 4096 takes 182 us at first and 190 to 230, by the card, once the clock
-// has fallen (1.0 PFLOP/s; the library's product of float16 matrices 211).
+// has fallen (1.0 PFLOP/s; the matrix cores busy for 59 % of the cycles, LDS for 22; the
+// library's product of float16 matrices 211).
 #include <algorithm>
 #include <cmath>
 

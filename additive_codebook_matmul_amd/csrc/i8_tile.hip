@@ -11,12 +11,13 @@
 //     KiB from LDS for RT NT instructions of 32 cycles.
 //   * GATED: of a wavefront's 32 RT rows the first half are the gate's, the second
 //     the same ones of up, so that both products of a result meet in a lane.
-// What bounds it: with many tokens the card's power. A 256 x 256 tile's step takes 1.15
-// us where its instructions need 1.09, alone, and the matrix cores are busy for nearly
-// all of it; with every CU at work the clock falls: 2048 x 8192 x 28672 takes 322 us with
-// zeros for data, 410 to 495 with codes (2.0 to 2.35 POP/s; LDS reads take 18 % of the
-// time, no bank conflicts). 1999 x 4096 x 11008 87 us, 2048 x 11008 x 4096 gated 186.
-// With few tokens the reading of W: 19 x 28672 x 8192 gated 72 us, 6.5 TB/s.
+// What bounds it: with many tokens the card's power and the wait for a step's loads at
+// its barrier. A 256 x 256 tile's step takes 1.15 us where its instructions need 1.09,
+// alone; with every CU at work the clock falls (2048 x 8192 x 28672 takes 322 us with
+// zeros for data, 410 to 495 with codes, 2.0 to 2.35 POP/s) and the matrix cores are busy
+// for 57 % of the cycles, LDS for 24 to 30. 1999 x 4096 x 11008 takes 85 us, 2048 x 11008 x
+// 4096 gated 186. With few tokens the reading of W: 19 x 28672 x 8192 gated 72 us, 6.5
+// TB/s.
 #include <algorithm>
 #include <cmath>
 
