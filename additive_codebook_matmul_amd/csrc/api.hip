@@ -128,7 +128,7 @@ const char *aqlm_status_string(int status) {
     case AQLM_ERR_SCRATCH: return "the call needs more scratch memory than the library's static "
                                   "scratch array holds (AQLM_STATIC_SCRATCH_BYTES = 64 MiB); "
                                   "use aqlm_gemm_ws with a workspace or aqlm_gemm";
-    case AQLM_ERR_TYPE: return "unknown element type or scale rule";
+    case AQLM_ERR_TYPE: return "unknown element type, scale rule or activation";
     default: return "unknown status";
   }
 }

@@ -53,7 +53,7 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : WAVES * 64) void i8_quantize_rows
 }
 
 // Rows of up to 128 values: 16 lanes a row, an octet each (28672 x 128 8.7 us by a
-// wavefront a row, @@ this way).
+// wavefront a row, 4.8 this way).
 template <MxType T>
 __global__ __launch_bounds__(256) void i8_quantize_short_kernel(const void *__restrict__ x, uint2 *__restrict__ codes,
                                                                 float *__restrict__ scales, int octets, int64_t rows) {

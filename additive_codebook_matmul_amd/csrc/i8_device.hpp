@@ -175,7 +175,8 @@ __device__ __forceinline__ void act_and_slope(I8Act act, float g, float &a, floa
     const float k = 1.59576912f, c = 0.044715f;  // 2 sqrt(2 / pi)
     const float s = i8_sigmoid(k * (g + c * g * g * g));
     a = g * s;
-    slope = s + g * s * (1.f - s) * (k * (1.f + 3.f * c * g * g));
+    // (where g^2 passes 2^40, s (1 - s) is 0 and the polynomial may not be infinite)
+    slope = s + g * s * (1.f - s) * (k * (1.f + 3.f * c * __builtin_fminf(g * g, 0x1p40f)));
   }
 }
 

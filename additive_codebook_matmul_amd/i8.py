@@ -15,7 +15,10 @@ fallback: a missing library or a failing call raises.
     y = down.forward(h)
 
 Under autograd an x that requires a gradient gets it, straight through the
-quantisation of the activations. The weights are constants.
+quantisation of the activations. The weights are constants. (As with torch's own
+operations, a backward pass that is captured into a HIP graph must meet no eager
+graph of the same leaves that is still alive: torch then accumulates into them on
+the eager graph's stream.)
 """
 from __future__ import annotations
 

@@ -93,7 +93,8 @@ typedef enum aqlm_status {
                              *_workspace_size */
   AQLM_ERR_SCRATCH = 8,   /* aqlm_gemm_noalloc: the call needs more than
                              AQLM_STATIC_SCRATCH_BYTES of scratch memory */
-  AQLM_ERR_TYPE = 9       /* aqlm_mx.h: unknown element type or scale rule */
+  AQLM_ERR_TYPE = 9       /* unknown element type, or aqlm_mx.h: scale rule,
+                             aqlm_i8.h: activation */
 } aqlm_status;
 
 /* Size of the static device scratch array behind aqlm_gemm_noalloc (64 MiB;

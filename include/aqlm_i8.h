@@ -126,7 +126,8 @@ AQLM_API int aqlm_i8_gated(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up,
  * straight through the quantisation; dy and dx of `type` (F16 or BF16). Each
  * token's gradients times the channels' scales enter the matrix instructions as
  * float16, relative to a power of two of the token's own: 11 significant bits
- * for what lies within 2^-28 of the token's largest, whatever its magnitude.
+ * for what lies within 2^-28 of the token's largest, whatever its magnitude (the
+ * terms themselves are float32).
  * rows need not be a multiple of anything; batch == 0 is a no-op.
  */
 AQLM_API int aqlm_i8_grad_input_workspace_size(const aqlm_i8_matrix *W, int64_t batch, int64_t *bytes);

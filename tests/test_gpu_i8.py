@@ -424,3 +424,31 @@ def test_conversion_of_short_rows(rows, cols, dtype):
     i8_dequant(dev(codes), dev(scales), dtype, out=out)
     same(out, half(codes.astype(np.float32) * scales[:, None], dtype))
     ok()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_gradient_over_the_range_of_the_gate(act):
+    """act' alone (up's scales are 0), a token for each gate, so that none hides below a larger one."""
+    g1 = np.concatenate([np.linspace(-1000, 1000, 61), np.linspace(-12, 12, 121),
+                         [0, 1e-30, -1e-30, 1e6, -1e6, 1e18, -1e18, 1e25, -1e25, 3e38, -3e38, np.nan]]).astype(np.float32)
+    batch, out, n_in = len(g1), 8, 16
+    codes = np.zeros((out, n_in), np.int8)
+    codes[0, 0] = 1
+    dh = torch.zeros((batch, out), dtype=torch.bfloat16)
+    dh[:, 0] = 1.0
+    g = np.zeros((batch, out), np.float32)
+    g[:, 0] = g1
+    gate, up = (codes, np.ones(out, np.float32)), (codes, np.zeros(out, np.float32))
+    got = I8Gated(layer_of(gate), layer_of(up), act).grad_input(
+        dh.to(DEV), dev(g), dev(np.ones((batch, out), np.float32))).cpu().double().numpy()
+    plain = np.isfinite(g1)
+    with np.errstate(over="ignore", under="ignore"):
+        _, slope = IO.act(np.where(plain, g1.astype(np.float64), 0), act)
+    # the roundings to float16 and bfloat16 are 2^-11 and 2^-8 at most; e^z is off by |z| 2^-23 of
+    # itself and a few steps, with |z| at most 90 where it is not 0; act' is a sum of parts up to 1
+    # + |g| that cancel near g = -1; from 2^-120 on down float32's e^z loses bits and vanishes
+    near = np.clip(np.abs(np.where(plain, g1.astype(np.float64), 0)), 0, 14)
+    tol = np.abs(slope) * (2.0 ** -11 + 2.0 ** -8 + 128 * 2.0 ** -23) + 16 * 2.0 ** -24 * np.exp2(-near) + 2.0 ** -120
+    assert (np.abs(got[:, 0] - slope) <= tol)[plain].all()
+    assert np.isnan(got[~plain, 0]).all()
+    assert (got[:, 1:][plain] == 0).all()
