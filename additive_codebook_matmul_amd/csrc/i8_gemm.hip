@@ -112,7 +112,7 @@ bool rows_pay(const I8Desc &W, bool gated, int64_t batch) {
 
 // Whether they also quantise x, every workgroup again, rather than a launch of its
 // own: one or two tokens (one of 4096 x 4096 5.2 us against 8.7, of 11008 x 4096 gated
-// 16.5 and 19.3), and four where the rows are few (4096 x 4096 8.3 and 10.1, 1376 x
+// 16.5 and 19.3, of 8192 x 28672 39 and 43, two of 4096 x 11008 12.6 and 15.3), and four where the rows are few (4096 x 4096 8.3 and 10.1, 1376 x
 // 4096 gated 7.8 and 8.9, but 11008 x 4096 gated 26 and 22).
 bool quant_pays(const I8Desc &W, bool gated, int64_t batch) {
   return rows_pay(W, gated, batch) && i8_rows_quantize(W.cols, batch) &&

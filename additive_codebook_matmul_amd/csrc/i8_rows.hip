@@ -6,10 +6,10 @@
 // gate and the same one of up, whose results meet there), its lanes 16 bytes each of
 // 1 KiB of a row, two such chunks ahead, and v_dot4_i32_i8 adds them up beside the
 // tokens' codes from LDS. The lanes' sums meet at a row's end.
-// (One token: 28672 x 8192 gated 76 us, 6.2 TB/s, 8192 x 28672 41 with the token's
-// quantisation, 5.8 TB/s, 11008 x 4096 gated 15.8, 5.7 TB/s.)
-// QUANT: x is halves, which every workgroup quantises on their way into LDS, where its
-// threads hold them in four octets each (i8_rows_quantize).
+// (One token: 28672 x 8192 gated 76 us, 6.2 TB/s, 8192 x 28672 39 with the token's
+// quantisation, 6.0 TB/s, 11008 x 4096 gated 15.8, 5.7 TB/s.)
+// HOLD > 0: x is halves, which every workgroup quantises on their way into LDS, while
+// its threads hold HOLD octets of each token (i8_rows_quantize).
 #include <algorithm>
 
 #include "i8_gemm.hpp"
@@ -46,10 +46,10 @@ __device__ __forceinline__ int lanes_sum(int v) {
   return v;
 }
 
-template <MxType T, bool GATED, int B, bool QUANT>
+template <MxType T, bool GATED, int B, int HOLD>
 __global__ __launch_bounds__(kThreads) void i8_rows_kernel(const I8Args A, const void *__restrict__ x) {
   constexpr int S = 2, kRows = GATED ? 1 : 2;  // streams, and rows of results, of a wavefront
-  constexpr int kHold = B > 4 ? 1 : 4 / B;               // octets of a token a thread keeps while it is quantised
+  constexpr bool QUANT = HOLD > 0;
   extern __shared__ __attribute__((aligned(16))) uint8_t codes[];  // [B][seg]
   __shared__ uint32_t tops[B][kWaves];
   const int seg = segment_bytes(A.cols, B);
@@ -83,12 +83,12 @@ __global__ __launch_bounds__(kThreads) void i8_rows_kernel(const I8Args A, const
 
   const int octets = A.cols >> 3;
   RowScale rs[QUANT ? B : 1];
-  Octet<T> held[QUANT ? B : 1][QUANT ? kHold : 1];
+  Octet<T> held[QUANT ? B : 1][QUANT ? HOLD : 1];
   if constexpr (QUANT) {
 #pragma unroll
     for (int b = 0; b < B; ++b)
 #pragma unroll
-      for (int u = 0; u < kHold; ++u) {
+      for (int u = 0; u < HOLD; ++u) {
         const int i = threadIdx.x + u * kThreads;
         if (i < octets) held[b][u] = load_octet<T, false>(x, (int64_t)min(b, A.batch - 1) * octets + i);
         else held[b][u] = {};
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(kThreads) void i8_rows_kernel(const I8Args A, const
     for (int b = 0; b < B; ++b) {
       uint32_t m = 0;
 #pragma unroll
-      for (int u = 0; u < kHold; ++u) m = max(m, octet_max<T>(held[b][u]));
+      for (int u = 0; u < HOLD; ++u) m = max(m, octet_max<T>(held[b][u]));
       m = wave_max(m);
       if (lane == 0) tops[b][wave] = m;
     }
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(kThreads) void i8_rows_kernel(const I8Args A, const
 #pragma unroll
       for (int b = 0; b < B; ++b)
 #pragma unroll
-        for (int u = 0; u < kHold; ++u) {
+        for (int u = 0; u < HOLD; ++u) {
           const int i = threadIdx.x + u * kThreads;
           if (i < octets) *reinterpret_cast<uint2 *>(codes + b * seg + 8 * i) = encode_octet<T>(held[b][u], rs[b]);
         }
@@ -197,10 +197,19 @@ template <MxType T, bool GATED, int B> void launch_b(const I8Args &A, const void
   const unsigned lds = (unsigned)(B * segment_bytes(A.cols, B));
   if constexpr (B <= 4)
     if (x) {
-      hipLaunchKernelGGL((i8_rows_kernel<T, GATED, B, true>), grid, dim3(kThreads), lds, stream, A, x);
-      return;
+      // (twice the octets cost registers: one token of 11008 x 4096 gated 17.2 us with
+      // four and 18.0 with eight)
+      constexpr int kHold = 4 / B;
+      if (A.cols / 8 <= kHold * kThreads) {
+        hipLaunchKernelGGL((i8_rows_kernel<T, GATED, B, kHold>), grid, dim3(kThreads), lds, stream, A, x);
+        return;
+      }
+      if constexpr (B <= 2) {
+        hipLaunchKernelGGL((i8_rows_kernel<T, GATED, B, 2 * kHold>), grid, dim3(kThreads), lds, stream, A, x);
+        return;
+      }
     }
-  hipLaunchKernelGGL((i8_rows_kernel<T, GATED, B, false>), grid, dim3(kThreads), lds, stream, A, x);
+  hipLaunchKernelGGL((i8_rows_kernel<T, GATED, B, 0>), grid, dim3(kThreads), lds, stream, A, x);
 }
 
 template <MxType T, bool GATED> hipError_t rows_as(const I8Args &A, const void *x, hipStream_t stream) {
@@ -214,8 +223,8 @@ template <MxType T, bool GATED> hipError_t rows_as(const I8Args &A, const void *
 }  // namespace
 
 bool i8_rows_quantize(int64_t cols, int64_t batch) {
-  const int64_t b = batch <= 2 ? batch : 4;
-  return batch <= 4 && cols / 8 <= 4 / b * kThreads && b * cols <= kMostLds;
+  const int64_t most = batch == 1 ? 8 : batch == 2 ? 4 : 1;  // octets of a token a thread holds
+  return batch <= 4 && cols / 8 <= most * kThreads;
 }
 
 hipError_t launch_i8_rows(const I8Args &A, const void *x, MxType type, bool gated, hipStream_t stream) {

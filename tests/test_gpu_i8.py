@@ -452,3 +452,19 @@ def test_gated_gradient_over_the_range_of_the_gate(act):
     assert (np.abs(got[:, 0] - slope) <= tol)[plain].all()
     assert np.isnan(got[~plain, 0]).all()
     assert (got[:, 1:][plain] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("batch,out,n_in", [(1, 40, 16384), (1, 37, 16400), (1, 21, 32768), (1, 20, 32784), (2, 37, 8192),
+                                            (2, 37, 8208), (2, 20, 16384), (2, 21, 16400), (3, 20, 4112)])
+def test_long_rows_of_few_tokens(batch, out, n_in, dtype):
+    """Around the lengths up to which a product's own workgroups quantise the tokens."""
+    w, up = weights(out, n_in, n_in), weights(out, n_in, n_in + 1)
+    x = activations(batch, n_in, dtype, out)
+    y, ok = guarded((batch, out), dtype)
+    layer_of(w).forward(x.to(DEV), out=y)
+    ok()
+    same(y, half(product(x, w, dtype), dtype))
+    h, g, u = I8Gated(layer_of(w), layer_of(up)).forward_saving(x.to(DEV))
+    assert np.array_equal(g.cpu().numpy(), product(x, w, dtype))
+    assert np.array_equal(u.cpu().numpy(), product(x, up, dtype))
