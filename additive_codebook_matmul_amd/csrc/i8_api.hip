@@ -96,7 +96,7 @@ int aqlm_i8_dequant(const aqlm_i8_matrix *m, int32_t type, void *W, void *stream
 
 int aqlm_i8_gemm_workspace_size(const aqlm_i8_matrix *W, int64_t batch, int64_t *bytes) {
   return workspace_size(W, nullptr, false, batch, bytes,
-                        [&](const aqlm::I8Desc &d) { return aqlm::i8_product_ws_bytes(d, false, batch, false); });
+                        [&](const aqlm::I8Desc &d) { return aqlm::i8_route(d, false, batch, false).ws_bytes; });
 }
 
 int aqlm_i8_gemm(const aqlm_i8_matrix *W, const aqlm_i8_matrix *x, void *y, int32_t type, void *workspace,
@@ -110,16 +110,17 @@ int aqlm_i8_gemm(const aqlm_i8_matrix *W, const aqlm_i8_matrix *x, void *y, int3
   if (dx.rows == 0) return AQLM_OK;
   if (!y) return AQLM_ERR_NULL;
   if (!aligned16(y)) return AQLM_ERR_ALIGN;
-  st = check_workspace(aqlm::i8_product_ws_bytes(d, false, dx.rows, false), workspace, workspace_bytes);
+  const aqlm::I8Route route = aqlm::i8_route(d, false, dx.rows, false);
+  st = check_workspace(route.ws_bytes, workspace, workspace_bytes);
   if (st != AQLM_OK) return st;
   const aqlm::I8Product p = {d, kNone, aqlm::I8Act::kSilu, nullptr, dx.codes, dx.scales, dx.rows,
                              y, nullptr, nullptr, static_cast<aqlm::MxType>(type)};
-  return from_hip(aqlm::launch_i8_product(p, workspace, static_cast<hipStream_t>(stream)));
+  return from_hip(aqlm::launch_i8_product(p, route, workspace, static_cast<hipStream_t>(stream)));
 }
 
 int aqlm_i8_gemm_quant_workspace_size(const aqlm_i8_matrix *W, int64_t batch, int64_t *bytes) {
   return workspace_size(W, nullptr, false, batch, bytes,
-                        [&](const aqlm::I8Desc &d) { return aqlm::i8_product_ws_bytes(d, false, batch, true); });
+                        [&](const aqlm::I8Desc &d) { return aqlm::i8_route(d, false, batch, true).ws_bytes; });
 }
 
 int aqlm_i8_gemm_quant(const aqlm_i8_matrix *W, const void *x, int64_t batch, void *y, int32_t type,
@@ -131,18 +132,19 @@ int aqlm_i8_gemm_quant(const aqlm_i8_matrix *W, const void *x, int64_t batch, vo
   if (!batch_ok(batch)) return AQLM_ERR_BATCH;
   if (batch == 0) return AQLM_OK;
   st = check_io(x, y);
-  if (st == AQLM_OK)
-    st = check_workspace(aqlm::i8_product_ws_bytes(d, false, batch, true), workspace, workspace_bytes);
+  if (st != AQLM_OK) return st;
+  const aqlm::I8Route route = aqlm::i8_route(d, false, batch, true);
+  st = check_workspace(route.ws_bytes, workspace, workspace_bytes);
   if (st != AQLM_OK) return st;
   const aqlm::I8Product p = {d, kNone, aqlm::I8Act::kSilu, x, nullptr, nullptr, batch,
                              y, nullptr, nullptr, static_cast<aqlm::MxType>(type)};
-  return from_hip(aqlm::launch_i8_product(p, workspace, static_cast<hipStream_t>(stream)));
+  return from_hip(aqlm::launch_i8_product(p, route, workspace, static_cast<hipStream_t>(stream)));
 }
 
 int aqlm_i8_gated_workspace_size(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, int64_t batch,
                                  int64_t *bytes) {
   return workspace_size(gate, up, true, batch, bytes,
-                        [&](const aqlm::I8Desc &d) { return aqlm::i8_product_ws_bytes(d, true, batch, true); });
+                        [&](const aqlm::I8Desc &d) { return aqlm::i8_route(d, true, batch, true).ws_bytes; });
 }
 
 int aqlm_i8_gated(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, const void *x, int64_t batch, int32_t act,
@@ -158,16 +160,19 @@ int aqlm_i8_gated(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, const vo
   if (st != AQLM_OK) return st;
   if (!g != !u) return AQLM_ERR_NULL;
   if (!aligned16(g) || !aligned16(u)) return AQLM_ERR_ALIGN;
-  st = check_workspace(aqlm::i8_product_ws_bytes(d, true, batch, true), workspace, workspace_bytes);
+  const aqlm::I8Route route = aqlm::i8_route(d, true, batch, true);
+  st = check_workspace(route.ws_bytes, workspace, workspace_bytes);
   if (st != AQLM_OK) return st;
   const aqlm::I8Product p = {d, e, static_cast<aqlm::I8Act>(act), x, nullptr, nullptr, batch,
                              h, g, u, static_cast<aqlm::MxType>(type)};
-  return from_hip(aqlm::launch_i8_product(p, workspace, static_cast<hipStream_t>(stream)));
+  return from_hip(aqlm::launch_i8_product(p, route, workspace, static_cast<hipStream_t>(stream)));
 }
 
 int aqlm_i8_grad_input_workspace_size(const aqlm_i8_matrix *W, int64_t batch, int64_t *bytes) {
   return workspace_size(W, nullptr, false, batch, bytes,
-                        [&](const aqlm::I8Desc &d) { return aqlm::i8_grad_ws_bytes(d, false, batch); });
+                        [&](const aqlm::I8Desc &d) {
+                          return aqlm::i8_grad_ws_bytes(d, false, batch, aqlm::i8_grad_plan(d, false, batch));
+                        });
 }
 
 int aqlm_i8_grad_input(const aqlm_i8_matrix *W, const void *dy, int64_t batch, void *dx, int32_t type,
@@ -179,17 +184,21 @@ int aqlm_i8_grad_input(const aqlm_i8_matrix *W, const void *dy, int64_t batch, v
   if (!batch_ok(batch)) return AQLM_ERR_BATCH;
   if (batch == 0) return AQLM_OK;
   st = check_io(dy, dx);
-  if (st == AQLM_OK) st = check_workspace(aqlm::i8_grad_ws_bytes(d, false, batch), workspace, workspace_bytes);
+  if (st != AQLM_OK) return st;
+  const aqlm::I8Plan plan = aqlm::i8_grad_plan(d, false, batch);
+  st = check_workspace(aqlm::i8_grad_ws_bytes(d, false, batch, plan), workspace, workspace_bytes);
   if (st != AQLM_OK) return st;
   const aqlm::I8Grad p = {d, kNone, aqlm::I8Act::kSilu, nullptr, nullptr, dy, batch, dx,
                           static_cast<aqlm::MxType>(type)};
-  return from_hip(aqlm::launch_i8_grad(p, workspace, static_cast<hipStream_t>(stream)));
+  return from_hip(aqlm::launch_i8_grad(p, plan, workspace, static_cast<hipStream_t>(stream)));
 }
 
 int aqlm_i8_gated_grad_workspace_size(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, int64_t batch,
                                       int64_t *bytes) {
   return workspace_size(gate, up, true, batch, bytes,
-                        [&](const aqlm::I8Desc &d) { return aqlm::i8_grad_ws_bytes(d, true, batch); });
+                        [&](const aqlm::I8Desc &d) {
+                          return aqlm::i8_grad_ws_bytes(d, true, batch, aqlm::i8_grad_plan(d, true, batch));
+                        });
 }
 
 int aqlm_i8_gated_grad(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, const float *g, const float *u,
@@ -203,11 +212,13 @@ int aqlm_i8_gated_grad(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, con
   if (batch == 0) return AQLM_OK;
   st = check_io(dh, dx);
   if (st == AQLM_OK) st = check_io(g, u);
-  if (st == AQLM_OK) st = check_workspace(aqlm::i8_grad_ws_bytes(d, true, batch), workspace, workspace_bytes);
+  if (st != AQLM_OK) return st;
+  const aqlm::I8Plan plan = aqlm::i8_grad_plan(d, true, batch);
+  st = check_workspace(aqlm::i8_grad_ws_bytes(d, true, batch, plan), workspace, workspace_bytes);
   if (st != AQLM_OK) return st;
   const aqlm::I8Grad p = {d, e, static_cast<aqlm::I8Act>(act), g, u, dh, batch, dx,
                           static_cast<aqlm::MxType>(type)};
-  return from_hip(aqlm::launch_i8_grad(p, workspace, static_cast<hipStream_t>(stream)));
+  return from_hip(aqlm::launch_i8_grad(p, plan, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -119,32 +119,37 @@ bool quant_pays(const I8Desc &W, bool gated, int64_t batch) {
          (batch <= 2 || W.rows * (gated ? 2 : 1) <= 8192);
 }
 
-// Of the others, where the tile kernels are the faster: the skinny one takes 0.95 us
-// and 0.054 us a token for each turn of its wavefronts, or, with many rows, 1.6 us and
-// 0.062 us a token for a turn of 256 workgroups (fitted as the tiles: 16 x 4096 x 4096
-// 7.2 us against 9.5, 16 x 11008 x 4096 15.8 and 13.3, 32 x 1024 x 8192 13.3 and 8.5).
-bool tiles_pay(const I8Desc &W, bool gated, int64_t batch) {
-  if (batch > 64) return true;
+// Modelled duration of the skinny kernel in us: 0.95 us and 0.054 us a token for each
+// turn of its wavefronts, or, with many rows, 1.6 us and 0.062 us a token for a turn of
+// 256 workgroups (fitted as the tiles: 16 x 4096 x 4096 7.2 us against their 9.5, 16 x
+// 11008 x 4096 15.8 and 13.3, 32 x 1024 x 8192 13.3 and 8.5).
+constexpr int64_t kMostSkinny = 64;  // tokens
+double skinny_us(const I8Desc &W, bool gated, int64_t batch) {
   const double turns = (double)((W.cols + 2047) / 2048), tok_tiles = (double)((batch + 31) / 32);
   const double tiles = (double)((W.rows + 15) / 16) * (gated ? 2 : 1) * tok_tiles;
   const double b = (double)std::min<int64_t>(batch, 32);
   const double alone = turns * (0.95 + 0.054 * b), full = tiles * turns / 256.0 * (1.6 + 0.062 * b);
-  const double us = 2.6 + std::cbrt(alone * alone * alone + full * full * full);
-  return i8_tile_us(W.rows, W.cols, gated, batch) < us;
+  return 2.6 + std::cbrt((float)(alone * alone * alone + full * full * full));
 }
 
 }  // namespace
 
-int64_t i8_product_ws_bytes(const I8Desc &W, bool gated, int64_t batch, bool quant) {
-  if (quant && quant_pays(W, gated, batch)) return 0;
-  return (quant ? product_at(W, batch) : 0) +
-         (!rows_pay(W, gated, batch) && tiles_pay(W, gated, batch) ? i8_tile_ws_bytes(W.rows, W.cols, gated, batch) : 0);
+I8Route i8_route(const I8Desc &W, bool gated, int64_t batch, bool quant) {
+  I8Route r = {I8Route::kRows, quant && quant_pays(W, gated, batch), {}, 0};
+  if (r.inside) return r;
+  if (!rows_pay(W, gated, batch)) {
+    r.plan = i8_tile_plan(W.rows, W.cols, gated, batch);
+    const bool tiles = batch > kMostSkinny || r.plan.us < skinny_us(W, gated, batch);
+    r.kind = tiles ? I8Route::kTiles : I8Route::kSkinny;
+  }
+  r.ws_bytes = (quant ? product_at(W, batch) : 0) + (r.kind == I8Route::kTiles ? r.plan.sums : 0);
+  return r;
 }
 
-hipError_t launch_i8_product(const I8Product &p, void *ws, hipStream_t stream) {
+hipError_t launch_i8_product(const I8Product &p, const I8Route &route, void *ws, hipStream_t stream) {
   I8Args A = {{p.W.codes, p.up.codes}, {p.W.scales, p.up.scales}, p.xcodes, p.xscales,
               static_cast<uint16_t *>(p.y), p.g, p.u, (int)p.W.rows, (int)p.W.cols, (int)p.batch, p.act};
-  if (p.x && quant_pays(p.W, p.gated(), p.batch)) return launch_i8_rows(A, p.x, p.type, p.gated(), stream);
+  if (route.inside) return launch_i8_rows(A, p.x, p.type, p.gated(), stream);
   if (p.x) {
     float *scales = static_cast<float *>(ws);
     int8_t *codes = static_cast<int8_t *>(ws) + codes_at(p.batch);
@@ -154,8 +159,8 @@ hipError_t launch_i8_product(const I8Product &p, void *ws, hipStream_t stream) {
     A.xs = scales;
     ws = static_cast<uint8_t *>(ws) + product_at(p.W, p.batch);
   }
-  if (rows_pay(p.W, p.gated(), p.batch)) return launch_i8_rows(A, nullptr, p.type, p.gated(), stream);
-  if (tiles_pay(p.W, p.gated(), p.batch)) return launch_i8_tile(A, p.type, p.gated(), ws, stream);
+  if (route.kind == I8Route::kRows) return launch_i8_rows(A, nullptr, p.type, p.gated(), stream);
+  if (route.kind == I8Route::kTiles) return launch_i8_tile(A, route.plan, p.type, p.gated(), ws, stream);
   if (p.type == MxType::kF16)
     return p.gated() ? skinny_as<MxType::kF16, true>(A, stream) : skinny_as<MxType::kF16, false>(A, stream);
   return p.gated() ? skinny_as<MxType::kBF16, true>(A, stream) : skinny_as<MxType::kBF16, false>(A, stream);

@@ -50,9 +50,8 @@ constexpr int kI8RowTokens = 8;
 bool i8_rows_quantize(int64_t cols, int64_t batch);
 hipError_t launch_i8_rows(const I8Args &A, const void *x, MxType type, bool gated, hipStream_t stream);
 
-// The tile kernels (i8_tile.hip): modelled duration in us, workspace, launch.
-double i8_tile_us(int64_t rows, int64_t cols, bool gated, int64_t batch);
-int64_t i8_tile_ws_bytes(int64_t rows, int64_t cols, bool gated, int64_t batch);
-hipError_t launch_i8_tile(const I8Args &A, MxType type, bool gated, void *ws, hipStream_t stream);
+// The tile kernels (i8_tile.hip).
+I8Plan i8_tile_plan(int64_t rows, int64_t cols, bool gated, int64_t batch);
+hipError_t launch_i8_tile(const I8Args &A, const I8Plan &p, MxType type, bool gated, void *ws, hipStream_t stream);
 
 }  // namespace aqlm

@@ -554,46 +554,6 @@ template <class S> constexpr GradCost cost_of(double f, double a, double b) {
 constexpr GradCost kCosts[] = {cost_of<Large>(1.94, 0.708, 0.0), cost_of<Half>(1.97, 0.517, 0.332),
                                cost_of<Middle>(1.91, 0.839, 0.344), cost_of<Small>(1.98, 0.486, 0.424)};
 
-struct GradPlan {
-  int shape, splits, steps_per_split;
-  int64_t col_tiles, tok_tiles;
-  int64_t ws_bytes() const {
-    return splits == 1 ? 0 : col_tiles * tok_tiles * splits * (int64_t)kCosts[shape].sums;
-  }
-};
-
-GradPlan plan_of(const I8Desc &W, bool gated, int64_t batch) {
-  GradPlan best{};
-  double best_us = 0.0;
-  const int64_t steps = (W.rows + 63) / 64 * (gated ? 2 : 1);
-  const double codes = (double)W.rows * (gated ? 2 : 1) * (double)W.cols;
-  const double read = codes / 5.3e6, power = 2.0 * codes * (double)batch / 1.2e9;
-  const double bounds = read * read * read + power * power * power;
-  for (int c = 0; c < (int)(sizeof(kCosts) / sizeof(kCosts[0])); ++c) {
-    const GradCost &k = kCosts[c];
-    GradPlan p{};
-    p.shape = c;
-    p.col_tiles = (W.cols + k.cols - 1) / k.cols;
-    p.tok_tiles = (batch + k.toks - 1) / k.toks;
-    const int64_t tiles = p.col_tiles * p.tok_tiles;
-    for (int s = 1; s <= 8; ++s) {
-      p.steps_per_split = (int)((steps + s - 1) / s);
-      p.splits = (int)((steps + p.steps_per_split - 1) / p.steps_per_split);
-      if (p.splits != s || (s > 1 && tiles * s > 512)) break;
-      const double whole = (double)(tiles * s / k.slots), rest = (double)(tiles * s % k.slots) / (double)k.slots;
-      const double turns = (double)((p.steps_per_split + k.kw - 1) / k.kw);
-      const double tile_us = whole * (k.f + turns * (k.a + k.b)) + (rest > 0 ? k.f + turns * (k.a + k.b * rest) : 0.0);
-      double us = std::cbrt(tile_us * tile_us * tile_us + bounds);
-      if (s > 1) us += 1.8 + (double)p.ws_bytes() * 2.0 / 4.2e6;
-      if (best.splits == 0 || us < best_us) {
-        best = p;
-        best_us = us;
-      }
-    }
-  }
-  return best;
-}
-
 template <MxType T, class S> hipError_t launch_shape(const I8GradArgs &A, hipStream_t stream) {
   const unsigned tiles = (unsigned)(A.col_tiles * A.tok_tiles);
   hipLaunchKernelGGL((i8_grad_kernel<T, S>), dim3(tiles * A.splits), dim3(S::kThreads * S::KW), 0, stream, A);
@@ -610,17 +570,16 @@ int64_t sums_at(const I8Desc &W, bool gated, int64_t batch) {
   return terms_at(batch) + (batch * part_of(W) * (gated ? 2 : 1) * 2 + 255) / 256 * 256;
 }
 
-template <MxType T> hipError_t grad_as(const I8Grad &p, void *ws, hipStream_t stream) {
+template <MxType T> hipError_t grad_as(const I8Grad &p, const I8Plan &g, void *ws, hipStream_t stream) {
   const int part = (int)part_of(p.W), ld = part * (p.gated() ? 2 : 1);
   int *const power = static_cast<int *>(ws);
   uint16_t *const d = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + terms_at(p.batch));
   const I8GradRowsArgs R = {p.dy, p.g, p.u, {p.W.scales, p.up.scales}, d, power, (int)p.W.rows, part, ld, p.act};
   if (p.gated()) launch_terms<T, true>(R, p.batch, stream);
   else launch_terms<T, false>(R, p.batch, stream);
-  const GradPlan g = plan_of(p.W, p.gated(), p.batch);
   float4_t *const sums = reinterpret_cast<float4_t *>(static_cast<uint8_t *>(ws) + sums_at(p.W, p.gated(), p.batch));
   const I8GradArgs A = {{p.W.codes, p.up.codes}, d, power, static_cast<uint16_t *>(p.dx), sums, (int)p.W.rows, part, ld,
-                        (int)p.W.cols, (int)p.batch, p.gated() ? 2 : 1, (int)g.col_tiles, (int)g.tok_tiles, g.splits,
+                        (int)p.W.cols, (int)p.batch, p.gated() ? 2 : 1, (int)g.across, (int)g.tok_tiles, g.splits,
                         g.steps_per_split};
   if (g.shape == 0) return launch_shape<T, Large>(A, stream);
   if (g.shape == 1) return launch_shape<T, Half>(A, stream);
@@ -630,12 +589,43 @@ template <MxType T> hipError_t grad_as(const I8Grad &p, void *ws, hipStream_t st
 
 }  // namespace
 
-int64_t i8_grad_ws_bytes(const I8Desc &W, bool gated, int64_t batch) {
-  return sums_at(W, gated, batch) + plan_of(W, gated, batch).ws_bytes();
+I8Plan i8_grad_plan(const I8Desc &W, bool gated, int64_t batch) {
+  I8Plan best{};
+  const int steps = (int)((W.rows + 63) / 64) * (gated ? 2 : 1);
+  const double codes = (double)W.rows * (gated ? 2 : 1) * (double)W.cols;
+  const double read = codes / 5.3e6, power = 2.0 * codes * (double)batch / 1.2e9;
+  const double bounds = read * read * read + power * power * power;
+  for (int c = 0; c < (int)(sizeof(kCosts) / sizeof(kCosts[0])); ++c) {
+    const GradCost &k = kCosts[c];
+    I8Plan p{};
+    p.shape = c;
+    p.across = (W.cols + k.cols - 1) / k.cols;
+    p.tok_tiles = (batch + k.toks - 1) / k.toks;
+    const int64_t tiles = p.across * p.tok_tiles;
+    for (int s = 1; s <= 8; ++s) {
+      p.steps_per_split = (steps + s - 1) / s;
+      p.splits = (steps + p.steps_per_split - 1) / p.steps_per_split;
+      if (p.splits != s || (s > 1 && tiles * s > 512)) break;
+      const double whole = (double)(tiles * s / k.slots), rest = (double)(tiles * s % k.slots) / (double)k.slots;
+      const double turns = (double)((p.steps_per_split + k.kw - 1) / k.kw);
+      const double tile_us = whole * (k.f + turns * (k.a + k.b)) + (rest > 0 ? k.f + turns * (k.a + k.b * rest) : 0.0);
+      p.sums = s > 1 ? tiles * s * k.sums : 0;
+      const double around = s > 1 ? 1.8 + (double)p.sums * (2.0 / 4.2e6) : 0.0;
+      if (best.splits != 0 && tile_us + around >= best.us) continue;  // (spares the root)
+      p.us = around + std::cbrt((float)(tile_us * tile_us * tile_us + bounds));
+      if (best.splits == 0 || p.us < best.us) best = p;
+    }
+  }
+  return best;
 }
 
-hipError_t launch_i8_grad(const I8Grad &p, void *ws, hipStream_t stream) {
-  return p.type == MxType::kF16 ? grad_as<MxType::kF16>(p, ws, stream) : grad_as<MxType::kBF16>(p, ws, stream);
+int64_t i8_grad_ws_bytes(const I8Desc &W, bool gated, int64_t batch, const I8Plan &plan) {
+  return sums_at(W, gated, batch) + plan.sums;
+}
+
+hipError_t launch_i8_grad(const I8Grad &p, const I8Plan &plan, void *ws, hipStream_t stream) {
+  return p.type == MxType::kF16 ? grad_as<MxType::kF16>(p, plan, ws, stream)
+                                : grad_as<MxType::kBF16>(p, plan, ws, stream);
 }
 
 }  // namespace aqlm

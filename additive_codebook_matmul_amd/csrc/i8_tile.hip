@@ -444,44 +444,6 @@ constexpr I8ShapeCost kCosts[] = {cost_of<Large>(2.52, 1.276, 0.0),    cost_of<W
                                   cost_of<Small>(3.2, 0.823, 0.171),   cost_of<Slim>(2.22, 0.583, 0.093),
                                   cost_of<Least>(2.05, 0.349, 0.366)};
 
-struct I8Plan {
-  int shape, splits, steps_per_split;
-  int64_t row_tiles, tok_tiles;
-  double us;
-  int64_t ws_bytes() const {
-    return splits == 1 ? 0 : row_tiles * tok_tiles * splits * (int64_t)kCosts[shape].sums;
-  }
-};
-
-I8Plan plan_of(int64_t rows, int64_t cols, bool gated, int64_t batch) {
-  I8Plan best{};
-  const int64_t steps = (cols + 127) / 128;
-  const double all_rows = (double)rows * (gated ? 2 : 1);
-  const double read = all_rows * (double)cols / 5.3e6, power = 2.0 * all_rows * (double)cols * (double)batch / 2.2e9;
-  const double bounds = read * read * read + power * power * power;
-  for (int c = 0; c < (int)(sizeof(kCosts) / sizeof(kCosts[0])); ++c) {
-    const I8ShapeCost &k = kCosts[c];
-    I8Plan p{};
-    p.shape = c;
-    const int out = gated ? k.rows / 2 : k.rows;
-    p.row_tiles = (rows + out - 1) / out;
-    p.tok_tiles = (batch + k.toks - 1) / k.toks;
-    const int64_t tiles = p.row_tiles * p.tok_tiles;
-    for (int s = 1; s <= 8; ++s) {
-      p.steps_per_split = (int)((steps + s - 1) / s);
-      p.splits = (int)((steps + p.steps_per_split - 1) / p.steps_per_split);
-      if (p.splits != s || (s > 1 && tiles * s > k.slots)) break;
-      const double whole = (double)(tiles * s / k.slots), rest = (double)(tiles * s % k.slots) / (double)k.slots;
-      const double turns = (double)((p.steps_per_split + k.kw - 1) / k.kw);
-      const double us = whole * (k.f + turns * (k.a + k.b)) + (rest > 0 ? k.f + turns * (k.a + k.b * rest) : 0.0);
-      p.us = 2.3 + std::cbrt(us * us * us + bounds);
-      if (s > 1) p.us += 1.7 + (double)p.ws_bytes() * 2.0 / 5.9e6;
-      if (best.splits == 0 || p.us < best.us) best = p;
-    }
-  }
-  return best;
-}
-
 template <MxType T, bool GATED, class S> hipError_t launch_shape(const I8TileArgs &B, hipStream_t stream) {
   const unsigned tiles = (unsigned)(B.row_tiles * B.tok_tiles);
   const dim3 grid(tiles * B.splits), block(S::kThreads * S::KW);
@@ -506,18 +468,40 @@ template <MxType T, bool GATED> hipError_t tile_as(int shape, const I8TileArgs &
 
 }  // namespace
 
-double i8_tile_us(int64_t rows, int64_t cols, bool gated, int64_t batch) {
-  return plan_of(rows, cols, gated, batch).us;
+I8Plan i8_tile_plan(int64_t rows, int64_t cols, bool gated, int64_t batch) {
+  I8Plan best{};
+  const int steps = (int)((cols + 127) / 128);
+  const double all_rows = (double)rows * (gated ? 2 : 1);
+  const double read = all_rows * (double)cols / 5.3e6, power = 2.0 * all_rows * (double)cols * (double)batch / 2.2e9;
+  const double bounds = read * read * read + power * power * power;
+  for (int c = 0; c < (int)(sizeof(kCosts) / sizeof(kCosts[0])); ++c) {
+    const I8ShapeCost &k = kCosts[c];
+    I8Plan p{};
+    p.shape = c;
+    const int out = gated ? k.rows / 2 : k.rows;
+    p.across = (rows + out - 1) / out;
+    p.tok_tiles = (batch + k.toks - 1) / k.toks;
+    const int64_t tiles = p.across * p.tok_tiles;
+    for (int s = 1; s <= 8; ++s) {
+      p.steps_per_split = (steps + s - 1) / s;
+      p.splits = (steps + p.steps_per_split - 1) / p.steps_per_split;
+      if (p.splits != s || (s > 1 && tiles * s > k.slots)) break;
+      const int64_t rounds = tiles * s < k.slots ? 0 : tiles * s / k.slots;
+      const double whole = (double)rounds, rest = (double)(tiles * s - rounds * k.slots) / (double)k.slots;
+      const double turns = (double)(k.kw == 1 ? p.steps_per_split : (p.steps_per_split + k.kw - 1) / k.kw);
+      const double us = whole * (k.f + turns * (k.a + k.b)) + (rest > 0 ? k.f + turns * (k.a + k.b * rest) : 0.0);
+      p.sums = s > 1 ? tiles * s * k.sums : 0;
+      const double around = s > 1 ? 4.0 + (double)p.sums * (2.0 / 5.9e6) : 2.3;
+      if (best.splits != 0 && us + around >= best.us) continue;  // (spares the root)
+      p.us = around + std::cbrt((float)(us * us * us + bounds));
+      if (best.splits == 0 || p.us < best.us) best = p;
+    }
+  }
+  return best;
 }
 
-int64_t i8_tile_ws_bytes(int64_t rows, int64_t cols, bool gated, int64_t batch) {
-  return plan_of(rows, cols, gated, batch).ws_bytes();
-}
-
-hipError_t launch_i8_tile(const I8Args &A, MxType type, bool gated, void *ws, hipStream_t stream) {
-  const I8Plan p = plan_of(A.rows, A.cols, gated, A.batch);
-  const I8TileArgs B = {A, static_cast<int4_vt *>(ws), (int)p.row_tiles, (int)p.tok_tiles, p.splits,
-                        p.steps_per_split};
+hipError_t launch_i8_tile(const I8Args &A, const I8Plan &p, MxType type, bool gated, void *ws, hipStream_t stream) {
+  const I8TileArgs B = {A, static_cast<int4_vt *>(ws), (int)p.across, (int)p.tok_tiles, p.splits, p.steps_per_split};
   if (type == MxType::kF16)
     return gated ? tile_as<MxType::kF16, true>(p.shape, B, stream) : tile_as<MxType::kF16, false>(p.shape, B, stream);
   return gated ? tile_as<MxType::kBF16, true>(p.shape, B, stream) : tile_as<MxType::kBF16, false>(p.shape, B, stream);

@@ -112,7 +112,7 @@ def _check_packed(codes: torch.Tensor, scales: torch.Tensor) -> Tuple[int, int]:
 
 def _output(out: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)  # (quicker than a tuple)
     _check_dense(out, "out", (dtype,), shape)
     if out.device != device:
         raise ValueError("out must be on the inputs' device")
