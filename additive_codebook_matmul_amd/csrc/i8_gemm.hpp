@@ -44,7 +44,8 @@ __device__ __forceinline__ void i8_store4(const I8Args &A, int tok, int row, con
   store4<T>(A.y + at, row, A.rows, float4_t{out[0], out[1], out[2], out[3]}, (A.rows & 3) == 0);
 }
 
-// Up to eight tokens by whole rows of W (i8_rows.hip); x: halves to be quantised on
+// Few tokens by whole rows of W (i8_rows.hip), up to four of a layer and kI8RowTokens
+// of a gated block; x: halves to be quantised on
 // the way, for sizes that i8_rows_quantize takes, or null where A.x and A.xs are given.
 constexpr int kI8RowTokens = 8;
 bool i8_rows_quantize(int64_t cols, int64_t batch);

@@ -1,5 +1,5 @@
-// Products of int8 layers and gated blocks for up to eight tokens: whole rows of W by
-// a wavefront.
+// Products of int8 layers for up to four tokens and of gated blocks for up to eight:
+// whole rows of W by a wavefront.
 //
 // Reading W bounds these (one token: a multiply and add for every byte), so that all
 // serves a steady stream: a wavefront takes two rows at a time (GATED: a row of the
@@ -215,8 +215,8 @@ template <MxType T, bool GATED, int B> void launch_b(const I8Args &A, const void
 template <MxType T, bool GATED> hipError_t rows_as(const I8Args &A, const void *x, hipStream_t stream) {
   if (A.batch == 1) launch_b<T, GATED, 1>(A, x, stream);
   else if (A.batch == 2) launch_b<T, GATED, 2>(A, x, stream);
-  else if (A.batch <= 4) launch_b<T, GATED, 4>(A, x, stream);
-  else launch_b<T, GATED, 8>(A, x, stream);
+  else if (!GATED || A.batch <= 4) launch_b<T, GATED, 4>(A, x, stream);
+  else if constexpr (GATED) launch_b<T, GATED, 8>(A, x, stream);
   return hipGetLastError();
 }
 

@@ -456,9 +456,11 @@ def test_gated_gradient_over_the_range_of_the_gate(act):
 
 @pytest.mark.parametrize("dtype", HALVES)
 @pytest.mark.parametrize("batch,out,n_in", [(1, 40, 16384), (1, 37, 16400), (1, 21, 32768), (1, 20, 32784), (2, 37, 8192),
-                                            (2, 37, 8208), (2, 20, 16384), (2, 21, 16400), (3, 20, 4112)])
+                                            (2, 37, 8208), (2, 20, 16384), (2, 21, 16400), (3, 20, 4112), (1, 21, 65536),
+                                            (1, 21, 131056), (2, 20, 32784), (2, 21, 131056), (4, 20, 16400), (4, 21, 131056),
+                                            (8, 21, 131056)])
 def test_long_rows_of_few_tokens(batch, out, n_in, dtype):
-    """Around the lengths up to which a product's own workgroups quantise the tokens."""
+    """Around the lengths up to which a product's own workgroups quantise the tokens, and to which LDS holds them."""
     w, up = weights(out, n_in, n_in), weights(out, n_in, n_in + 1)
     x = activations(batch, n_in, dtype, out)
     y, ok = guarded((batch, out), dtype)
