@@ -6,9 +6,9 @@
 // i8_grad_rows_kernel writes D once, as float16 times a power of two of the token's
 // own that takes its largest magnitude to [2^14, 2^15), and the kernels after it
 // multiply by the codes, which float16 holds exactly, sum in float32 and take the
-// power of two back. A code is 8 bits and float16 has 11, so this rounding to 2^-12
+// power of two back. A code is 8 bits and float16 has 11, so this rounding by 2^-11
 // of the value is the only one before the last (bfloat16 gradients times float32
-// scales would lose 2^-9 in bfloat16).
+// scales would lose 2^-8 in bfloat16).
 // What bounds the product of many tokens is the card's power, as for the int8 products:
 // 2048 x 11008 x 4096 takes 182 us at first and 190 to 230, by the card, once the clock
 // has fallen (1.0 PFLOP/s; the matrix cores busy for 59 % of the cycles, LDS for 22; the

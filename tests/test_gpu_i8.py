@@ -283,14 +283,15 @@ def test_grad_input_exact(batch, out, n_in, dtype):
 
 
 def grad_tolerance(terms, ref, codes, dtype):
-    """Half a step of the result, half a float16 step and three float32 roundings of each
-    term (float16 below 2^-14 of the token's 2^14: 2^-39 of the largest), and the additions'."""
+    """Half a step of the result, half a float16 step (11 significant bits: values of [1, 2) are
+    2^-10 apart, so 2^-11 of the term) and three float32 roundings of each term (float16 below
+    2^-14 of the token's 2^14: 2^-39 of the largest), and the additions'."""
     bound = np.abs(terms) @ np.abs(codes.astype(np.float64))
     top = np.abs(terms).max(axis=1, keepdims=True)
     flat = np.abs(codes.astype(np.float64)).sum(axis=0)[None, :] * top * 2.0 ** -39
     K = codes.shape[0]
     tiny = 2.0 ** -25 if dtype == torch.float16 else 2.0 ** -134
-    return (torch.finfo(dtype).eps / 2 * np.abs(ref) + bound * (2.0 ** -12 + 3 * 2.0 ** -24 + K * 2.0 ** -23)
+    return (torch.finfo(dtype).eps / 2 * np.abs(ref) + bound * (2.0 ** -11 + 3 * 2.0 ** -24 + K * 2.0 ** -23)
             + flat + tiny)
 
 
