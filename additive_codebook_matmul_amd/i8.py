@@ -105,7 +105,7 @@ def i8_quantize(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]
         raise ValueError("cols must be a multiple of 16")
     codes = _output(None if out is None else out[0], (rows, cols), torch.int8, x.device)
     if out is None:
-        scales = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        scales = torch.empty(rows, dtype=torch.float32, device=x.device)
     else:
         scales = out[1]
         _check_packed(codes, scales)
