@@ -3,16 +3,20 @@
 // one after the other), the gradient of each product times its channel's scale:
 //   a layer  D = dy w
 //   gated    D = (dh u act'(g) w_gate, dh act(g) w_up)
-// i8_grad_rows_kernel writes D once, as float16 times a power of two of the token's
-// own that takes its largest magnitude to [2^14, 2^15), and the kernels after it
-// multiply by the codes, which float16 holds exactly, sum in float32 and take the
-// power of two back. A code is 8 bits and float16 has 11, so this rounding by 2^-11
-// of the value is the only one before the last (bfloat16 gradients times float32
-// scales would lose 2^-8 in bfloat16).
+// A term is float32 and a matrix instruction takes float16, so a term goes there as the
+// sum of two. i8_grad_rows_kernel writes D once, each term times a power of two of the
+// token's own that takes the largest magnitude to [2^14, 2^15): its nearest float16, and
+// 2^11 times what that leaves, its nearest float16 too. The first is off by 2^-11 of the
+// term at most, so the second leaves 2^-23 of it (or 2^-36, a 2^-50th of the token's
+// largest, where it is subnormal): float32's own roundings are no smaller. The kernels
+// after it multiply the first by the codes and the second by the codes times 2^-11, both of
+// which float16 holds exactly, sum in float32 and take the power of two back. (One float16
+// a term spares half of the instructions, 2048 x 11008 x 4096 193 to 203 us, and loses 2^-11
+// of every term.)
 // What bounds the product of many tokens is the card's power, as for the int8 products:
-// 2048 x 11008 x 4096 takes 182 us at first and 190 to 230, by the card, once the clock
-// has fallen (1.0 PFLOP/s; the matrix cores busy for 59 % of the cycles, LDS for 22; the
-// library's product of float16 matrices 211).
+// with its terms' launch 2048 x 11008 x 4096 takes 335 to 355 us, and 239 with zeros for
+// codes and gradients (gated 700 and 516): 1.1 PFLOP/s of float16 instructions. (The
+// library's product of float16 matrices, half as many, 211.)
 #include <algorithm>
 #include <cmath>
 
@@ -26,7 +30,8 @@ struct I8GradRowsArgs {
   const void *dy;
   const float *g, *u;
   const float *ws[2];
-  uint16_t *d;   // [batch][ld]: matrix m's part begins at m * part, zeros behind its rows
+  uint16_t *d;   // [batch][ld]: matrix m's part begins at 2 m part; 64 terms' first halves, then
+                 // their second ones, zeros behind its rows
   int *power;    // [batch]
   int rows, part, ld;
   I8Act act;
@@ -67,6 +72,16 @@ template <int WAVES> __device__ __forceinline__ int power_of(uint32_t top, uint3
   for (int w = 0; w < WAVES; ++w) top = max(top, tops[w]);
   return top == 0 ? 0 : 15 - __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, top));
 }
+
+// The two float16 numbers of a term, v times 2^power. (Infinity and NaN are the first's.)
+__device__ __forceinline__ void split_term(float v, int power, uint32_t &first, uint32_t &second) {
+  const float scaled = __builtin_amdgcn_ldexpf(v, power);
+  first = f2h(scaled);
+  second = (first & 0x7C00u) == 0x7C00u ? 0u : f2h((scaled - h2f(first)) * 0x1p11f);
+}
+
+// Where row i's first half lies in its matrix's part; the second is 64 further on.
+__device__ __forceinline__ int term_at(int i) { return 2 * (i & ~63) + (i & 63); }
 
 // A token a workgroup, 8 rows of the matrix a thread and round, the terms in
 // registers between their maximum and their rounding: everything is read and written
@@ -124,11 +139,14 @@ __global__ __launch_bounds__(WAVES * 64) void i8_grad_rows_kernel(const I8GradRo
       if (i < A.part) {
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-          uint32_t o[8];
+          uint32_t o[2][8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = f2h(__builtin_amdgcn_ldexpf(v[r][m][e], e2));
-          *reinterpret_cast<uint4 *>(A.d + tok * A.ld + m * A.part + i) =
-              make_uint4(o[0] | (o[1] << 16), o[2] | (o[3] << 16), o[4] | (o[5] << 16), o[6] | (o[7] << 16));
+          for (int e = 0; e < 8; ++e) split_term(v[r][m][e], e2, o[0][e], o[1][e]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<uint4 *>(A.d + tok * A.ld + 2 * m * A.part + term_at(i) + 64 * k) =
+                make_uint4(o[k][0] | (o[k][1] << 16), o[k][2] | (o[k][3] << 16), o[k][4] | (o[k][5] << 16),
+                           o[k][6] | (o[k][7] << 16));
         }
       }
     }
@@ -160,7 +178,13 @@ __global__ __launch_bounds__(1024) void i8_grad_any_rows_kernel(const I8GradRows
       float v[M] = {};
       if (i < A.rows) terms(i, v);
 #pragma unroll
-      for (int m = 0; m < M; ++m) A.d[tok * A.ld + m * A.part + i] = (uint16_t)f2h(__builtin_amdgcn_ldexpf(v[m], e2));
+      for (int m = 0; m < M; ++m) {
+        uint32_t first, second;
+        split_term(v[m], e2, first, second);
+        uint16_t *const to = A.d + tok * A.ld + 2 * m * A.part + term_at(i);
+        to[0] = (uint16_t)first;
+        to[64] = (uint16_t)second;
+      }
     }
   }
 }
@@ -187,13 +211,15 @@ template <MxType T, bool GATED> void launch_terms(const I8GradRowsArgs &R, int64
 //   * A K step is 64 rows of one matrix. Codes and D go from memory straight to LDS,
 //     one or two steps ahead. 16-byte chunk c of row r of the codes lies at chunk
 //     c ^ turn(r), so that the 32 lanes that read 8 rows x 32 columns at once touch
-//     all banks; D's 128-byte rows are permuted as in the other tile kernels.
+//     all banks; D's 128-byte rows, first halves and second, are permuted as in the other
+//     tile kernels.
 //   * ds_read_b64_tr_b8 transposes on the way out of LDS: 16 lanes give the places of
 //     8 rows x 16 columns and each receives eight rows of one column, which is one
 //     side of v_mfma_f32_32x32x16_f16 but for the type.
 //   * A code becomes float16 in registers: its bits with the sign bit turned, below
-//     the exponent of 1024, are 1152 more than it, exactly. Ten instructions for
-//     the eight terms of a lane, between the products of the chunk before.
+//     the exponent of 1024, are 1152 more than it, exactly; times 2^-11 it is one still.
+//     14 instructions for the eight terms of a lane, between the products of the chunk
+//     before.
 struct I8GradArgs {
   const int8_t *w[2];
   const uint16_t *d;  // [batch][ld]
@@ -209,7 +235,7 @@ template <int RT_, int NT_, int RW_, int TW_, int KW_, int STAGES_> struct Shape
   static constexpr int RT = RT_, NT = NT_, RW = RW_, TW = TW_, KW = KW_, STAGES = STAGES_;
   static constexpr int kWaves = RW * TW, kThreads = 64 * kWaves;  // of one share of K
   static constexpr int kCols = 32 * RT * RW, kToks = 32 * NT * TW;
-  static constexpr int kWBytes = 64 * kCols, kStage = kWBytes + kToks * 128;
+  static constexpr int kWBytes = 64 * kCols, kXBytes = kToks * 128, kStage = kWBytes + 2 * kXBytes;
   static constexpr int kSums = kCols * kToks * 4;
   // LDS bytes of a stage's array: the stage, the shares' sums in the first one, the
   // results in the second (and third: half of the wavefronts each)
@@ -224,23 +250,26 @@ template <int COLS> __device__ __forceinline__ int turn_of(int r) {
   return COLS == 256 ? 2 * (r & 7) : 2 * ((r >> 1) & 3);
 }
 
-// Eight codes as float16.
-__device__ __forceinline__ uint4 codes_to_f16(const uint2 &c) {
+// Eight codes as float16, and times 2^-11.
+__device__ __forceinline__ void codes_to_f16(const uint2 &c, uint4 &whole, uint4 &small) {
   const uint32_t in[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
-  const half2_t off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
-  uint32_t r[4];
+  const half2_t off = {(_Float16)-1152.0f, (_Float16)-1152.0f}, by = {(_Float16)0x1p-11f, (_Float16)0x1p-11f};
+  uint32_t r[4], s[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t v = __builtin_amdgcn_perm(0x64646464u, in[i >> 1], i & 1 ? 0x04030402u : 0x04010400u);
-    r[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, v) + off);
+    const half2_t code = __builtin_bit_cast(half2_t, v) + off;
+    r[i] = __builtin_bit_cast(uint32_t, code);
+    s[i] = __builtin_bit_cast(uint32_t, code * by);
   }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+  whole = make_uint4(r[0], r[1], r[2], r[3]);
+  small = make_uint4(s[0], s[1], s[2], s[3]);
 }
 
 template <MxType T, class S>
 __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8GradArgs A) {
   constexpr int RT = S::RT, NT = S::NT, TW = S::TW, KW = S::KW, kWaves = S::kWaves, kCols = S::kCols;
-  constexpr int kStage = S::kStage, kWBytes = S::kWBytes;
+  constexpr int kStage = S::kStage, kWBytes = S::kWBytes, kXBytes = S::kXBytes;
   constexpr int kArray = S::kArray;
   // one array per stage: the compiler then knows which loads into LDS a read
   // of LDS can depend on
@@ -283,7 +312,8 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
 
   // Step t into a stage: loads of a wavefront fill 1 KiB in lane order, 1024 /
   // kCols rows of codes or eight tokens.
-  constexpr int kWLoads = 64 * kCols / 1024 / kWaves, kXLoads = S::kToks / 8 / kWaves;
+  constexpr int kWLoads = 64 * kCols / 1024 / kWaves, kXLoads = S::kToks / 8 / kWaves;  // (of each half)
+  constexpr int kLoads = kWLoads + 2 * kXLoads;
   constexpr int kLoadRows = 1024 / kCols, kRowLanes = kCols / 16;
   static_assert(64 * kCols % (1024 * kWaves) == 0 && S::kToks % (8 * kWaves) == 0, "loads");
   static_assert(kWLoads <= 8 && kXLoads <= 8, "places of a lane's loads");
@@ -307,16 +337,18 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
     const int rows = __builtin_amdgcn_readfirstlane(t < g1 ? max(0, min(64, A.rows - o)) : 0);
     const int8_t *const base = second ? A.w[1] : A.w[0];
     const Rsrc wrs = make_rsrc(base + (rows > 0 ? (int64_t)o * cols : 0), (uint32_t)rows * cols);
-    const uint32_t k = t < g1 ? (uint32_t)t * 128u : kMxOOB;
+    const uint32_t k = t < g1 ? (uint32_t)t * 256u : kMxOOB;
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(wrs, (LdsPtr)(a + (kw * kStage + (wave + i * kWaves) * 1024)), 16,
                                                woff[i], 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs,
-                                               (LdsPtr)(a + (kw * kStage + kWBytes + (wave + i * kWaves) * 1024)), 16,
-                                               xoff[i] + k, 0, 0, 0);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            xrs, (LdsPtr)(a + (kw * kStage + kWBytes + p * kXBytes + (wave + i * kWaves) * 1024)), 16,
+            xoff[i] + k + 128u * p, 0, 0, 0);
   };
 
   // places of the lane's operands: 16 further rows of codes, 32 further columns or
@@ -335,11 +367,14 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
   }
   static_assert(RT <= 4, "places of the operands");
   uint2 raw[2][RT];
-  uint4 w[2][RT], b[2][NT];
+  uint4 w[2][2][RT], b[2][2][NT];  // [chunk's parity][first or second halves]
 #pragma unroll
-  for (int i = 0; i < RT; ++i) w[1][i] = make_uint4(0, 0, 0, 0);
+  for (int p = 0; p < 2; ++p) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j) b[1][j] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < RT; ++i) w[1][p][i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) b[1][p][j] = make_uint4(0, 0, 0, 0);
+  }
   auto read_w = [&](const uint8_t *a, int s) __attribute__((always_inline)) {
     typedef int int2_vt __attribute__((ext_vector_type(2)));
     typedef __attribute__((address_space(3))) int2_vt *TrPtr;
@@ -350,17 +385,22 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
   };
   auto read_x = [&](const uint8_t *a, int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) b[s & 1][j] = *reinterpret_cast<const uint4 *>(a + (xbase[s] + 4096u * j));
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        b[s & 1][p][j] = *reinterpret_cast<const uint4 *>(a + (xbase[s] + (uint32_t)(p * kXBytes) + 4096u * j));
   };
   auto convert = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) w[s & 1][i] = codes_to_f16(raw[s & 1][i]);
+    for (int i = 0; i < RT; ++i) codes_to_f16(raw[s & 1][i], w[s & 1][0][i], w[s & 1][1][i]);
   };
   auto products = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma32<MxType::kF16>(w[s & 1][i], b[s & 1][j], acc[i][j]);
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = mx_mfma32<MxType::kF16>(w[s & 1][p][i], b[s & 1][p][j], acc[i][j]);
   };
   // Step t from stage `a`. `far` is the stage that the step before read, filled for
   // step t + STAGES - 1. Codes are read two chunks ahead and converted one ahead; the
@@ -383,12 +423,12 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
       if (s < 2) read_w(a, s + 2);
       products(s);
       convert(s + 1);
-      __builtin_amdgcn_sched_group_barrier(0x100, NT, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * NT, 0);
       if (s < 2) __builtin_amdgcn_sched_group_barrier(0x100, RT, 0);
 #pragma unroll
-      for (int k = 0; k < RT * NT; ++k) {
+      for (int k = 0; k < 2 * RT * NT; ++k) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, (10 + NT - 1) / NT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, (14 + 2 * NT - 1) / (2 * NT), 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -398,7 +438,7 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[i][j][0] = materialize(acc[i][j][0]);
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"((S::STAGES - 2) * (kWLoads + kXLoads)) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "i"((S::STAGES - 2) * kLoads) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" : : : "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -409,7 +449,7 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
     fill(g0 + 1, s1);
     __builtin_amdgcn_sched_barrier(0);
   }
-  asm volatile("s_waitcnt vmcnt(%0)" : : "i"((S::STAGES - 2) * (kWLoads + kXLoads)) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0)" : : "i"((S::STAGES - 2) * kLoads) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" : : : "memory");
   // (whole turns of the stages: with a way out after each step the compiler keeps
@@ -531,28 +571,28 @@ __global__ __launch_bounds__(S::kThreads) void i8_grad_sum_kernel(const I8GradAr
 }
 
 typedef Shape<2, 2, 4, 2, 1, 3> Large;   // 256 columns x 128 tokens
-typedef Shape<2, 1, 4, 2, 1, 3> Half;    // 256 x 64
-typedef Shape<2, 2, 2, 1, 2, 2> Middle;  // 128 x 64
-typedef Shape<2, 1, 2, 1, 2, 3> Small;   // 128 x 32
+typedef Shape<2, 1, 4, 2, 1, 2> Half;    // 256 x 64
+typedef Shape<2, 1, 2, 1, 2, 2> Small;   // 128 x 32
 
 // Tile of a product and the workgroups K is split over, chosen as for the int8
-// products (i8_tile.hip): reading at 5.3 TB/s, products at 1.2 PFLOP/s, sums of splits
-// at 4.2 TB/s. Fitted to eight layers from 1 to 2048 tokens, each shape and split
-// measured at each, within 4 % at the median; the choice costs 2 % on average against
-// the best one.
-// (Each shape with its best splits, Large to Small: 301 x 4096 x 11008 60, 49, 48 and 62
-// us, 2048 x 11008 x 4096 203, 241, 256, 331, 333 x 1376 x 4096 24, 20, 17, 17, 1 x
-// 28672 x 8192 60, 51, 57, 56.)
+// products (i8_tile.hip) but for c us more a step from where CUs hold two workgroups:
+// reading at 5.3 TB/s, products at 0.7 PFLOP/s, sums of splits at 4.8 TB/s. Fitted to eight
+// layers from 1 to 2048 tokens, each shape and 1, 2, 4 and 8 splits measured at each,
+// within 5 % at the median; the choice costs 0.3 % on average against the best one.
+// (Each shape with its best splits, terms' launch included, Large to Small: 301 x 4096 x
+// 11008 94, 72 and 95 us, 2048 x 11008 x 4096 348, 374, 486, 333 x 1376 x 4096 30, 27, 22, 1
+// x 28672 x 8192 92, 70, 58. Tiles of 128 x 64, by two or four wavefronts, and 256 x 64 by
+// four would spare 0.1 % of the choice's time.)
 struct GradCost {
   int cols, toks, kw, sums;  // sums: bytes of a workgroup's in the workspace
   int slots;                 // workgroups the chip holds at a time
-  double f, a, b;
+  double f, a, b, c;
 };
-template <class S> constexpr GradCost cost_of(double f, double a, double b) {
-  return {S::kCols, S::kToks, S::KW, S::kSums, S::kSlots, f, a, b};
+template <class S> constexpr GradCost cost_of(double f, double a, double b, double c) {
+  return {S::kCols, S::kToks, S::KW, S::kSums, S::kSlots, f, a, b, c};
 }
-constexpr GradCost kCosts[] = {cost_of<Large>(1.94, 0.708, 0.0), cost_of<Half>(1.97, 0.517, 0.332),
-                               cost_of<Middle>(1.91, 0.839, 0.344), cost_of<Small>(1.98, 0.486, 0.424)};
+constexpr GradCost kCosts[] = {cost_of<Large>(0.07, 1.317, 0.0, 0.0), cost_of<Half>(0.55, 0.841, 0.247, 0.522),
+                               cost_of<Small>(1.28, 0.736, 0.465, 0.185)};
 
 template <MxType T, class S> hipError_t launch_shape(const I8GradArgs &A, hipStream_t stream) {
   const unsigned tiles = (unsigned)(A.col_tiles * A.tok_tiles);
@@ -567,11 +607,11 @@ int64_t part_of(const I8Desc &W) { return (W.rows + 63) / 64 * 64; }
 // Workspace: the powers, D and the split sums, from multiples of 256 bytes on.
 int64_t terms_at(int64_t batch) { return (batch * 4 + 255) / 256 * 256; }
 int64_t sums_at(const I8Desc &W, bool gated, int64_t batch) {
-  return terms_at(batch) + (batch * part_of(W) * (gated ? 2 : 1) * 2 + 255) / 256 * 256;
+  return terms_at(batch) + (batch * part_of(W) * (gated ? 2 : 1) * 4 + 255) / 256 * 256;
 }
 
 template <MxType T> hipError_t grad_as(const I8Grad &p, const I8Plan &g, void *ws, hipStream_t stream) {
-  const int part = (int)part_of(p.W), ld = part * (p.gated() ? 2 : 1);
+  const int part = (int)part_of(p.W), ld = 2 * part * (p.gated() ? 2 : 1);
   int *const power = static_cast<int *>(ws);
   uint16_t *const d = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + terms_at(p.batch));
   const I8GradRowsArgs R = {p.dy, p.g, p.u, {p.W.scales, p.up.scales}, d, power, (int)p.W.rows, part, ld, p.act};
@@ -583,7 +623,6 @@ template <MxType T> hipError_t grad_as(const I8Grad &p, const I8Plan &g, void *w
                         g.steps_per_split};
   if (g.shape == 0) return launch_shape<T, Large>(A, stream);
   if (g.shape == 1) return launch_shape<T, Half>(A, stream);
-  if (g.shape == 2) return launch_shape<T, Middle>(A, stream);
   return launch_shape<T, Small>(A, stream);
 }
 
@@ -593,7 +632,7 @@ I8Plan i8_grad_plan(const I8Desc &W, bool gated, int64_t batch) {
   I8Plan best{};
   const int steps = (int)((W.rows + 63) / 64) * (gated ? 2 : 1);
   const double codes = (double)W.rows * (gated ? 2 : 1) * (double)W.cols;
-  const double read = codes / 5.3e6, power = 2.0 * codes * (double)batch / 1.2e9;
+  const double read = codes / 5.3e6, power = 2.0 * codes * (double)batch / 0.7e9;
   const double bounds = read * read * read + power * power * power;
   for (int c = 0; c < (int)(sizeof(kCosts) / sizeof(kCosts[0])); ++c) {
     const GradCost &k = kCosts[c];
@@ -608,9 +647,10 @@ I8Plan i8_grad_plan(const I8Desc &W, bool gated, int64_t batch) {
       if (p.splits != s || (s > 1 && tiles * s > 512)) break;
       const double whole = (double)(tiles * s / k.slots), rest = (double)(tiles * s % k.slots) / (double)k.slots;
       const double turns = (double)((p.steps_per_split + k.kw - 1) / k.kw);
-      const double tile_us = whole * (k.f + turns * (k.a + k.b)) + (rest > 0 ? k.f + turns * (k.a + k.b * rest) : 0.0);
+      const double last = rest > 0 ? k.f + turns * (k.a + k.b * rest + (rest > 0.5 ? k.c : 0.0)) : 0.0;
+      const double tile_us = whole * (k.f + turns * (k.a + k.b + k.c)) + last;
       p.sums = s > 1 ? tiles * s * k.sums : 0;
-      const double around = s > 1 ? 1.8 + (double)p.sums * (2.0 / 4.2e6) : 0.0;
+      const double around = s > 1 ? 2.3 + (double)p.sums * (2.0 / 4.8e6) : 0.0;
       if (best.splits != 0 && tile_us + around >= best.us) continue;  // (spares the root)
       p.us = around + std::cbrt((float)(tile_us * tile_us * tile_us + bounds));
       if (best.splits == 0 || p.us < best.us) best = p;

@@ -123,11 +123,11 @@ AQLM_API int aqlm_i8_gated(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up,
 /*
  * aqlm_i8_grad_input: dx [batch][cols] = dy [batch][rows] . W, the gradient of
  * aqlm_i8_gemm_quant with respect to x through the (constant) weights and
- * straight through the quantisation; dy and dx of `type` (F16 or BF16). Each
- * token's gradients times the channels' scales enter the matrix instructions as
- * float16, relative to a power of two of the token's own: 11 significant bits
- * for what lies within 2^-28 of the token's largest, whatever its magnitude (the
- * terms themselves are float32).
+ * straight through the quantisation; dy and dx of `type` (F16 or BF16). The terms,
+ * each token's gradients times the channels' scales, are float32 and enter the
+ * matrix instructions as the sum of two float16 numbers, relative to a power of two
+ * of the token's own: off by at most 2^-23 of the term, or 2^-50 of the token's
+ * largest one, whatever its magnitude.
  * rows need not be a multiple of anything; batch == 0 is a no-op.
  */
 AQLM_API int aqlm_i8_grad_input_workspace_size(const aqlm_i8_matrix *W, int64_t batch, int64_t *bytes);
