@@ -96,7 +96,9 @@ int aqlm_i8_dequant(const aqlm_i8_matrix *m, int32_t type, void *W, void *stream
 
 int aqlm_i8_gemm_workspace_size(const aqlm_i8_matrix *W, int64_t batch, int64_t *bytes) {
   return workspace_size(W, nullptr, false, batch, bytes,
-                        [&](const aqlm::I8Desc &d) { return aqlm::i8_route(d, false, batch, false).ws_bytes; });
+                        [&](const aqlm::I8Desc &d) {
+                          return aqlm::i8_route(d.rows, d.cols, false, batch, false).ws_bytes;
+                        });
 }
 
 int aqlm_i8_gemm(const aqlm_i8_matrix *W, const aqlm_i8_matrix *x, void *y, int32_t type, void *workspace,
@@ -110,7 +112,7 @@ int aqlm_i8_gemm(const aqlm_i8_matrix *W, const aqlm_i8_matrix *x, void *y, int3
   if (dx.rows == 0) return AQLM_OK;
   if (!y) return AQLM_ERR_NULL;
   if (!aligned16(y)) return AQLM_ERR_ALIGN;
-  const aqlm::I8Route route = aqlm::i8_route(d, false, dx.rows, false);
+  const aqlm::I8Route route = aqlm::i8_route(d.rows, d.cols, false, dx.rows, false);
   st = check_workspace(route.ws_bytes, workspace, workspace_bytes);
   if (st != AQLM_OK) return st;
   const aqlm::I8Product p = {d, kNone, aqlm::I8Act::kSilu, nullptr, dx.codes, dx.scales, dx.rows,
@@ -120,7 +122,9 @@ int aqlm_i8_gemm(const aqlm_i8_matrix *W, const aqlm_i8_matrix *x, void *y, int3
 
 int aqlm_i8_gemm_quant_workspace_size(const aqlm_i8_matrix *W, int64_t batch, int64_t *bytes) {
   return workspace_size(W, nullptr, false, batch, bytes,
-                        [&](const aqlm::I8Desc &d) { return aqlm::i8_route(d, false, batch, true).ws_bytes; });
+                        [&](const aqlm::I8Desc &d) {
+                          return aqlm::i8_route(d.rows, d.cols, false, batch, true).ws_bytes;
+                        });
 }
 
 int aqlm_i8_gemm_quant(const aqlm_i8_matrix *W, const void *x, int64_t batch, void *y, int32_t type,
@@ -133,7 +137,7 @@ int aqlm_i8_gemm_quant(const aqlm_i8_matrix *W, const void *x, int64_t batch, vo
   if (batch == 0) return AQLM_OK;
   st = check_io(x, y);
   if (st != AQLM_OK) return st;
-  const aqlm::I8Route route = aqlm::i8_route(d, false, batch, true);
+  const aqlm::I8Route route = aqlm::i8_route(d.rows, d.cols, false, batch, true);
   st = check_workspace(route.ws_bytes, workspace, workspace_bytes);
   if (st != AQLM_OK) return st;
   const aqlm::I8Product p = {d, kNone, aqlm::I8Act::kSilu, x, nullptr, nullptr, batch,
@@ -144,7 +148,9 @@ int aqlm_i8_gemm_quant(const aqlm_i8_matrix *W, const void *x, int64_t batch, vo
 int aqlm_i8_gated_workspace_size(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, int64_t batch,
                                  int64_t *bytes) {
   return workspace_size(gate, up, true, batch, bytes,
-                        [&](const aqlm::I8Desc &d) { return aqlm::i8_route(d, true, batch, true).ws_bytes; });
+                        [&](const aqlm::I8Desc &d) {
+                          return aqlm::i8_route(d.rows, d.cols, true, batch, true).ws_bytes;
+                        });
 }
 
 int aqlm_i8_gated(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, const void *x, int64_t batch, int32_t act,
@@ -160,7 +166,7 @@ int aqlm_i8_gated(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, const vo
   if (st != AQLM_OK) return st;
   if (!g != !u) return AQLM_ERR_NULL;
   if (!aligned16(g) || !aligned16(u)) return AQLM_ERR_ALIGN;
-  const aqlm::I8Route route = aqlm::i8_route(d, true, batch, true);
+  const aqlm::I8Route route = aqlm::i8_route(d.rows, d.cols, true, batch, true);
   st = check_workspace(route.ws_bytes, workspace, workspace_bytes);
   if (st != AQLM_OK) return st;
   const aqlm::I8Product p = {d, e, static_cast<aqlm::I8Act>(act), x, nullptr, nullptr, batch,
@@ -171,7 +177,8 @@ int aqlm_i8_gated(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, const vo
 int aqlm_i8_grad_input_workspace_size(const aqlm_i8_matrix *W, int64_t batch, int64_t *bytes) {
   return workspace_size(W, nullptr, false, batch, bytes,
                         [&](const aqlm::I8Desc &d) {
-                          return aqlm::i8_grad_ws_bytes(d, false, batch, aqlm::i8_grad_plan(d, false, batch));
+                          return aqlm::i8_grad_ws_bytes(d.rows, false, batch,
+                                                        aqlm::i8_grad_plan(d.rows, d.cols, false, batch));
                         });
 }
 
@@ -185,8 +192,8 @@ int aqlm_i8_grad_input(const aqlm_i8_matrix *W, const void *dy, int64_t batch, v
   if (batch == 0) return AQLM_OK;
   st = check_io(dy, dx);
   if (st != AQLM_OK) return st;
-  const aqlm::I8Plan plan = aqlm::i8_grad_plan(d, false, batch);
-  st = check_workspace(aqlm::i8_grad_ws_bytes(d, false, batch, plan), workspace, workspace_bytes);
+  const aqlm::I8Plan plan = aqlm::i8_grad_plan(d.rows, d.cols, false, batch);
+  st = check_workspace(aqlm::i8_grad_ws_bytes(d.rows, false, batch, plan), workspace, workspace_bytes);
   if (st != AQLM_OK) return st;
   const aqlm::I8Grad p = {d, kNone, aqlm::I8Act::kSilu, nullptr, nullptr, dy, batch, dx,
                           static_cast<aqlm::MxType>(type)};
@@ -197,7 +204,8 @@ int aqlm_i8_gated_grad_workspace_size(const aqlm_i8_matrix *gate, const aqlm_i8_
                                       int64_t *bytes) {
   return workspace_size(gate, up, true, batch, bytes,
                         [&](const aqlm::I8Desc &d) {
-                          return aqlm::i8_grad_ws_bytes(d, true, batch, aqlm::i8_grad_plan(d, true, batch));
+                          return aqlm::i8_grad_ws_bytes(d.rows, true, batch,
+                                                        aqlm::i8_grad_plan(d.rows, d.cols, true, batch));
                         });
 }
 
@@ -213,8 +221,8 @@ int aqlm_i8_gated_grad(const aqlm_i8_matrix *gate, const aqlm_i8_matrix *up, con
   st = check_io(dh, dx);
   if (st == AQLM_OK) st = check_io(g, u);
   if (st != AQLM_OK) return st;
-  const aqlm::I8Plan plan = aqlm::i8_grad_plan(d, true, batch);
-  st = check_workspace(aqlm::i8_grad_ws_bytes(d, true, batch, plan), workspace, workspace_bytes);
+  const aqlm::I8Plan plan = aqlm::i8_grad_plan(d.rows, d.cols, true, batch);
+  st = check_workspace(aqlm::i8_grad_ws_bytes(d.rows, true, batch, plan), workspace, workspace_bytes);
   if (st != AQLM_OK) return st;
   const aqlm::I8Grad p = {d, e, static_cast<aqlm::I8Act>(act), g, u, dh, batch, dx,
                           static_cast<aqlm::MxType>(type)};

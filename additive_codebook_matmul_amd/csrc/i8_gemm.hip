@@ -6,9 +6,6 @@
 // just what v_mfma_i32_16x16x64_i8 takes. The integer sums meet in LDS. It serves short
 // layers, where a launch and two or three round trips to memory are all there is (16 x
 // 4096 x 4096 7.2 us, 2048 x 1024 3.6).
-#include <algorithm>
-#include <cmath>
-
 #include "i8_gemm.hpp"
 
 namespace aqlm {
@@ -97,54 +94,7 @@ template <MxType T, bool GATED> hipError_t skinny_as(const I8Args &A, hipStream_
   return hipGetLastError();
 }
 
-// Workspace of quantised activations: scales, then codes, from multiples of 256 bytes on.
-int64_t codes_at(int64_t batch) { return (batch * 4 + 255) / 256 * 256; }
-int64_t product_at(const I8Desc &W, int64_t batch) { return codes_at(batch) + (batch * W.cols + 255) / 256 * 256; }
-
-// Where whole-row wavefronts are the faster: up to four tokens, and up to eight for a
-// gated block, which gives them twice the rows, of at most 4096 (with the tokens'
-// quantisation, four tokens of 4096 x 4096 8.3 us against 9.8 of the better of the
-// others, of 28672 x 8192 gated 82 and 94; eight of 1376 x 4096 gated 10.6 and 12.1,
-// but of 4096 x 4096 11.7 and 10.0, of 11008 x 4096 gated 26.6 and 23.7).
-bool rows_pay(const I8Desc &W, bool gated, int64_t batch) {
-  return batch <= 4 || (gated && batch <= kI8RowTokens && W.rows <= 4096);
-}
-
-// Whether they also quantise x, every workgroup again, rather than a launch of its
-// own: one or two tokens (one of 4096 x 4096 5.2 us against 8.7, of 11008 x 4096 gated
-// 16.5 and 19.3, of 8192 x 28672 39 and 43, two of 4096 x 11008 12.6 and 15.3), and four where the rows are few (4096 x 4096 8.3 and 10.1, 1376 x
-// 4096 gated 7.8 and 8.9, but 11008 x 4096 gated 26 and 22).
-bool quant_pays(const I8Desc &W, bool gated, int64_t batch) {
-  return rows_pay(W, gated, batch) && i8_rows_quantize(W.cols, batch) &&
-         (batch <= 2 || W.rows * (gated ? 2 : 1) <= 8192);
-}
-
-// Modelled duration of the skinny kernel in us: 0.95 us and 0.054 us a token for each
-// turn of its wavefronts, or, with many rows, 1.6 us and 0.062 us a token for a turn of
-// 256 workgroups (fitted as the tiles: 16 x 4096 x 4096 7.2 us against their 9.5, 16 x
-// 11008 x 4096 15.8 and 13.3, 32 x 1024 x 8192 13.3 and 8.5).
-constexpr int64_t kMostSkinny = 64;  // tokens
-double skinny_us(const I8Desc &W, bool gated, int64_t batch) {
-  const double turns = (double)((W.cols + 2047) / 2048), tok_tiles = (double)((batch + 31) / 32);
-  const double tiles = (double)((W.rows + 15) / 16) * (gated ? 2 : 1) * tok_tiles;
-  const double b = (double)std::min<int64_t>(batch, 32);
-  const double alone = turns * (0.95 + 0.054 * b), full = tiles * turns / 256.0 * (1.6 + 0.062 * b);
-  return 2.6 + std::cbrt((float)(alone * alone * alone + full * full * full));
-}
-
 }  // namespace
-
-I8Route i8_route(const I8Desc &W, bool gated, int64_t batch, bool quant) {
-  I8Route r = {I8Route::kRows, quant && quant_pays(W, gated, batch), {}, 0};
-  if (r.inside) return r;
-  if (!rows_pay(W, gated, batch)) {
-    r.plan = i8_tile_plan(W.rows, W.cols, gated, batch);
-    const bool tiles = batch > kMostSkinny || r.plan.us < skinny_us(W, gated, batch);
-    r.kind = tiles ? I8Route::kTiles : I8Route::kSkinny;
-  }
-  r.ws_bytes = (quant ? product_at(W, batch) : 0) + (r.kind == I8Route::kTiles ? r.plan.sums : 0);
-  return r;
-}
 
 hipError_t launch_i8_product(const I8Product &p, const I8Route &route, void *ws, hipStream_t stream) {
   I8Args A = {{p.W.codes, p.up.codes}, {p.W.scales, p.up.scales}, p.xcodes, p.xscales,
@@ -152,12 +102,12 @@ hipError_t launch_i8_product(const I8Product &p, const I8Route &route, void *ws,
   if (route.inside) return launch_i8_rows(A, p.x, p.type, p.gated(), stream);
   if (p.x) {
     float *scales = static_cast<float *>(ws);
-    int8_t *codes = static_cast<int8_t *>(ws) + codes_at(p.batch);
+    int8_t *codes = static_cast<int8_t *>(ws) + i8_codes_at(p.batch);
     const hipError_t e = launch_i8_quantize(p.x, p.type, p.batch, p.W.cols, codes, scales, stream);
     if (e != hipSuccess) return e;
     A.x = codes;
     A.xs = scales;
-    ws = static_cast<uint8_t *>(ws) + product_at(p.W, p.batch);
+    ws = static_cast<uint8_t *>(ws) + i8_product_at(p.W.cols, p.batch);
   }
   if (route.kind == I8Route::kRows) return launch_i8_rows(A, nullptr, p.type, p.gated(), stream);
   if (route.kind == I8Route::kTiles) return launch_i8_tile(A, route.plan, p.type, p.gated(), ws, stream);

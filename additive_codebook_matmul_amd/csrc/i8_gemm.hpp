@@ -47,12 +47,9 @@ __device__ __forceinline__ void i8_store4(const I8Args &A, int tok, int row, con
 // Few tokens by whole rows of W (i8_rows.hip), up to four of a layer and kI8RowTokens
 // of a gated block; x: halves to be quantised on
 // the way, for sizes that i8_rows_quantize takes, or null where A.x and A.xs are given.
-constexpr int kI8RowTokens = 8;
-bool i8_rows_quantize(int64_t cols, int64_t batch);
 hipError_t launch_i8_rows(const I8Args &A, const void *x, MxType type, bool gated, hipStream_t stream);
 
 // The tile kernels (i8_tile.hip).
-I8Plan i8_tile_plan(int64_t rows, int64_t cols, bool gated, int64_t batch);
 hipError_t launch_i8_tile(const I8Args &A, const I8Plan &p, MxType type, bool gated, void *ws, hipStream_t stream);
 
 }  // namespace aqlm

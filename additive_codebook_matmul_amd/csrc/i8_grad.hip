@@ -18,7 +18,6 @@
 // codes and gradients (gated 700 and 516): 1.1 PFLOP/s of float16 instructions. (The
 // library's product of float16 matrices, half as many, 211.)
 #include <algorithm>
-#include <cmath>
 
 #include "i8_device.hpp"
 #include "mx_tile.hpp"
@@ -228,20 +227,6 @@ struct I8GradArgs {
   float4_t *part;     // [splits][tiles][RT * NT * 4][64 RW TW], or null
   int rows, part_rows, ld, cols, batch, matrices;
   int col_tiles, tok_tiles, splits, steps_per_split;
-};
-
-// RW x TW wavefronts of RT x NT 32 x 32 tiles, KW such sets that share K.
-template <int RT_, int NT_, int RW_, int TW_, int KW_, int STAGES_> struct Shape {
-  static constexpr int RT = RT_, NT = NT_, RW = RW_, TW = TW_, KW = KW_, STAGES = STAGES_;
-  static constexpr int kWaves = RW * TW, kThreads = 64 * kWaves;  // of one share of K
-  static constexpr int kCols = 32 * RT * RW, kToks = 32 * NT * TW;
-  static constexpr int kWBytes = 64 * kCols, kXBytes = kToks * 128, kStage = kWBytes + 2 * kXBytes;
-  static constexpr int kSums = kCols * kToks * 4;
-  // LDS bytes of a stage's array: the stage, the shares' sums in the first one, the
-  // results in the second (and third: half of the wavefronts each)
-  static constexpr int kStore = RT * 2048;  // a wavefront's results
-  static constexpr int kArray = std::max({KW * kStage, KW > 1 ? kSums : 0, kWaves * kStore / (STAGES > 2 ? 2 : 1)});
-  static constexpr int kSlots = 256 * (160 * 1024 / (STAGES * kArray));  // workgroups the chip holds
 };
 
 // Where chunk c of row r of the codes lies: c ^ turn.
@@ -570,30 +555,6 @@ __global__ __launch_bounds__(S::kThreads) void i8_grad_sum_kernel(const I8GradAr
   store4<T>(A.dx + (int64_t)tok * A.cols, col, A.cols, v, true);
 }
 
-typedef Shape<2, 2, 4, 2, 1, 3> Large;   // 256 columns x 128 tokens
-typedef Shape<2, 1, 4, 2, 1, 2> Half;    // 256 x 64
-typedef Shape<2, 1, 2, 1, 2, 2> Small;   // 128 x 32
-
-// Tile of a product and the workgroups K is split over, chosen as for the int8
-// products (i8_tile.hip) but for c us more a step from where CUs hold two workgroups:
-// reading at 5.3 TB/s, products at 0.7 PFLOP/s, sums of splits at 4.8 TB/s. Fitted to eight
-// layers from 1 to 2048 tokens, each shape and 1, 2, 4 and 8 splits measured at each,
-// within 5 % at the median; the choice costs 0.3 % on average against the best one.
-// (Each shape with its best splits, terms' launch included, Large to Small: 301 x 4096 x
-// 11008 94, 72 and 95 us, 2048 x 11008 x 4096 348, 374, 486, 333 x 1376 x 4096 30, 27, 22, 1
-// x 28672 x 8192 92, 70, 58. Tiles of 128 x 64, by two or four wavefronts, and 256 x 64 by
-// four would spare 0.1 % of the choice's time.)
-struct GradCost {
-  int cols, toks, kw, sums;  // sums: bytes of a workgroup's in the workspace
-  int slots;                 // workgroups the chip holds at a time
-  double f, a, b, c;
-};
-template <class S> constexpr GradCost cost_of(double f, double a, double b, double c) {
-  return {S::kCols, S::kToks, S::KW, S::kSums, S::kSlots, f, a, b, c};
-}
-constexpr GradCost kCosts[] = {cost_of<Large>(0.07, 1.317, 0.0, 0.0), cost_of<Half>(0.55, 0.841, 0.247, 0.522),
-                               cost_of<Small>(1.28, 0.736, 0.465, 0.185)};
-
 template <MxType T, class S> hipError_t launch_shape(const I8GradArgs &A, hipStream_t stream) {
   const unsigned tiles = (unsigned)(A.col_tiles * A.tok_tiles);
   hipLaunchKernelGGL((i8_grad_kernel<T, S>), dim3(tiles * A.splits), dim3(S::kThreads * S::KW), 0, stream, A);
@@ -602,66 +563,24 @@ template <MxType T, class S> hipError_t launch_shape(const I8GradArgs &A, hipStr
   return hipGetLastError();
 }
 
-// Rows of one matrix in D: whole steps.
-int64_t part_of(const I8Desc &W) { return (W.rows + 63) / 64 * 64; }
-// Workspace: the powers, D and the split sums, from multiples of 256 bytes on.
-int64_t terms_at(int64_t batch) { return (batch * 4 + 255) / 256 * 256; }
-int64_t sums_at(const I8Desc &W, bool gated, int64_t batch) {
-  return terms_at(batch) + (batch * part_of(W) * (gated ? 2 : 1) * 4 + 255) / 256 * 256;
-}
-
 template <MxType T> hipError_t grad_as(const I8Grad &p, const I8Plan &g, void *ws, hipStream_t stream) {
-  const int part = (int)part_of(p.W), ld = 2 * part * (p.gated() ? 2 : 1);
+  const int part = (int)i8_term_rows(p.W.rows), ld = 2 * part * (p.gated() ? 2 : 1);
   int *const power = static_cast<int *>(ws);
-  uint16_t *const d = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + terms_at(p.batch));
+  uint16_t *const d = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + i8_terms_at(p.batch));
   const I8GradRowsArgs R = {p.dy, p.g, p.u, {p.W.scales, p.up.scales}, d, power, (int)p.W.rows, part, ld, p.act};
   if (p.gated()) launch_terms<T, true>(R, p.batch, stream);
   else launch_terms<T, false>(R, p.batch, stream);
-  float4_t *const sums = reinterpret_cast<float4_t *>(static_cast<uint8_t *>(ws) + sums_at(p.W, p.gated(), p.batch));
+  float4_t *const sums = reinterpret_cast<float4_t *>(static_cast<uint8_t *>(ws) + i8_grad_sums_at(p.W.rows, p.gated(), p.batch));
   const I8GradArgs A = {{p.W.codes, p.up.codes}, d, power, static_cast<uint16_t *>(p.dx), sums, (int)p.W.rows, part, ld,
                         (int)p.W.cols, (int)p.batch, p.gated() ? 2 : 1, (int)g.across, (int)g.tok_tiles, g.splits,
                         g.steps_per_split};
+  using namespace i8_grad;  // (in the order of its costs)
   if (g.shape == 0) return launch_shape<T, Large>(A, stream);
   if (g.shape == 1) return launch_shape<T, Half>(A, stream);
   return launch_shape<T, Small>(A, stream);
 }
 
 }  // namespace
-
-I8Plan i8_grad_plan(const I8Desc &W, bool gated, int64_t batch) {
-  I8Plan best{};
-  const int steps = (int)((W.rows + 63) / 64) * (gated ? 2 : 1);
-  const double codes = (double)W.rows * (gated ? 2 : 1) * (double)W.cols;
-  const double read = codes / 5.3e6, power = 2.0 * codes * (double)batch / 0.7e9;
-  const double bounds = read * read * read + power * power * power;
-  for (int c = 0; c < (int)(sizeof(kCosts) / sizeof(kCosts[0])); ++c) {
-    const GradCost &k = kCosts[c];
-    I8Plan p{};
-    p.shape = c;
-    p.across = (W.cols + k.cols - 1) / k.cols;
-    p.tok_tiles = (batch + k.toks - 1) / k.toks;
-    const int64_t tiles = p.across * p.tok_tiles;
-    for (int s = 1; s <= 8; ++s) {
-      p.steps_per_split = (steps + s - 1) / s;
-      p.splits = (steps + p.steps_per_split - 1) / p.steps_per_split;
-      if (p.splits != s || (s > 1 && tiles * s > 512)) break;
-      const double whole = (double)(tiles * s / k.slots), rest = (double)(tiles * s % k.slots) / (double)k.slots;
-      const double turns = (double)((p.steps_per_split + k.kw - 1) / k.kw);
-      const double last = rest > 0 ? k.f + turns * (k.a + k.b * rest + (rest > 0.5 ? k.c : 0.0)) : 0.0;
-      const double tile_us = whole * (k.f + turns * (k.a + k.b + k.c)) + last;
-      p.sums = s > 1 ? tiles * s * k.sums : 0;
-      const double around = s > 1 ? 2.3 + (double)p.sums * (2.0 / 4.8e6) : 0.0;
-      if (best.splits != 0 && tile_us + around >= best.us) continue;  // (spares the root)
-      p.us = around + std::cbrt((float)(tile_us * tile_us * tile_us + bounds));
-      if (best.splits == 0 || p.us < best.us) best = p;
-    }
-  }
-  return best;
-}
-
-int64_t i8_grad_ws_bytes(const I8Desc &W, bool gated, int64_t batch, const I8Plan &plan) {
-  return sums_at(W, gated, batch) + plan.sums;
-}
 
 hipError_t launch_i8_grad(const I8Grad &p, const I8Plan &plan, void *ws, hipStream_t stream) {
   return p.type == MxType::kF16 ? grad_as<MxType::kF16>(p, plan, ws, stream)

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "i8_plan.hpp"
 #include "mx_internal.hpp"
 
 namespace aqlm {
@@ -23,14 +24,6 @@ hipError_t launch_i8_quantize(const void *x, MxType type, int64_t rows, int64_t 
                               float *scales, hipStream_t stream);
 hipError_t launch_i8_dequant(const I8Desc &m, MxType type, void *W, hipStream_t stream);
 
-// How a tile kernel does a product or a gradient.
-struct I8Plan {
-  int shape, splits, steps_per_split;
-  int64_t across, tok_tiles;  // tiles of W's rows (a gradient: of its columns), and of tokens
-  int64_t sums;               // bytes of the split parts' sums in the workspace
-  double us;                  // modelled duration
-};
-
 // A product of one layer, or the two of a gated block (up.codes not null).
 struct I8Product {
   I8Desc W;   // the layer, or the gate
@@ -45,15 +38,6 @@ struct I8Product {
   MxType type;
   bool gated() const { return up.codes != nullptr; }
 };
-// The kernels of a product (`quant`: x is halves), by its sizes: chosen once a call,
-// since a choice takes the host a microsecond.
-struct I8Route {
-  enum Kind { kRows, kSkinny, kTiles } kind;
-  bool inside;  // the product's own workgroups quantise x
-  I8Plan plan;  // kTiles
-  int64_t ws_bytes;
-};
-I8Route i8_route(const I8Desc &W, bool gated, int64_t batch, bool quant);
 hipError_t launch_i8_product(const I8Product &p, const I8Route &route, void *ws, hipStream_t stream);
 
 // The gradient with respect to the activations: of a layer (up.codes null, g
@@ -68,8 +52,6 @@ struct I8Grad {
   MxType type;
   bool gated() const { return up.codes != nullptr; }
 };
-I8Plan i8_grad_plan(const I8Desc &W, bool gated, int64_t batch);
-int64_t i8_grad_ws_bytes(const I8Desc &W, bool gated, int64_t batch, const I8Plan &plan);
 hipError_t launch_i8_grad(const I8Grad &p, const I8Plan &plan, void *ws, hipStream_t stream);
 
 }  // namespace aqlm

@@ -17,7 +17,7 @@
 namespace aqlm {
 namespace {
 
-constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kThreads = kI8RowThreads, kWaves = kThreads / 64;
 constexpr int kMostLds = 65536;  // bytes of codes in LDS
 
 // Bytes of codes of a token in LDS: all of them in whole chunks where they fit.
@@ -221,11 +221,6 @@ template <MxType T, bool GATED> hipError_t rows_as(const I8Args &A, const void *
 }
 
 }  // namespace
-
-bool i8_rows_quantize(int64_t cols, int64_t batch) {
-  const int64_t most = batch == 1 ? 8 : batch == 2 ? 4 : 1;  // octets of a token a thread holds
-  return batch <= 4 && cols / 8 <= most * kThreads;
-}
 
 hipError_t launch_i8_rows(const I8Args &A, const void *x, MxType type, bool gated, hipStream_t stream) {
   if (type == MxType::kF16)

@@ -18,9 +18,6 @@
 // for 57 % of the cycles, LDS for 24 to 30. 1999 x 4096 x 11008 takes 85 us, 2048 x 11008 x
 // 4096 gated 186. With few tokens the reading of W: 19 x 28672 x 8192 gated 72 us, 6.5
 // TB/s.
-#include <algorithm>
-#include <cmath>
-
 #include "i8_gemm.hpp"
 #include "mx_tile.hpp"
 
@@ -41,15 +38,6 @@ __device__ __forceinline__ uint32_t row_off(int r, int c) {
 __device__ __forceinline__ int4_vt quarter_of(const int16_vt &v, int q) {
   return int4_vt{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
 }
-
-// RW x TW wavefronts of RT x NT 32 x 32 tiles, KW such sets that share K.
-template <int RT_, int NT_, int RW_, int TW_, int KW_, int STAGES_> struct Shape {
-  static constexpr int RT = RT_, NT = NT_, RW = RW_, TW = TW_, KW = KW_, STAGES = STAGES_;
-  static constexpr int kWaves = RW * TW, kThreads = 64 * kWaves;  // of one share of K
-  static constexpr int kRows = 32 * RT * RW, kToks = 32 * NT * TW;
-  static constexpr int kWBytes = kRows * 128, kStage = kWBytes + kToks * 128;
-  static constexpr int kSums = kRows * kToks * 4;
-};
 
 // ONCE: the tile's rows are read by this workgroup alone (one tile of tokens), past
 // the caches.
@@ -411,39 +399,6 @@ __global__ __launch_bounds__(S::kThreads) void i8_tile_sum_kernel(const I8TileAr
   i8_store4<T, GATED>(A, tok, row, v);
 }
 
-typedef Shape<4, 2, 2, 4, 1, 2> Large;    // 256 rows x 256 tokens
-typedef Shape<2, 3, 4, 2, 1, 2> Wide;     // 256 x 192
-typedef Shape<2, 2, 4, 2, 1, 3> Middle;   // 256 x 128
-typedef Shape<2, 1, 4, 2, 1, 3> Half;     // 256 x 64
-typedef Shape<2, 2, 2, 1, 2, 3> Small;    // 128 x 64
-typedef Shape<2, 1, 2, 1, 2, 3> Slim;     // 128 x 32
-typedef Shape<2, 1, 1, 1, 2, 3> Least;    // 64 x 32, two workgroups to a CU
-
-// Tile of a product and the workgroups K is split over: the choice with the
-// shortest modelled time. The grid runs in rounds of as many workgroups as the chip
-// holds (`slots`); a round takes f us, and a + b * (its share of the slots) us for
-// each step of a share of K. That, the reading of W at 5.3 TB/s and the products at
-// 2.2 POP/s, where the power limit holds the clock, are joined as a cube root of
-// cubes, 2.3 us pass around them, and a split launches a second kernel and writes and
-// reads its sums at 5.9 TB/s. Fitted to eight layers (1024 x 8192 to 22016 x 4096, 8192
-// x 28672) from 9 to 2048 tokens, each shape and split measured at each, within 6 %
-// at the median; the choice costs 2.5 % on average against the best one.
-// (Each shape with its best splits, Large to Least: 64 x 8192 x 28672 60, 58, 49, 46,
-// 47, 60 and 64 us, 301 x 11008 x 4096 43, 41, 31, 28, 40, 52, 51, 2048 x 4096 x 11008
-// 116, 123, 91, 133, 195, 251, 245, 16 x 4096 x 4096 14, 13, 11, 10.5, 12, 9.7, 8.9.)
-struct I8ShapeCost {
-  int rows, toks, kw, sums;  // sums: bytes of a workgroup's in the workspace
-  int slots;
-  double f, a, b;
-};
-template <class S> constexpr I8ShapeCost cost_of(double f, double a, double b) {
-  return {S::kRows, S::kToks, S::KW, S::kSums, 256 * (160 * 1024 / (S::STAGES * S::KW * S::kStage)), f, a, b};
-}
-constexpr I8ShapeCost kCosts[] = {cost_of<Large>(2.52, 1.276, 0.0),    cost_of<Wide>(2.0, 1.171, 0.0),
-                                  cost_of<Middle>(2.41, 0.708, 0.151), cost_of<Half>(2.14, 0.612, 0.09),
-                                  cost_of<Small>(3.2, 0.823, 0.171),   cost_of<Slim>(2.22, 0.583, 0.093),
-                                  cost_of<Least>(2.05, 0.349, 0.366)};
-
 template <MxType T, bool GATED, class S> hipError_t launch_shape(const I8TileArgs &B, hipStream_t stream) {
   const unsigned tiles = (unsigned)(B.row_tiles * B.tok_tiles);
   const dim3 grid(tiles * B.splits), block(S::kThreads * S::KW);
@@ -457,6 +412,7 @@ template <MxType T, bool GATED, class S> hipError_t launch_shape(const I8TileArg
 }
 
 template <MxType T, bool GATED> hipError_t tile_as(int shape, const I8TileArgs &B, hipStream_t stream) {
+  using namespace i8_tile;  // (in the order of its costs)
   if (shape == 0) return launch_shape<T, GATED, Large>(B, stream);
   if (shape == 1) return launch_shape<T, GATED, Wide>(B, stream);
   if (shape == 2) return launch_shape<T, GATED, Middle>(B, stream);
@@ -467,38 +423,6 @@ template <MxType T, bool GATED> hipError_t tile_as(int shape, const I8TileArgs &
 }
 
 }  // namespace
-
-I8Plan i8_tile_plan(int64_t rows, int64_t cols, bool gated, int64_t batch) {
-  I8Plan best{};
-  const int steps = (int)((cols + 127) / 128);
-  const double all_rows = (double)rows * (gated ? 2 : 1);
-  const double read = all_rows * (double)cols / 5.3e6, power = 2.0 * all_rows * (double)cols * (double)batch / 2.2e9;
-  const double bounds = read * read * read + power * power * power;
-  for (int c = 0; c < (int)(sizeof(kCosts) / sizeof(kCosts[0])); ++c) {
-    const I8ShapeCost &k = kCosts[c];
-    I8Plan p{};
-    p.shape = c;
-    const int out = gated ? k.rows / 2 : k.rows;
-    p.across = (rows + out - 1) / out;
-    p.tok_tiles = (batch + k.toks - 1) / k.toks;
-    const int64_t tiles = p.across * p.tok_tiles;
-    for (int s = 1; s <= 8; ++s) {
-      p.steps_per_split = (steps + s - 1) / s;
-      p.splits = (steps + p.steps_per_split - 1) / p.steps_per_split;
-      if (p.splits != s || (s > 1 && tiles * s > k.slots)) break;
-      const int64_t rounds = tiles * s < k.slots ? 0 : tiles * s / k.slots;
-      const double whole = (double)rounds, rest = (double)(tiles * s - rounds * k.slots) / (double)k.slots;
-      const double turns = (double)(k.kw == 1 ? p.steps_per_split : (p.steps_per_split + k.kw - 1) / k.kw);
-      const double us = whole * (k.f + turns * (k.a + k.b)) + (rest > 0 ? k.f + turns * (k.a + k.b * rest) : 0.0);
-      p.sums = s > 1 ? tiles * s * k.sums : 0;
-      const double around = s > 1 ? 4.0 + (double)p.sums * (2.0 / 5.9e6) : 2.3;
-      if (best.splits != 0 && us + around >= best.us) continue;  // (spares the root)
-      p.us = around + std::cbrt((float)(us * us * us + bounds));
-      if (best.splits == 0 || p.us < best.us) best = p;
-    }
-  }
-  return best;
-}
 
 hipError_t launch_i8_tile(const I8Args &A, const I8Plan &p, MxType type, bool gated, void *ws, hipStream_t stream) {
   const I8TileArgs B = {A, static_cast<int4_vt *>(ws), (int)p.across, (int)p.tok_tiles, p.splits, p.steps_per_split};
