@@ -153,6 +153,15 @@ __device__ __forceinline__ float materialize(float v) {
   return v;
 }
 
+// Between a wavefront's writes to LDS and the reads of other lanes' places, and before the
+// next writes there. The hardware keeps a wavefront's LDS accesses in order; this keeps the
+// compiler, which sees one lane's addresses, from moving one across. No instruction.
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Exact decode of one weight from its codewords' halves: float32 sum in
 // ascending codebook order starting from the first codeword, float32 scale,
 // one round to float16.

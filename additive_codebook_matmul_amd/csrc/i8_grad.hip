@@ -516,6 +516,7 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
         *reinterpret_cast<uint2 *>(mine + (l32 * kChunks + c) * 16 + 8 * h) =
             make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
       }
+    wave_exchange();
 #pragma unroll
     for (int k = 0; k < kChunks / 2; ++k) {
       const int id = 64 * k + lane, tt = id / kChunks, c = id % kChunks;
@@ -523,6 +524,7 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
       const int tok = wtok0 + 32 * j + tt, col = wcol0 + 8 * c;
       if (tok < A.batch && col < A.cols) *reinterpret_cast<uint4 *>(A.dx + (int64_t)tok * A.cols + col) = r;
     }
+    wave_exchange();
   }
 }
 

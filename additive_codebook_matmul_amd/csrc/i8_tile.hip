@@ -319,6 +319,7 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
           *reinterpret_cast<uint2 *>(mine + (l32 * kChunks + c) * 16 + 8 * h) =
               make_uint2(f2t<T>(o[0]) | (f2t<T>(o[1]) << 16), f2t<T>(o[2]) | (f2t<T>(o[3]) << 16));
         }
+      wave_exchange();
 #pragma unroll
       for (int k = 0; k < kChunks / 2; ++k) {
         const int id = 64 * k + lane, tt = id / kChunks, c = id % kChunks;
@@ -326,6 +327,7 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
         const int tok = tokj + tt, row = wrow0 + 8 * c;
         if (tok < A.batch && row < A.rows) *reinterpret_cast<uint4 *>(A.y + (int64_t)tok * A.rows + row) = r;
       }
+      wave_exchange();
     } else if (tokj + l32 < A.batch) {
 #pragma unroll
       for (int i = 0; i < OT; ++i)
@@ -345,6 +347,7 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               *reinterpret_cast<float4_t *>(mine + l32 * 128 + (((2 * q + h) ^ (l32 & 7)) << 4)) = v[m][i][q];
+            wave_exchange();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int tt = 8 * k + (lane >> 3), c = lane & 7;
@@ -353,6 +356,7 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
               if (tok < A.batch && row < A.rows)
                 *reinterpret_cast<float4_t *>(to + (int64_t)tok * A.rows + row) = r;
             }
+            wave_exchange();
           } else if (tokj + l32 < A.batch) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)

@@ -216,6 +216,7 @@ __device__ __forceinline__ void store_tile(const TileArgs &A, const float16_t (&
               make_uint2(f2t<T>(acc[i][j][4 * q]) | (f2t<T>(acc[i][j][4 * q + 1]) << 16),
                          f2t<T>(acc[i][j][4 * q + 2]) | (f2t<T>(acc[i][j][4 * q + 3]) << 16));
         }
+      wave_exchange();
 #pragma unroll
       for (int k = 0; k < kChunks / 2; ++k) {
         const int id = 64 * k + lane, tt = id / kChunks, c = id % kChunks;
@@ -224,6 +225,7 @@ __device__ __forceinline__ void store_tile(const TileArgs &A, const float16_t (&
         if (tok < A.batch && row < A.rows)
           *reinterpret_cast<uint4 *>(A.y + (int64_t)tok * A.rows + row) = v;
       }
+      wave_exchange();
     }
     return;
   }
