@@ -15,7 +15,10 @@ fallback: a missing library or a failing call raises.
     y = down.forward(h)
 
 Under autograd an x that requires a gradient gets it, straight through the
-quantisation of the activations. The weights are constants. (As with torch's own
+quantisation of the activations: I8Layer.forward and I8Gated.forward are recorded.
+The weights are constants. What quantisation, expansion, gemm_i8, forward_saving and
+grad_input return is outside autograd. Forward-mode derivatives are not computed: a
+tensor that carries a tangent is refused. (As with torch's own
 operations, a backward pass that is captured into a HIP graph must meet no eager
 graph of the same leaves that is still alive: torch then accumulates into them on
 the eager graph's stream.)
@@ -98,7 +101,7 @@ def i8_quantize(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]
     """(codes [rows, cols] int8, scales [rows] float32) of a dense matrix.
 
     x is float16, bfloat16 or float32, cols a multiple of 16. A row's largest
-    magnitude becomes 127 or -127."""
+    magnitude becomes 127 or -127. Not recorded by autograd."""
     _check_dense(x, "x", tuple(I8_TYPES))
     rows, cols = x.shape
     if cols < 16 or cols % 16:
@@ -116,7 +119,8 @@ def i8_quantize(x: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]
 
 def i8_dequant(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.float16,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """The dense [rows, cols] matrix of an int8 one, in float16, bfloat16 or float32."""
+    """The dense [rows, cols] matrix of an int8 one, in float16, bfloat16 or float32. Not recorded
+    by autograd."""
     rows, cols = _check_packed(codes, scales)
     if dtype not in I8_TYPES:
         raise ValueError("dtype must be float16, bfloat16 or float32")

@@ -13,7 +13,9 @@ fallback: a missing library or a failing call raises.
 
 Under autograd an x that requires a gradient gets it: forward, forward_mx, gemm,
 gemv and mx_gemv_batched are recorded with grad_input as their backward
-(forward_mx: straight through the quantisation). The weights are constants.
+(forward_mx: straight through the quantisation). The weights are constants. What
+quantisation, expansion, gemm_mx and grad_input return is outside autograd. Forward-mode
+derivatives are not computed: a tensor that carries a tangent is refused.
 """
 from __future__ import annotations
 
@@ -22,6 +24,7 @@ import struct
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from ._lib import _check, load_library
@@ -97,6 +100,9 @@ def _check_dense(t: torch.Tensor, what: str, dtypes, shape=None) -> None:
         raise ValueError(f"{what} must be a contiguous 2-D tensor on the GPU, of type {names}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
+    # (the level is the quick question, where the installed torch answers it)
+    if getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{what} carries a forward-mode tangent, which would be lost")
 
 
 def _check_packed(codes: torch.Tensor, scales: torch.Tensor) -> Tuple[int, int]:
