@@ -19,7 +19,7 @@
 // library's product of float16 matrices, half as many, 211.)
 #include <algorithm>
 
-#include "i8_device.hpp"
+#include "i8_tile.hpp"
 #include "mx_tile.hpp"
 
 namespace aqlm {
@@ -453,78 +453,22 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_grad_kernel(const I8Gra
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   __syncthreads();
 
-  if constexpr (KW > 1) {  // the shares' sums, in order
-    auto slot = [&](int i, int j, int q) __attribute__((always_inline)) {
-      return reinterpret_cast<float4_t *>(s0 + ((((i * NT + j) * 4 + q) * kWaves + wave) * 64 + lane) * 16);
-    };
-#pragma unroll 1
-    for (int k = 1; k < KW; ++k) {
-      if (k > 1) __syncthreads();
-      if (kw == k) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) *slot(i, j, q) = quarter(acc[i][j], q);
-      }
-      __syncthreads();
-      if (kw == 0) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4_t v = *slot(i, j, q);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
-            }
-      }
-    }
-    if (kw != 0) return;
-  }
+  if (i8_join_shares<S>(acc, kw, wave, lane, s0)) return;
+  if (A.splits > 1) return i8_store_part<S>(acc, A.part, job, wave, lane, wtok0, A.batch);
 
-  if (A.splits > 1) {
-    float4_t *p = A.part + (int64_t)job * (RT * NT * 4 * S::kThreads) + wave * 64 + lane;
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (wtok0 + 32 * j + l32 < A.batch) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) p[((i * NT + j) * 4 + q) * S::kThreads] = quarter(acc[i][j], q);
-        }
-    return;
-  }
-  // Register 4 q + e of a 32 x 32 tile is column 8 q + 4 h + e, token l32. The results
-  // pass through LDS, 32 tokens at a time, from where neighbouring lanes store a
-  // token's columns (a multiple of 16).
-  constexpr int kChunks = 4 * RT;  // of 16 bytes, eight columns, for a token
+  // 32 tokens of the wavefront at a time (columns are a multiple of 16)
   uint8_t *const mine = S::STAGES == 2 ? s1 + wave * S::kStore
                                        : (wave & 1 ? s2 : s1) + (wave >> 1) * S::kStore;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
+    float4_t out[RT][4];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t o[4];
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = f2t<T>(materialize(__builtin_amdgcn_ldexpf(acc[i][j][4 * q + e], power[j])));
-        const int c = (4 * i + q) ^ (l32 & (kChunks - 1));
-        *reinterpret_cast<uint2 *>(mine + (l32 * kChunks + c) * 16 + 8 * h) =
-            make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
-      }
-    wave_exchange();
-#pragma unroll
-    for (int k = 0; k < kChunks / 2; ++k) {
-      const int id = 64 * k + lane, tt = id / kChunks, c = id % kChunks;
-      const uint4 r = *reinterpret_cast<const uint4 *>(mine + (tt * kChunks + (c ^ (tt & (kChunks - 1)))) * 16);
-      const int tok = wtok0 + 32 * j + tt, col = wcol0 + 8 * c;
-      if (tok < A.batch && col < A.cols) *reinterpret_cast<uint4 *>(A.dx + (int64_t)tok * A.cols + col) = r;
-    }
-    wave_exchange();
+        for (int e = 0; e < 4; ++e) out[i][q][e] = materialize(__builtin_amdgcn_ldexpf(acc[i][j][4 * q + e], power[j]));
+    i8_store_lines<T>(out, mine, lane, A.dx, wtok0 + 32 * j, wcol0, A.batch, A.cols);
   }
 }
 
@@ -542,15 +486,7 @@ __global__ __launch_bounds__(S::kThreads) void i8_grad_sum_kernel(const I8GradAr
   if (tok >= A.batch || col >= A.cols) return;
   const float4_t *p = A.part + ((int64_t)tile * (RT * NT * 4) + slot) * S::kThreads + tid;
   const int64_t stride = (int64_t)tiles * (RT * NT * 4) * S::kThreads;
-  float4_t v = p[0];
-  for (int s = 1; s < A.splits; s += 4) {  // four loads under way
-    float4_t u[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) u[k] = p[min(s + k, A.splits - 1) * stride];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (s + k < A.splits) v += u[k];
-  }
+  float4_t v = i8_sum_parts(p, stride, A.splits);
   const int power = A.power[tok];
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = materialize(__builtin_amdgcn_ldexpf(v[e], power));

@@ -19,6 +19,7 @@
 // 4096 gated 186. With few tokens the reading of W: 19 x 28672 x 8192 gated 72 us, 6.5
 // TB/s.
 #include "i8_gemm.hpp"
+#include "i8_tile.hpp"
 #include "mx_tile.hpp"
 
 namespace aqlm {
@@ -33,10 +34,6 @@ struct I8TileArgs {
 // Byte offset of chunk c (of 8) of row r in its part of a stage.
 __device__ __forceinline__ uint32_t row_off(int r, int c) {
   return (uint32_t)r * 128u + (uint32_t)((c ^ ((r >> 1) & 7)) << 4);
-}
-
-__device__ __forceinline__ int4_vt quarter_of(const int16_vt &v, int q) {
-  return int4_vt{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
 }
 
 // ONCE: the tile's rows are read by this workgroup alone (one tile of tokens), past
@@ -235,56 +232,10 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
   if ((int)threadIdx.x < S::kRows) scales[threadIdx.x] = channel;
   if constexpr (KW == 1) __syncthreads();
 
-  if constexpr (KW > 1) {  // whole numbers: any order gives the same
-    static_assert(S::kSums <= kArray, "room for the sums");
-    auto slot = [&](int i, int j, int q) __attribute__((always_inline)) {
-      return reinterpret_cast<int4_vt *>(s0 + ((((i * NT + j) * 4 + q) * kWaves + wave) * 64 + lane) * 16);
-    };
-#pragma unroll 1
-    for (int k = 1; k < KW; ++k) {
-      if (k > 1) __syncthreads();
-      if (kw == k) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) *slot(i, j, q) = quarter_of(acc[i][j], q);
-      }
-      __syncthreads();
-      if (kw == 0) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int4_vt v = *slot(i, j, q);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
-            }
-      }
-    }
-    if (kw != 0) return;
-  }
+  if (i8_join_shares<S>(acc, kw, wave, lane, s0)) return;  // (whole numbers: any order gives the same)
+  if (B.splits > 1) return i8_store_part<S>(acc, B.part, job, wave, lane, wtok0, A.batch);
 
-  if (B.splits > 1) {
-    int4_vt *p = B.part + (int64_t)job * (RT * NT * 4 * S::kThreads) + wave * 64 + lane;
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (wtok0 + 32 * j + l32 < A.batch) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) p[((i * NT + j) * 4 + q) * S::kThreads] = quarter_of(acc[i][j], q);
-        }
-    return;
-  }
-
-  // Register 4 q + e of a 32 x 32 tile is row 8 q + 4 h + e, token l32, so a lane's
-  // values are four rows apart from the next lane's token. They pass through LDS, 32
-  // tokens at a time, from where neighbouring lanes store a token's rows: 8-byte
-  // stores from the registers left 16 of 64 bytes a line and took 12 to 15 us.
+  // 32 tokens of the wavefront at a time
   uint8_t *const mine = s1 + wave * kStore;
   const bool lines = (A.rows & 7) == 0;
 #pragma unroll
@@ -309,6 +260,7 @@ __global__ __launch_bounds__(S::kThreads *S::KW) void i8_tile_kernel(const I8Til
         }
       }
     if (lines) {
+      // (i8_store_lines, here in place: as a call it costs the gated 256 x 256 tile spills)
       constexpr int kChunks = 4 * OT;  // of 16 bytes, eight rows, for a token
 #pragma unroll
       for (int i = 0; i < OT; ++i)
@@ -390,15 +342,7 @@ __global__ __launch_bounds__(S::kThreads) void i8_tile_sum_kernel(const I8TileAr
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     const int4_vt *p = B.part + ((int64_t)tile * (S::RT * NT * 4) + ((i + m * OT) * NT + j) * 4 + q) * S::kThreads + tid;
-    v[m] = p[0];
-    for (int s = 1; s < B.splits; s += 4) {  // four loads under way
-      int4_vt u[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) u[k] = p[min(s + k, B.splits - 1) * stride];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (s + k < B.splits) v[m] += u[k];
-    }
+    v[m] = i8_sum_parts(p, stride, B.splits);
   }
   i8_store4<T, GATED>(A, tok, row, v);
 }

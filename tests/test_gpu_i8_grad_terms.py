@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from additive_codebook_matmul_amd import I8Gated
+from additive_codebook_matmul_amd import I8Gated, I8Layer
 from oracle import i8_oracle as IO
 from test_gpu_i8 import ACTS, half, layer_of, weights
 from test_gpu_mx import DEV, HALVES, dev, guarded, rounded, same
@@ -120,3 +120,24 @@ def test_terms_far_below_the_largest(batch):
     got = layer_of(w).grad_input(dy.to(DEV)).cpu().double().numpy()
     off = np.abs(ref) * (2.0 ** -23 + 2.0 ** -24 + 2.0 ** -22) + 128 * np.abs(terms).max(axis=1, keepdims=True) * 2.0 ** -50
     assert (np.abs(got - ref) <= (np.abs(ref) + off) * 2.0 ** -8 + off).all()
+
+
+@pytest.mark.parametrize("batch,n_in", [(3, 16), (140, 16), (250, 4096)])
+def test_the_most_rows_of_a_gated_block(batch, n_in):
+    """With 4096 columns the tile is of 128 tokens, whose terms are 2^31 bytes. One 1 in each token's gradient (and
+    a 2 in its last place): a result is a sum of four codes, exactly."""
+    out = 1 << 21
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(batch)
+    gate, up = (torch.randint(-127, 128, (out, n_in), generator=gen, device=DEV, dtype=torch.int8) for _ in range(2))
+    dh = torch.zeros((batch, out), dtype=torch.float16, device=DEV)
+    at = torch.randint(0, out - 1, (batch,), generator=gen, device=DEV)
+    dh.scatter_(1, at[:, None], 1.0)
+    dh[:, out - 1] = 2.0
+    g, u = torch.full((batch, out), 64.0, device=DEV), torch.full((batch, out), 3.0, device=DEV)
+    one = torch.ones(out, device=DEV)
+    dx = I8Gated(I8Layer(gate, one), I8Layer(up, one / 64), "silu").grad_input(dh, g, u)
+    want = 3 * (gate[at].float() + 2 * gate[out - 1].float()) + up[at].float() + 2 * up[out - 1].float()
+    assert torch.equal(dx, want.half())
+    del gate, up, dh, g, u, dx
+    torch.cuda.empty_cache()
