@@ -141,8 +141,10 @@ __global__ __launch_bounds__(256) void i8_dequant_kernel(const int8_t *__restric
 
 unsigned row_grid(int64_t rows) { return (unsigned)std::min<int64_t>(rows, int64_t(1) << 20); }
 
-// From these sizes on a half matrix is read, or a matrix written, without a place in
-// the caches (as the MXFP4 conversions).
+// From these sizes on a dense matrix is read, or written, without a place in the caches,
+// which then keep the codes: 28672 x 8192 quantised and expanded in turn takes 217 us in
+// float16 and 379 in float32, 242 and 427 with ordinary loads, 241 and 430 with ordinary
+// stores; quantised alone 122 and 210, with ordinary loads 128 and 217.
 constexpr int64_t kNtLoad = (int64_t)64 << 20, kNtStore = (int64_t)256 << 20;
 
 template <MxType T, int WAVES, int ROUNDS>
@@ -151,7 +153,7 @@ void quantize_rows(const void *x, int64_t rows, int64_t cols, int8_t *codes, flo
   const dim3 grid(row_grid((rows + kPer - 1) / kPer)), block(WAVES < 4 ? 256 : WAVES * 64);
   uint2 *const c = reinterpret_cast<uint2 *>(codes);
   const int octets = (int)(cols / 8);
-  if (T != MxType::kF32 && rows * cols * 2 >= kNtLoad)
+  if (rows * cols * (T == MxType::kF32 ? 4 : 2) >= kNtLoad)
     hipLaunchKernelGGL((i8_quantize_rows_kernel<T, WAVES, ROUNDS, true>), grid, block, 0, stream, x, c, scales, octets, rows);
   else
     hipLaunchKernelGGL((i8_quantize_rows_kernel<T, WAVES, ROUNDS, false>), grid, block, 0, stream, x, c, scales, octets, rows);
