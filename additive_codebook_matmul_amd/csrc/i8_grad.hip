@@ -515,7 +515,8 @@ template <MxType T> hipError_t grad_as(const I8Grad &p, const I8Plan &g, void *w
   using namespace i8_grad;  // (in the order of its costs)
   if (g.shape == 0) return launch_shape<T, Large>(A, stream);
   if (g.shape == 1) return launch_shape<T, Half>(A, stream);
-  return launch_shape<T, Small>(A, stream);
+  if (g.shape == 2) return launch_shape<T, Small>(A, stream);
+  return launch_shape<T, Deep>(A, stream);
 }
 
 }  // namespace

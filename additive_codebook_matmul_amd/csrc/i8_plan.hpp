@@ -209,17 +209,19 @@ namespace i8_grad {
 typedef I8GradShape<2, 2, 4, 2, 1, 3> Large;   // 256 columns x 128 tokens
 typedef I8GradShape<2, 1, 4, 2, 1, 2> Half;    // 256 x 64, two workgroups to a CU
 typedef I8GradShape<2, 1, 2, 1, 2, 2> Small;   // 128 x 32, two
+typedef I8GradShape<2, 1, 2, 1, 2, 3> Deep;    // 128 x 32, one, with a step more under way
 
 // Fitted to eight layers from 1 to 2048 tokens, each shape and 1, 2, 4 and 8 splits
 // measured at each, within 5 % at the median; the choice costs 0.3 % on average against
 // the best one.
-// (Each shape with its best splits, terms' launch included, Large to Small: 301 x 4096 x
-// 11008 94, 72 and 95 us, 2048 x 11008 x 4096 348, 374, 486, 333 x 1376 x 4096 30, 27, 22, 1
-// x 28672 x 8192 92, 70, 58. Tiles of 128 x 64, by two or four wavefronts, and 256 x 64 by
-// four would spare 0.1 % of the choice's time.)
-constexpr I8TileCost kCosts[] = {i8_cost_of<Large>(0.07, 1.317, 0.0, 0.0), i8_cost_of<Half>(0.55, 0.841, 0.247, 0.522),
-                                 i8_cost_of<Small>(1.28, 0.736, 0.465, 0.185)};
-constexpr I8Rates kRates = {5.3e6, 0.7e9, 4.8e6, 0.0, 2.3, 512};
+// (Each shape with its best splits, terms' launch included, Large to Deep: 301 x 4096 x
+// 11008 94, 72, 95 and 121 us, 2048 x 11008 x 4096 348, 374, 486, 587, 1 x 28672 x 8192 92,
+// 70, 58, 60, 9 x 11008 x 4096 41, 32, 24, 22. Tiles of 128 x 64, by two or four
+// wavefronts, 256 x 64 by four and 256 x 128 by four would spare 0.1 % of the choice's time
+// at most.)
+constexpr I8TileCost kCosts[] = {i8_cost_of<Large>(1.07, 1.309, 0.0, 0.0), i8_cost_of<Half>(1.42, 0.836, 0.261, 0.514),
+                                 i8_cost_of<Small>(2.12, 0.73, 0.462, 0.189), i8_cost_of<Deep>(2.12, 0.719, 0.122, 0.0)};
+constexpr I8Rates kRates = {5.3e6, 0.7e9, 4.7e6, 0.0, 2.2, 512};
 }  // namespace i8_grad
 
 inline I8Plan i8_grad_plan(int64_t rows, int64_t cols, bool gated, int64_t batch) {

@@ -12,7 +12,7 @@ from additive_codebook_matmul_amd import build
 
 KINDS = ("rows", "skinny", "tiles")
 TILES = ("Large", "Wide", "Middle", "Half", "Small", "Slim", "Least")
-GRAD_TILES = ("Large", "Half", "Small")
+GRAD_TILES = ("Large", "Half", "Small", "Deep")
 
 SOURCE = """
 #include "i8_plan.hpp"
@@ -85,7 +85,7 @@ def shapes(of_gradient):
 
 # stages of K in LDS and shares of K of each tile shape: where a kernel's loop turns
 RING = {"Large": (2, 1), "Wide": (2, 1), "Middle": (3, 1), "Half": (3, 1), "Small": (3, 2), "Slim": (3, 2), "Least": (3, 2)}
-GRAD_RING = {"Large": (3, 1), "Half": (2, 1), "Small": (2, 2)}
+GRAD_RING = {"Large": (3, 1), "Half": (2, 1), "Small": (2, 2), "Deep": (3, 2)}
 
 
 def _loop(steps, plan, ring):

@@ -42,21 +42,25 @@ GATED = [
     (4274, 395, 9776), (207, 8241, 13200),
 ]
 GRADS = [
-    (1, 8, 16), (1, 1, 272), (1, 65, 16), (129, 1, 16), (1, 72, 144), (36, 66, 16), (1, 4240, 16), (33, 70, 176),
-    (1, 8416, 144), (35, 592, 160), (656, 1, 11184), (41, 17032, 16), (4492, 70, 144), (35, 152, 14432),
-    (1433, 1592, 192), (35, 2120, 6256), (175, 1543, 1856), (4417, 421, 800), (4549, 22038, 16), (2743, 2723, 288),
-    (65, 3128, 11472),
+    (1, 8, 16), (1, 1, 272), (1, 65, 16), (66, 1, 16), (1, 66, 144), (68, 1, 272), (33, 77, 16), (1, 6493, 16),
+    (35, 657, 16), (33, 80, 144), (1, 10736, 144), (34, 584, 144), (1, 5208, 6832), (1661, 2636, 16),
+    (4126, 216, 144), (33, 1904, 5584), (1355, 2132, 144), (41, 2568, 5424), (262, 2582, 1168), (2914, 401, 1296),
+    (4236, 25464, 16), (65, 3272, 10912), (3001, 2864, 272),
 ]
 GATED_GRADS = [
-    (1, 1, 16), (1, 1, 144), (34, 1, 16), (34, 1, 144), (1, 2145, 16), (1, 2256, 144), (4214, 1, 144),
-    (66, 1, 11584), (36, 4120, 16), (33, 19032, 144), (1355, 1040, 176), (40, 1062, 6128), (236, 1312, 1344),
-    (2833, 200, 1360), (4106, 13920, 16), (2210, 2223, 272), (70, 1580, 12272),
+    (1, 1, 16), (1, 1, 144), (33, 1, 16), (33, 1, 144), (1, 3224, 16), (4200, 1, 144), (67, 1, 11280),
+    (1, 4528, 176), (34, 272, 160), (34, 17880, 16), (1, 1384, 10912), (2732, 956, 16), (4662, 76, 144),
+    (36, 1288, 3376), (45, 1064, 5408), (1395, 1050, 208), (108, 1296, 3120), (4435, 11376, 16), (3267, 272, 1104),
+    (2766, 1528, 304), (77, 1504, 11152),
 ]
 # and the sizes of Llama-2 layers
 PRODUCTS += [(77, 4096, 11008), (1999, 4096, 11008), (16, 4096, 4096), (1, 8192, 28672)]
 GATED += [(1, 11008, 4096), (8, 11008, 4096), (19, 28672, 8192), (2048, 11008, 4096), (333, 1376, 4096)]
 GRADS += [(301, 4096, 11008), (2048, 11008, 4096)]
-GATED_GRADS += [(100, 131, 33840), (60, 70, 33840), (333, 1376, 4096), (2048, 11008, 4096)]
+GATED_GRADS += [(333, 1376, 4096), (2048, 11008, 4096)]
+# and one tile of tokens for the chip with K whole: many columns
+GRADS += [(91, 968, 39152), (60, 689, 71376), (30, 1037, 37120), (21, 845, 30976)]
+GATED_GRADS += [(113, 282, 98032), (56, 202, 68592), (3, 344, 68656), (24, 1189, 25264)]
 
 
 def _gen(*sizes):
