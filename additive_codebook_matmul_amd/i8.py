@@ -32,7 +32,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._lib import _check, load_library
-from .mx import _HALVES, _call, _check_dense, _output, _record
+from .mx import _HALVES, _call, _check_dense, _output, _record, _refuse_tangent
 
 I8_MAX_DIM = 1 << 21
 I8_MAX_COLS = (1 << 17) - 16
@@ -85,6 +85,7 @@ def _check_packed(codes: torch.Tensor, scales: torch.Tensor) -> Tuple[int, int]:
     if (scales.dtype != torch.float32 or scales.shape != (rows,) or not scales.is_contiguous()
             or scales.device != codes.device):
         raise ValueError("scales must be float32 [rows], contiguous and on the codes' device")
+    _refuse_tangent(scales, "scales")
     if cols < 16 or cols % 16:
         raise ValueError("cols must be a multiple of 16")
     return rows, cols

@@ -94,15 +94,19 @@ def _call(device: torch.device, fn, *args) -> None:
         _check(status)
 
 
+def _refuse_tangent(t: torch.Tensor, what: str) -> None:
+    # (the level is the quick question, where the installed torch answers it)
+    if getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{what} carries a forward-mode tangent, which would be lost")
+
+
 def _check_dense(t: torch.Tensor, what: str, dtypes, shape=None) -> None:
     if t.dtype not in dtypes or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
         names = ", ".join(str(d).replace("torch.", "") for d in dtypes)
         raise ValueError(f"{what} must be a contiguous 2-D tensor on the GPU, of type {names}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
-    # (the level is the quick question, where the installed torch answers it)
-    if getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(t).tangent is not None:
-        raise ValueError(f"{what} carries a forward-mode tangent, which would be lost")
+    _refuse_tangent(t, what)
 
 
 def _check_packed(codes: torch.Tensor, scales: torch.Tensor) -> Tuple[int, int]:

@@ -4,7 +4,8 @@ import pytest
 import torch
 from torch.autograd import forward_ad
 
-from additive_codebook_matmul_amd import (I8Gated, I8Layer, MxLayer, i8_quantize, mx_gemv_batched, mx_quantize)
+from additive_codebook_matmul_amd import (I8Gated, I8Layer, MxLayer, i8_dequant, i8_quantize, mx_gemv_batched,
+                                          mx_quantize)
 from test_gpu_mx import DEV, HALVES
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +44,14 @@ def test_a_tangent_is_refused(name, dtype, recorded):
         got = call(x)                                # a plain tensor passes inside of a level too
     for a, b in zip(want if isinstance(want, (tuple, list)) else [want], got if isinstance(got, (tuple, list)) else [got]):
         assert torch.equal(a, b) and a.requires_grad == b.requires_grad
+
+
+@pytest.mark.parametrize("name", ["gemm_i8", "i8_dequant", "I8Layer"])
+def test_a_tangent_of_scales_is_refused(name):
+    codes, scales = i8_quantize(_dense(40, 64, torch.float16, 1))
+    layer = I8Layer(codes, scales)
+    call = {"gemm_i8": layer.gemm_i8, "i8_dequant": i8_dequant, "I8Layer": I8Layer}[name]
+    with forward_ad.dual_level():
+        call(codes, scales)
+        with pytest.raises(ValueError, match="tangent"):
+            call(codes, forward_ad.make_dual(scales, torch.ones_like(scales)))
